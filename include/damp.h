@@ -75,7 +75,8 @@ typedef enum damp_status {
 /* Gate form ([C2] step 2, "For KDA" remark; [DAMP]). */
 typedef enum damp_decay {
   DAMP_DECAY_SCALAR = 0,  /* GDN: alpha is [B][H] */
-  DAMP_DECAY_PER_KEY = 1  /* KDA: alpha is [B][H][d_k] */
+  DAMP_DECAY_PER_KEY = 1, /* KDA: alpha is [B][H][d_k] */
+  DAMP_DECAY_PER_HEAD = 2 /* linear attention only: alpha is [H], one fixed decay per head */
 } damp_decay;
 
 /* Element type of q, k, v. beta, alpha and the readout are always fp32. */
@@ -486,6 +487,125 @@ damp_status stq_decode_step(stq_state* state, void* dst_pool, const int32_t* slo
                             const void* q, const void* k, const void* v, damp_dtype qkv_dtype,
                             const float* alpha, damp_decay decay, const float* beta, float* out,
                             void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Linear attention and prompts, on an FP32 state pool [num_slots][num_heads][d_k][d_v] (the pool of
+ * fp32_decode_step; damp_state_quantize or stq_state_quantize moves its states into the other
+ * formats). Linear attention with a decay is the update without the delta rule,
+ *   S_t = a_t S_{t-1} + k_t v_t^T,  o_t = S_t^T q_t,
+ * no normaliser and no query scale. The prompt forms take whole runs of tokens per request: the
+ * tokens of request b are rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of q, k, v, alpha, beta and
+ * out. d_k == d_v in {16, 32, 64, 128}.
+ * ------------------------------------------------------------------------------------- */
+
+/* One token per request of linear attention: arguments as fp32_decode_step without beta. alpha is
+ * [B][num_heads] (DAMP_DECAY_SCALAR), [B][num_heads][d_k] (PER_KEY) or [num_heads] (PER_HEAD).
+ * out fp32 [B][num_heads][d_v], 16-byte aligned: the readout of the updated state. */
+damp_status fp32_linear_step(float* pool, int32_t num_slots, int32_t num_heads, int32_t d_k,
+                             int32_t d_v, const int32_t* slot_idx, int32_t B, const void* q,
+                             const void* k, const void* v, damp_dtype qkv_dtype,
+                             const float* alpha, damp_decay decay, float* out, void* stream);
+
+/* Device bytes of workspace that a prefill call of these sizes needs (0: none, or invalid sizes);
+ * delta: 0 for fp32_linear_prefill, 1 for fp32_delta_prefill. Its contents before the call do not
+ * matter and nothing in it is kept for a later call; calls that may overlap need their own. */
+size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t num_heads, int32_t d,
+                                    damp_dtype qkv_dtype, damp_decay decay);
+
+/* Linear attention over B prompts: for each request the readouts of all its tokens and, in its
+ * slot of the pool, its state after the last one.
+ *   slot_idx   dev int32 [B], distinct. A request whose slot is outside [0, num_slots) is skipped.
+ *   cu_seqlens dev int32 [B + 1], ascending from 0, cu_seqlens[B] <= T. Rows of out behind the last
+ *              request are not written. Values are kept inside [0, T] (no access leaves the
+ *              arrays); a list that does not ascend gives unspecified readouts and states.
+ *              DAMP_DEBUG=1 returns DAMP_ERR_SLOT_INDEX for one.
+ *   resume     dev int32 [B] or NULL: nonzero continues from the slot's state (a prompt in parts),
+ *              zero or NULL starts from the zero state without reading the slot
+ *   q, k, v    dev [T][num_heads][d] of qkv_dtype, 16-byte aligned
+ *   alpha      dev fp32 [T][num_heads], [T][num_heads][d] or [num_heads] (by decay), each in [0, 1]
+ *   out        dev [T][num_heads][d] of qkv_dtype (the next layer's input type), 16-byte aligned
+ *   workspace  dev, 256-byte aligned, fp32_prefill_workspace_bytes
+ * A request of no tokens keeps its state. B == 0 or T == 0 is a no-op. bf16 inputs with d in
+ * {64, 128} and a decay per head (SCALAR, PER_HEAD) run chunk by chunk on the matrix cores, with
+ * binary32 states, sums and decays; other forms token by token in binary32.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (d), SLOT_INDEX (debug), HIP. */
+damp_status fp32_linear_prefill(float* pool, int32_t num_slots, int32_t num_heads, int32_t d_k,
+                                int32_t d_v, const int32_t* slot_idx, const int32_t* cu_seqlens,
+                                const int32_t* resume, int32_t B, int32_t T, const void* q,
+                                const void* k, const void* v, damp_dtype qkv_dtype,
+                                const float* alpha, damp_decay decay, void* out, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* The gated delta rule over B prompts, the prompt form of fp32_decode_step: per token
+ *   S' = D_t S, delta = beta (v - S'^T k), S = S' + k delta^T, out = S^T q.
+ *   beta  dev fp32 [T][num_heads]
+ *   decay SCALAR or PER_KEY
+ * Other arguments and errors as fp32_linear_prefill. As there, q and k come normalised. */
+damp_status fp32_delta_prefill(float* pool, int32_t num_slots, int32_t num_heads, int32_t d_k,
+                               int32_t d_v, const int32_t* slot_idx, const int32_t* cu_seqlens,
+                               const int32_t* resume, int32_t B, int32_t T, const void* q,
+                               const void* k, const void* v, damp_dtype qkv_dtype,
+                               const float* alpha, damp_decay decay, const float* beta, void* out,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Paged key-value cache, for the full-attention layers between the recurrent ones: keys and values
+ * in pages, bf16 [num_pages][num_kv_heads][page_size][d] each, d in {64, 128}, page_size a power of
+ * two up to 32,768. Request b's token at position p lies in page block_table[b][p / page_size], row
+ * p mod page_size; its cache slot is page * page_size + row.
+ * ------------------------------------------------------------------------------------- */
+
+/* The tables of one serving step, in one launch: request b has seq_lens[b] tokens with this step, of
+ * which new_lens[b] are this step's (clamped to [0, seq_lens[b]]). Pages that a request's new tokens
+ * need beyond those its earlier tokens fill are taken from free_pages in the order of the requests.
+ *   seq_lens, new_lens dev int32 [B]
+ *   free_pages  dev int32 [num_free]: ids of unused pages
+ *   block_table dev int32 [B][max_blocks]: entries of new pages are written, others left as they are
+ *   slot_map    dev int64 [T]: the cache slot of each new token, requests in order; -1 behind the
+ *               last token, and for a token without a page (free list or table too short, or a
+ *               negative entry of the table)
+ *   positions   dev int32 [T] or NULL: each new token's position in its request, -1 behind the last
+ *   cu_new      dev int32 [B + 1]: running sums of the new tokens (cu_seqlens of the prefill calls)
+ *   used        dev int32 [1]: pages needed; if that is more than num_free, the entries and slots
+ *               that got no page are -1
+ * The new tokens must sum to less than 2^31. At most 8,000 requests (else UNSUPPORTED).
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP. */
+damp_status kv_build_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t B,
+                            const int32_t* free_pages, int32_t num_free, int32_t page_size,
+                            int32_t* block_table, int32_t max_blocks, int64_t* slot_map,
+                            int32_t* positions, int32_t T, int32_t* cu_new, int32_t* used,
+                            void* stream);
+
+/* Stores k, v (dev bf16 [T][num_kv_heads][d], 16-byte aligned) of T tokens at slot_map (dev int64
+ * [T]); a slot outside the cache (such as -1) is skipped, a repeated one races. */
+damp_status kv_append(const void* k, const void* v, const int64_t* slot_map, int32_t T,
+                      int32_t num_kv_heads, int32_t d, void* k_pages, void* v_pages,
+                      int32_t num_pages, int32_t page_size, void* stream);
+
+/* Device bytes of workspace kv_decode_attention needs (0: none). Its contents before the call do
+ * not matter and nothing in it is kept; calls that may overlap need their own. */
+size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t num_kv_heads,
+                                           int32_t d, int32_t max_len);
+
+/* Attention of one new token per request over its cached tokens:
+ *   out = softmax(scale * q K^T) V over positions 0 .. seq_lens[b] - 1,
+ * query head h reading key-value head h / (num_q_heads / num_kv_heads).
+ *   q, out      dev bf16 [B][num_q_heads][d], 16-byte aligned
+ *   block_table dev int32 [B][max_blocks]; tokens of a page id outside [0, num_pages) are left out
+ *   seq_lens    dev int32 [B], the new token included. 0: out is 0.
+ *   max_len     no request is longer than this (in [0, 2^30]; e.g. max_blocks * page_size). Tokens
+ *               past it or past the table are left out.
+ *   k_new, v_new dev bf16 [B][num_kv_heads][d] or both NULL: the new token's key and value, stored
+ *               at position seq_lens[b] - 1 before the attention reads it (NULL: already stored).
+ *               That position's page must be the request's alone; other pages may be shared.
+ * Scores, softmax statistics and sums are binary32; the softmax weights are rounded to bf16 for the
+ * product with V. B == 0 is a no-op. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
+damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages,
+                                const int32_t* block_table, const int32_t* seq_lens, int32_t B,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t d,
+                                int32_t num_pages, int32_t page_size, int32_t max_blocks,
+                                int32_t max_len, float scale, const void* k_new, const void* v_new,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Message for the last non-OK status returned on the calling thread ("" if none). The string
  * is owned by the library and valid until the thread's next call. (Library infrastructure: no

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdamp.so")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("damp_api.hip", "step_kernels.hip", "window_kernels.hip", "calib_kernels.hip",
-            "stq_kernels.hip", "order_kernels.hip")]
+            "stq_kernels.hip", "order_kernels.hip", "linear_kernels.hip", "prompt_kernels.hip",
+            "kv_kernels.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -42,14 +43,14 @@ FLAGS = [
 ]
 
 
-# The host layer validates caller data (NaN included), so it keeps IEEE NaN semantics; it holds
-# no device arithmetic.
-HOST_ONLY = {"damp_api.hip"}
+# The host layer validates caller data (NaN included), and the attention, linear-attention and
+# prompt kernels pass NaN and infinities of the caller's through, so these keep IEEE NaN semantics.
+IEEE_NANS = {"damp_api.hip", "linear_kernels.hip", "prompt_kernels.hip", "kv_kernels.hip"}
 
 
 def _compile(src: str, obj: str, extra: list[str]) -> tuple[int, str]:
     flags = [f for f in FLAGS if f != "-shared"]
-    if os.path.basename(src) in HOST_ONLY:
+    if os.path.basename(src) in IEEE_NANS:
         flags = [f for f in flags if f != "-fno-honor-nans"]
     res = subprocess.run([HIPCC, *flags, *extra, "-c", src, "-o", obj], capture_output=True, text=True)
     return res.returncode, res.stdout + res.stderr

@@ -395,6 +395,103 @@ damp_status scratch_for(hipStream_t stream, int32_t** out) {
   return DAMP_OK;
 }
 
+// ---- linear attention, prompts and the paged cache --------------------------------------------
+damp_status check_fp32_pool(const float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v) {
+  if (num_slots <= 0 || H <= 0)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_slots (%d) and num_heads (%d) must be positive", num_slots, H);
+  if (d_k != d_v || !supported_d(d_k))
+    return fail(DAMP_ERR_UNSUPPORTED, "d_k = %d, d_v = %d: supported sizes are d_k == d_v in "
+                "{16, 32, 64, 128}", d_k, d_v);
+  if (!pool) return fail(DAMP_ERR_INVALID_ARGUMENT, "pool is NULL");
+  if (!aligned(pool, 16)) return fail(DAMP_ERR_INVALID_ARGUMENT, "pool must be 16-byte aligned");
+  return DAMP_OK;
+}
+
+// DAMP_DEBUG=1: synchronously check that cu_seqlens ascends from 0 and ends within the tokens.
+damp_status debug_check_seqlens(const int32_t* cu, int32_t B, int32_t T, hipStream_t stream) {
+  if (!debug_mode()) return DAMP_OK;
+  std::vector<int32_t> h(static_cast<size_t>(B) + 1);
+  hipError_t e = hipMemcpyAsync(h.data(), cu, sizeof(int32_t) * h.size(), hipMemcpyDeviceToHost, stream);
+  if (e == hipSuccess) e = hipStreamSynchronize(stream);
+  if (e != hipSuccess) return fail(DAMP_ERR_HIP, "reading cu_seqlens for DAMP_DEBUG: %s", hipGetErrorString(e));
+  for (int32_t b = 0; b <= B; ++b)
+    if (h[static_cast<size_t>(b)] < (b ? h[static_cast<size_t>(b) - 1] : 0) || h[static_cast<size_t>(b)] > T ||
+        (b == 0 && h[0] != 0))
+      return fail(DAMP_ERR_SLOT_INDEX, "cu_seqlens[%d] = %d: must start at 0, ascend and end within the %d tokens",
+                  b, h[static_cast<size_t>(b)], T);
+  return DAMP_OK;
+}
+
+damp_status run_prefill(bool delta, float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v,
+                        const int32_t* slot_idx, const int32_t* cu, const int32_t* resume, int32_t B,
+                        int32_t T, const void* q, const void* k, const void* v, damp_dtype dt,
+                        const float* alpha, damp_decay decay, const float* beta, void* out,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || T < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d) and T (%d) must be >= 0", B, T);
+  if (dt != DAMP_F32 && dt != DAMP_BF16)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "qkv_dtype %d is not DAMP_F32 or DAMP_BF16", int(dt));
+  const bool ok_decay = decay == DAMP_DECAY_SCALAR || decay == DAMP_DECAY_PER_KEY ||
+                        (!delta && decay == DAMP_DECAY_PER_HEAD);
+  if (!ok_decay) return fail(DAMP_ERR_INVALID_ARGUMENT, "decay %d is not one this call takes", int(decay));
+  damp_status st = check_fp32_pool(pool, num_slots, H, d_k, d_v);
+  if (st != DAMP_OK) return st;
+  if (B == 0 || T == 0) return ok();
+  if (!slot_idx || !cu || !q || !k || !v || !alpha || !out || (delta && !beta))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among slot_idx/cu_seqlens/q/k/v/alpha/beta/out");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "q, k, v and out must be 16-byte aligned");
+  if (!aligned(slot_idx, 4) || !aligned(cu, 4) || !aligned(resume, 4) || !aligned(alpha, 4) || !aligned(beta, 4))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned input pointer (need natural alignment)");
+  if ((static_cast<int64_t>(T) / 64 + B) * H > 0x7fffffffLL / 8)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "T = %d tokens of %d requests with %d heads exceed the grid limit", T, B, H);
+  const int64_t need = damp::prefill_ws_bytes(delta, d_k, decay, dt == DAMP_BF16, B, T, H);
+  if (need > 0 && (!workspace || !aligned(workspace, kBlockAlign) || workspace_bytes < static_cast<size_t>(need)))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned and hold %lld bytes (%zu given)",
+                static_cast<long long>(need), workspace ? workspace_bytes : size_t(0));
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  st = debug_check_slots(slot_idx, B, num_slots, s);
+  if (st != DAMP_OK) return st;
+  st = debug_check_seqlens(cu, B, T, s);
+  if (st != DAMP_OK) return st;
+  damp::PromptArgs a{};
+  a.pool = pool;
+  a.num_slots = num_slots;
+  a.H = H;
+  a.slot_idx = slot_idx;
+  a.cu = cu;
+  a.resume = resume;
+  a.B = B;
+  a.T = T;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.out = out;
+  a.ws = static_cast<uint8_t*>(workspace);
+  return launched(damp::launch_prefill(delta, d_k, decay, dt == DAMP_BF16, a, s),
+                  delta ? "delta prefill" : "linear prefill");
+}
+
+// log2 of a page size, or -1 if it is not a power of two in [1, 32768].
+int page_log2(int32_t page_size) {
+  for (int i = 0; i <= 15; ++i)
+    if (page_size == (1 << i)) return i;
+  return -1;
+}
+
+damp_status check_cache(int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_size) {
+  if (Hkv <= 0 || num_pages <= 0)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_kv_heads (%d) and num_pages (%d) must be positive", Hkv, num_pages);
+  if (d != 64 && d != 128)
+    return fail(DAMP_ERR_UNSUPPORTED, "d = %d: the paged cache supports d in {64, 128}", d);
+  if (page_log2(page_size) < 0)
+    return fail(DAMP_ERR_UNSUPPORTED, "page_size %d is not a power of two in [1, 32768]", page_size);
+  return DAMP_OK;
+}
+
+constexpr double kLog2E = 1.4426950408889634;
+
 }  // namespace
 
 extern "C" {
@@ -1039,4 +1136,172 @@ damp_status stq_decode_step(stq_state* s, void* dst_pool, const int32_t* slot_id
   return launched(damp::launch_stq(0, s->d, decay == DAMP_DECAY_PER_KEY, dt == DAMP_BF16, a, hs), "stq step");
 }
 
+// ---- linear attention, prompts and the paged cache --------------------------------------------
+damp_status fp32_linear_step(float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v,
+                             const int32_t* slot_idx, int32_t B, const void* q, const void* k,
+                             const void* v, damp_dtype dt, const float* alpha, damp_decay decay,
+                             float* out, void* stream) {
+  damp_status st = check_fp32_pool(pool, num_slots, H, d_k, d_v);
+  if (st != DAMP_OK) return st;
+  // (beta is not used: alpha stands in for the pointer check)
+  st = check_step_args(B, H, d_k, slot_idx, q, k, v, dt, alpha,
+                       decay == DAMP_DECAY_PER_HEAD ? DAMP_DECAY_SCALAR : decay, alpha, out);
+  if (st != DAMP_OK) return st;
+  if (B == 0) return ok();
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  st = debug_check_slots(slot_idx, B, num_slots, s);
+  if (st != DAMP_OK) return st;
+  damp::StepArgs a{};
+  a.st.hbase = reinterpret_cast<uint8_t*>(pool);
+  a.st.hstride = static_cast<int64_t>(d_k) * d_k * 4;
+  a.st.num_slots = num_slots;
+  a.slot_idx = slot_idx;
+  a.B = B;
+  a.H = H;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.alpha = alpha;
+  a.out = out;
+  return launched(damp::launch_linear_step(d_k, decay, dt == DAMP_BF16, a, s), "linear step");
+}
+
+size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t H, int32_t d,
+                                    damp_dtype dt, damp_decay decay) {
+  if (B <= 0 || T <= 0 || H <= 0 || !supported_d(d)) return 0;
+  return static_cast<size_t>(damp::prefill_ws_bytes(delta != 0, d, decay, dt == DAMP_BF16, B, T, H));
+}
+
+damp_status fp32_linear_prefill(float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v,
+                                const int32_t* slot_idx, const int32_t* cu_seqlens, const int32_t* resume,
+                                int32_t B, int32_t T, const void* q, const void* k, const void* v,
+                                damp_dtype dt, const float* alpha, damp_decay decay, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return run_prefill(false, pool, num_slots, H, d_k, d_v, slot_idx, cu_seqlens, resume, B, T, q, k, v,
+                     dt, alpha, decay, nullptr, out, workspace, workspace_bytes, stream);
+}
+
+damp_status fp32_delta_prefill(float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v,
+                               const int32_t* slot_idx, const int32_t* cu_seqlens, const int32_t* resume,
+                               int32_t B, int32_t T, const void* q, const void* k, const void* v,
+                               damp_dtype dt, const float* alpha, damp_decay decay, const float* beta,
+                               void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_prefill(true, pool, num_slots, H, d_k, d_v, slot_idx, cu_seqlens, resume, B, T, q, k, v,
+                     dt, alpha, decay, beta, out, workspace, workspace_bytes, stream);
+}
+
+damp_status kv_build_tables(const int32_t* seq_lens, const int32_t* new_lens, int32_t B,
+                            const int32_t* free_pages, int32_t num_free, int32_t page_size,
+                            int32_t* block_table, int32_t max_blocks, int64_t* slot_map,
+                            int32_t* positions, int32_t T, int32_t* cu_new, int32_t* used, void* stream) {
+  if (B < 0 || T < 0 || num_free < 0 || max_blocks < 0)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d), T (%d), num_free (%d) and max_blocks (%d) must be >= 0", B,
+                T, num_free, max_blocks);
+  if (page_log2(page_size) < 0)
+    return fail(DAMP_ERR_UNSUPPORTED, "page_size %d is not a power of two in [1, 32768]", page_size);
+  if (B > damp::kv_tables_max_requests())
+    return fail(DAMP_ERR_UNSUPPORTED, "B = %d: at most %d requests", B, damp::kv_tables_max_requests());
+  if (!cu_new || !used || (B > 0 && (!seq_lens || !new_lens)) || (B > 0 && max_blocks > 0 && !block_table) ||
+      (num_free > 0 && !free_pages) || (T > 0 && !slot_map))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among seq_lens/new_lens/free_pages/block_table/slot_map/cu_new/used");
+  if (!aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) ||
+      !aligned(slot_map, 8) || !aligned(positions, 4) || !aligned(cu_new, 4) || !aligned(used, 4))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned pointer (need natural alignment)");
+  damp::TableArgs a{};
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.table = block_table;
+  a.slot_map = slot_map;
+  a.positions = positions;
+  a.cu_new = cu_new;
+  a.used = used;
+  a.B = B;
+  a.T = T;
+  a.num_free = num_free;
+  a.max_blocks = max_blocks;
+  a.page_log2 = page_log2(page_size);
+  return launched(damp::launch_kv_tables(a, static_cast<hipStream_t>(stream)), "block tables");
+}
+
+damp_status kv_append(const void* k, const void* v, const int64_t* slot_map, int32_t T, int32_t num_kv_heads,
+                      int32_t d, void* k_pages, void* v_pages, int32_t num_pages, int32_t page_size,
+                      void* stream) {
+  if (T < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "T (%d) must be >= 0", T);
+  damp_status st = check_cache(num_kv_heads, d, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (T == 0) return ok();
+  if (!k || !v || !slot_map || !k_pages || !v_pages)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among k/v/slot_map/k_pages/v_pages");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(slot_map, 8))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "k, v and the pages must be 16-byte, slot_map 8-byte aligned");
+  damp::AppendArgs a{};
+  a.k = static_cast<const uint8_t*>(k);
+  a.v = static_cast<const uint8_t*>(v);
+  a.slot_map = slot_map;
+  a.k_pages = static_cast<uint8_t*>(k_pages);
+  a.v_pages = static_cast<uint8_t*>(v_pages);
+  a.page_log2 = page_log2(page_size);
+  a.num_slots = static_cast<int64_t>(num_pages) << a.page_log2;
+  a.T = T;
+  a.Hkv = num_kv_heads;
+  a.d = d;
+  return launched(damp::launch_kv_append(a, static_cast<hipStream_t>(stream)), "cache append");
+}
+
+size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t num_kv_heads, int32_t d,
+                                           int32_t max_len) {
+  if (B <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || (d != 64 && d != 128) ||
+      max_len < 0 || max_len > (1 << 30))
+    return 0;
+  return damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);
+}
+
+damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages, const int32_t* block_table,
+                                const int32_t* seq_lens, int32_t B, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t d, int32_t num_pages, int32_t page_size, int32_t max_blocks,
+                                int32_t max_len, float scale, const void* k_new, const void* v_new, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || max_blocks < 0 || max_len < 0 || max_len > (1 << 30))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d) and max_blocks (%d) must be >= 0, max_len (%d) in [0, 2^30]", B, max_blocks, max_len);
+  damp_status st = check_cache(num_kv_heads, d, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (num_q_heads <= 0 || num_q_heads % num_kv_heads)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)", num_q_heads, num_kv_heads);
+  if (B == 0) return ok();
+  if (!q || !k_pages || !v_pages || !seq_lens || !out || (max_blocks > 0 && !block_table))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among q/k_pages/v_pages/block_table/seq_lens/out");
+  if (!k_new != !v_new) return fail(DAMP_ERR_INVALID_ARGUMENT, "k_new and v_new must be given together");
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_new, 16) ||
+      !aligned(v_new, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages, k_new, v_new and out must be 16-byte, block_table and seq_lens 4-byte aligned");
+  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > 0x7fffffffLL ||
+      static_cast<int64_t>(B) * num_q_heads > 0x7fffffffLL)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_len = %d exceeds the grid limit", B, max_len);
+  const size_t need = damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned and hold %zu bytes (%zu given)", need,
+                workspace ? workspace_bytes : size_t(0));
+  damp::AttnArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k_pages = static_cast<uint8_t*>(k_pages);
+  a.v_pages = static_cast<uint8_t*>(v_pages);
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.k_new = static_cast<const uint8_t*>(k_new);
+  a.v_new = static_cast<const uint8_t*>(v_new);
+  a.out = static_cast<uint8_t*>(out);
+  a.ws = static_cast<float*>(workspace);
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2E);
+  a.B = B;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.page_log2 = page_log2(page_size);
+  a.max_len = max_len;
+  return launched(damp::launch_kv_attention(d, a, static_cast<hipStream_t>(stream)), "decode attention");
+}
+
 }  // extern "C"
+

@@ -104,6 +104,79 @@ struct StqArgs {
 // mode 0 = decode step, 1 = pack, 2 = unpack; d is 64 or 128.
 hipError_t launch_stq(int mode, int d, int per_key, int bf16, const StqArgs& a, hipStream_t s);
 
+// Linear attention and the prompt forms, on an fp32 state pool [num_slots][H][d][d]
+// (linear_kernels.hip, prompt_kernels.hip).
+enum Decay : int { DECAY_SCALAR = 0, DECAY_KEY = 1, DECAY_HEAD = 2 };  // alpha [.][H], [.][H][d], [H]
+
+struct PromptArgs {
+  float* pool;
+  int32_t num_slots;        // a request whose slot index is outside [0, num_slots) is skipped
+  int32_t H;
+  const int32_t* slot_idx;  // [B]
+  const int32_t* cu;        // [B + 1]: request b holds the tokens cu[b] .. cu[b + 1] - 1
+  const int32_t* resume;    // [B] or nullptr: nonzero = start from the slot's state, else from zero
+  int32_t B;
+  int32_t T;                // token rows of q, k, v, alpha, beta, out
+  const void* q;            // [T][H][d], fp32 or bf16
+  const void* k;
+  const void* v;
+  const float* alpha;       // [T][H], [T][H][d] or [H]
+  const float* beta;        // [T][H] (delta rule)
+  void* out;                // [T][H][d], the type of q
+  uint8_t* ws;              // the chunked forms' workspace
+};
+
+hipError_t launch_linear_step(int d, int decay, int bf16, const StepArgs& a, hipStream_t s);
+// Chooses between the chunked and the token-by-token form; ws_bytes is what that choice needs.
+int64_t prefill_ws_bytes(bool delta, int d, int decay, int bf16, int32_t B, int32_t T, int32_t H);
+hipError_t launch_prefill(bool delta, int d, int decay, int bf16, const PromptArgs& a, hipStream_t s);
+hipError_t launch_prompt_token(int d, bool delta, int decay, int bf16, const PromptArgs& a, hipStream_t s);
+
+// Paged key-value cache (kv_kernels.hip): pages [num_pages][Hkv][page][d] bf16, page = 1 << page_log2.
+struct TableArgs {
+  const int32_t* seq_lens;   // [B] tokens of each request after this call's
+  const int32_t* new_lens;   // [B] of which this call's
+  const int32_t* free_pages; // [num_free]
+  int32_t* table;            // [B][max_blocks]
+  int64_t* slot_map;         // [T]
+  int32_t* positions;        // [T] or nullptr
+  int32_t* cu_new;           // [B + 1]
+  int32_t* used;             // [1]
+  int32_t B, T, num_free, max_blocks, page_log2;
+};
+
+struct AppendArgs {
+  const uint8_t* k;          // [T][Hkv][d] bf16
+  const uint8_t* v;
+  const int64_t* slot_map;   // [T]
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  int64_t num_slots;         // num_pages << page_log2: a slot outside [0, num_slots) is skipped
+  int32_t T, Hkv, d, page_log2;
+};
+
+struct AttnArgs {
+  const uint8_t* q;          // [B][Hq][d] bf16
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  const int32_t* table;      // [B][max_blocks]
+  const int32_t* seq_lens;   // [B]
+  const uint8_t* k_new;      // [B][Hkv][d] bf16 or nullptr
+  const uint8_t* v_new;
+  uint8_t* out;              // [B][Hq][d] bf16
+  float* ws;                 // partial readouts, then {maximum, sum} pairs
+  float scale_log2;          // scale * log2(e)
+  int32_t B, Hq, Hkv, num_pages, max_blocks, page_log2;
+  int32_t max_len;           // no request is read past this many tokens
+};
+
+int kv_tables_max_requests();
+hipError_t launch_kv_tables(const TableArgs& a, hipStream_t s);
+hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
+size_t kv_attention_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len);
+int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len);
+hipError_t launch_kv_attention(int d, const AttnArgs& a, hipStream_t s);
+
 // Calibration (calib_kernels.hip). Sizes are validated by the caller: d in {16, 32, 64, 128},
 // H * d <= alloc_max_rows(), H * (r_max / g) <= alloc_max_groups(), R % g == 0.
 hipError_t launch_risk_scores(int d, const float* S, int32_t n, int32_t H, const float* abar,

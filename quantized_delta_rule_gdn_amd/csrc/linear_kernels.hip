@@ -1,0 +1,204 @@
+// linear_kernels.hip -- gfx950 kernels of linear attention with a decay (S <- a S + k v^T,
+// o = S^T q) on an fp32 state pool: the single-token step, and the token-by-token prompt form
+// that also takes the gated delta rule (e = beta (v - S'^T k) in place of v). The chunked prompt
+// form is in prompt_kernels.hip.
+#include "prompt_common.h"
+
+namespace damp {
+namespace {
+
+// ---- the single-token step -----------------------------------------------------------------
+// One workgroup per unit; the state crosses HBM once in and once out, and nothing else of its
+// size moves, so the kernel is bound by that stream (2 * 4 d^2 bytes per unit against 5 d^2
+// flops). A row of the state is D / 4 lanes of 16 bytes; the whole unit is in flight at once
+// (64 fp32 values per lane at d = 128). The readout is taken from the updated row while it is in
+// registers; the partial column sums of the row groups meet in LDS, added in a fixed order.
+template <int D>
+struct LinGeo {
+  static constexpr int LPR = D / 4;                         // lanes per row
+  static constexpr int NT = D >= 64 ? 256 : 64;             // threads per workgroup
+  static constexpr int RPS = NT / LPR;                      // rows per row step
+  static constexpr int RPL = D / RPS;                       // rows per lane
+  static_assert(RPL >= 1 && RPL * RPS == D, "unsupported d");
+};
+
+template <int D, int DECAY, int BF16>
+__global__ __launch_bounds__(LinGeo<D>::NT) void linear_step_kernel(const StepArgs a) {
+  using G = LinGeo<D>;
+  __shared__ float sk[D], sq[D], sa[D];
+  __shared__ float4 red[G::RPS][G::LPR];
+  const int tid = __builtin_amdgcn_workitem_id_x();
+  const int bh = __builtin_amdgcn_workgroup_id_x();
+  const int b = bh / a.H, head = bh - b * a.H;
+  const int64_t slot = a.slot_idx[b];
+  if (!slot_in_pool(slot, a.st.num_slots)) return;
+  const int rg = tid / G::LPR, cg = tid % G::LPR;
+  using f4 = __attribute__((ext_vector_type(4))) float;
+  f4* base = reinterpret_cast<f4*>(a.st.hbase + (slot * a.H + head) * a.st.hstride) + rg * G::LPR + cg;
+  f4 S[G::RPL];
+#pragma unroll
+  for (int t = 0; t < G::RPL; ++t) S[t] = __builtin_nontemporal_load(base + t * G::RPS * G::LPR);
+  const int64_t at = int64_t(bh) * D;
+  for (int i = tid; i < D; i += G::NT) {
+    sk[i] = load_in<BF16>(a.k, at + i);
+    sq[i] = load_in<BF16>(a.q, at + i);
+    if constexpr (DECAY == DECAY_KEY) sa[i] = a.alpha[at + i];
+  }
+  float v[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) v[c] = load_in<BF16>(a.v, at + cg * 4 + c);
+  const float decay = DECAY == DECAY_KEY ? 0.0f : a.alpha[DECAY == DECAY_HEAD ? head : bh];
+  __syncthreads();
+  float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int t = 0; t < G::RPL; ++t) {
+    const int i = t * G::RPS + rg;
+    const float k = sk[i], q = sq[i], al = DECAY == DECAY_KEY ? sa[i] : decay;
+    f4 x = S[t];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      x[c] = fmaf(k, v[c], al * S[t][c]);
+      p[c] = fmaf(q, x[c], p[c]);
+    }
+    __builtin_nontemporal_store(x, base + t * G::RPS * G::LPR);
+  }
+  red[rg][cg] = make_float4(p[0], p[1], p[2], p[3]);
+  __syncthreads();
+  if (tid < D) {
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < G::RPS; ++r) s += reinterpret_cast<const float*>(red[r])[tid];
+    a.out[at + tid] = s;
+  }
+}
+
+// ---- prompts, token by token -----------------------------------------------------------------
+// One wave per (request, head, 16 value columns): column j of the state only needs column j of v,
+// so the waves are independent and the state stays in registers for the whole prompt (D / 4 rows
+// of one column per lane; the 4 row groups of a wave add up by cross-row lane swaps). Every
+// operation is binary32, in token order. It serves what the chunked form is not built for: fp32
+// inputs, a decay per key channel, d below 64. It is bound by the latency of the token chain:
+// each token's instructions depend on the last's.
+constexpr int kTokBlock = 16;   // tokens staged in LDS at a time
+
+template <int D, bool DELTA, int DECAY, int BF16>
+__global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
+  constexpr int RPL = D / 4;
+  __shared__ __align__(16) float sk[kTokBlock][D], sq[kTokBlock][D];
+  __shared__ __align__(16) float sa[DECAY == DECAY_KEY ? kTokBlock : 1][DECAY == DECAY_KEY ? D : 4];
+  __shared__ float sg[kTokBlock], sb[kTokBlock], sv[kTokBlock][16];
+  const int lane = __builtin_amdgcn_workitem_id_x();
+  const int unit = __builtin_amdgcn_workgroup_id_x() / (D / 16), c0 = (__builtin_amdgcn_workgroup_id_x() % (D / 16)) * 16;
+  const int b = unit / a.H, head = unit - b * a.H;
+  const int64_t slot = a.slot_idx[b];
+  if (!slot_in_pool(slot, a.num_slots)) return;
+  const Span sp = span_of(a, b);
+  if (sp.end <= sp.begin) return;
+  const int rg = lane >> 4, c = lane & 15;
+  float* pool = a.pool + ((slot * a.H + head) * D + rg * RPL) * int64_t(D) + c0 + c;
+  float S[RPL];
+  const bool resume = a.resume && a.resume[b] != 0;
+#pragma unroll
+  for (int i = 0; i < RPL; ++i) S[i] = resume ? pool[i * D] : 0.0f;
+
+  for (int t0 = sp.begin; t0 < sp.end; t0 += kTokBlock) {
+    const int n = min(kTokBlock, sp.end - t0);
+    __syncthreads();
+    for (int x = lane; x < n * D; x += 64) {
+      const int t = x / D, i = x % D;
+      const int64_t at = (int64_t(t0 + t) * a.H + head) * D + i;
+      sk[t][i] = load_in<BF16>(a.k, at);
+      sq[t][i] = load_in<BF16>(a.q, at);
+      if constexpr (DECAY == DECAY_KEY) sa[t][i] = a.alpha[at];
+    }
+    for (int x = lane; x < n * 16; x += 64)
+      sv[x >> 4][x & 15] = load_in<BF16>(a.v, (int64_t(t0 + (x >> 4)) * a.H + head) * D + c0 + (x & 15));
+    if (lane < n) {
+      const int64_t at = int64_t(t0 + lane) * a.H + head;
+      if constexpr (DECAY != DECAY_KEY) sg[lane] = a.alpha[DECAY == DECAY_HEAD ? head : at];
+      if constexpr (DELTA) sb[lane] = a.beta[at];
+    }
+    __syncthreads();
+    for (int t = 0; t < n; ++t) {
+      float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (DECAY == DECAY_KEY) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) S[i] *= sa[t][rg * RPL + i];
+      } else {
+        const float g = sg[t];
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) S[i] *= g;
+      }
+      float e = sv[t][c];
+      if constexpr (DELTA) {
+#pragma unroll
+        for (int i = 0; i < RPL; ++i) u[i & 3] = fmaf(sk[t][rg * RPL + i], S[i], u[i & 3]);
+        e = sb[t] * (e - sum_row_slots((u[0] + u[1]) + (u[2] + u[3])));
+      }
+#pragma unroll
+      for (int i = 0; i < RPL; ++i) {
+        S[i] = fmaf(sk[t][rg * RPL + i], e, S[i]);
+        p[i & 3] = fmaf(sq[t][rg * RPL + i], S[i], p[i & 3]);
+      }
+      const float o = sum_row_slots((p[0] + p[1]) + (p[2] + p[3]));
+      if (rg == 0) {
+        const int64_t at = (int64_t(t0 + t) * a.H + head) * D + c0 + c;
+        if constexpr (BF16) reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(o);
+        else reinterpret_cast<float*>(a.out)[at] = o;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RPL; ++i) pool[i * D] = S[i];
+}
+
+template <int D>
+hipError_t linear_step_d(int decay, int bf16, const StepArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H)), block(LinGeo<D>::NT);
+  with_decay(decay, [&]<int DECAY>() {
+    if (bf16) hipLaunchKernelGGL((linear_step_kernel<D, DECAY, 1>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((linear_step_kernel<D, DECAY, 0>), grid, block, 0, s, a);
+  });
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t prompt_token_d(bool delta, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H) * (D / 16));
+  with_decay(decay, [&]<int DECAY>() {
+    if (delta) {
+      if constexpr (DECAY != DECAY_HEAD) {   // the delta rule takes no fixed decays
+        if (bf16) hipLaunchKernelGGL((prompt_token_kernel<D, true, DECAY, 1>), grid, dim3(64), 0, s, a);
+        else hipLaunchKernelGGL((prompt_token_kernel<D, true, DECAY, 0>), grid, dim3(64), 0, s, a);
+      }
+    } else {
+      if (bf16) hipLaunchKernelGGL((prompt_token_kernel<D, false, DECAY, 1>), grid, dim3(64), 0, s, a);
+      else hipLaunchKernelGGL((prompt_token_kernel<D, false, DECAY, 0>), grid, dim3(64), 0, s, a);
+    }
+  });
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linear_step(int d, int decay, int bf16, const StepArgs& a, hipStream_t s) {
+  switch (d) {
+    case 16: return linear_step_d<16>(decay, bf16, a, s);
+    case 32: return linear_step_d<32>(decay, bf16, a, s);
+    case 64: return linear_step_d<64>(decay, bf16, a, s);
+    case 128: return linear_step_d<128>(decay, bf16, a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_prompt_token(int d, bool delta, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
+  switch (d) {
+    case 16: return prompt_token_d<16>(delta, decay, bf16, a, s);
+    case 32: return prompt_token_d<32>(delta, decay, bf16, a, s);
+    case 64: return prompt_token_d<64>(delta, decay, bf16, a, s);
+    case 128: return prompt_token_d<128>(delta, decay, bf16, a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace damp

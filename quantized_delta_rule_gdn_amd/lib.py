@@ -24,6 +24,7 @@ DAMP_ERR_HIP = -5
 
 DAMP_DECAY_SCALAR = 0
 DAMP_DECAY_PER_KEY = 1
+DAMP_DECAY_PER_HEAD = 2  # linear attention only
 DAMP_F32 = 0
 DAMP_BF16 = 1
 SORTED_MAX_B = 65536  # DAMP_SORTED_MAX_B: the library-held order buffer of damp_decode_step_sorted
@@ -38,7 +39,9 @@ EXPORTS = (
     "damp_window_flush", "stq_state_bytes", "stq_state_alloc", "stq_state_free",
     "stq_state_head_info", "stq_state_quantize", "stq_state_dequantize", "stq_decode_step",
     "damp_batch_order", "damp_decode_step_ordered", "damp_decode_step_fused_ordered",
-    "damp_window_step_ordered", "damp_decode_step_sorted",
+    "damp_window_step_ordered", "damp_decode_step_sorted", "fp32_linear_step",
+    "fp32_prefill_workspace_bytes", "fp32_linear_prefill", "fp32_delta_prefill", "kv_build_tables",
+    "kv_append", "kv_decode_attention_workspace_bytes", "kv_decode_attention",
 )
 
 
@@ -115,6 +118,18 @@ def load() -> ctypes.CDLL:
                                       ctypes.c_int, P, P, P], ctypes.c_int),
         "damp_decode_step_sorted": ([P, P, I32, P, P, P, ctypes.c_int, P, ctypes.c_int, P, P, P],
                                     ctypes.c_int),
+        "fp32_linear_step": ([P, I32, I32, I32, I32, P, I32, P, P, P, ctypes.c_int, P, ctypes.c_int,
+                              P, P], ctypes.c_int),
+        "fp32_prefill_workspace_bytes": ([I32, I32, I32, I32, I32, ctypes.c_int, ctypes.c_int], SZ),
+        "fp32_linear_prefill": ([P, I32, I32, I32, I32, P, P, P, I32, I32, P, P, P, ctypes.c_int, P,
+                                 ctypes.c_int, P, P, SZ, P], ctypes.c_int),
+        "fp32_delta_prefill": ([P, I32, I32, I32, I32, P, P, P, I32, I32, P, P, P, ctypes.c_int, P,
+                                ctypes.c_int, P, P, P, SZ, P], ctypes.c_int),
+        "kv_build_tables": ([P, P, I32, P, I32, I32, P, I32, P, P, I32, P, P, P], ctypes.c_int),
+        "kv_append": ([P, P, P, I32, I32, I32, P, P, I32, I32, P], ctypes.c_int),
+        "kv_decode_attention_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+        "kv_decode_attention": ([P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32,
+                                 ctypes.c_float, P, P, P, P, SZ, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -585,3 +600,228 @@ class StqState:
         _check(load().stq_decode_step(self._h, _ptr(dst) if dst is not None else None, _ptr(slot_idx),
                                       B, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), decay,
                                       _ptr(beta), _ptr(out), _stream(stream)))
+
+
+# ------------------------------------------------------------------------------------------
+# linear attention and prompts
+# ------------------------------------------------------------------------------------------
+def _on(device, stream):
+    """A context in which ``device`` is current and ``stream`` (or that device's current stream)
+    runs the call: workspaces allocated inside belong to that stream."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(device)
+
+
+def _fp32_pool(pool, dev):
+    torch = _torch()
+    if not isinstance(pool, torch.Tensor) or pool.dim() != 4:
+        raise ValueError("pool must be a tensor [num_slots, H, d, d]")
+    S_, H, d, d2 = pool.shape
+    _need(pool, "pool", torch.float32, (S_, H, d, d2), dev)
+    if d != d2:
+        raise ValueError("pool must be square per head")
+    return S_, H, d
+
+
+def _dtype(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.bfloat16:
+        return DAMP_BF16
+    if t.dtype == torch.float32:
+        return DAMP_F32
+    raise TypeError(f"{name} dtype {t.dtype} is not float32 or bfloat16")
+
+
+def _decay(alpha, n, H, d, dev, fixed):
+    """alpha [n, H], [n, H, d] or (where ``fixed``) [H]."""
+    torch = _torch()
+    if not isinstance(alpha, torch.Tensor):
+        raise TypeError("alpha must be a torch.Tensor")
+    if alpha.dim() == 3:
+        _need(alpha, "alpha", torch.float32, (n, H, d), dev)
+        return DAMP_DECAY_PER_KEY
+    if fixed and alpha.dim() == 1:
+        _need(alpha, "alpha", torch.float32, (H,), dev)
+        return DAMP_DECAY_PER_HEAD
+    _need(alpha, "alpha", torch.float32, (n, H), dev)
+    return DAMP_DECAY_SCALAR
+
+
+def _workspace(workspace, nbytes, dev):
+    torch = _torch()
+    if nbytes == 0:
+        return 0, 0
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    if workspace.numel() < nbytes:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, {nbytes} needed")
+    return _ptr(workspace), workspace.numel()
+
+
+def fp32_linear_step(pool, slot_idx, q, k, v, alpha, out, stream=None) -> None:
+    """One token per request of linear attention on an fp32 state pool [num_slots, H, d, d]:
+    S <- alpha S + k v^T, out = S^T q. q, k, v bf16 or fp32 [B, H, d]; alpha fp32 [B, H],
+    [B, H, d] (per key channel) or [H] (fixed per head); out fp32 [B, H, d]."""
+    torch = _torch()
+    _need(slot_idx, "slot_idx", torch.int32, (slot_idx.numel(),))
+    B, dev = slot_idx.shape[0], slot_idx.device
+    S_, H, d = _fp32_pool(pool, dev)
+    dt = _dtype(q, "q")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, q.dtype, (B, H, d), dev)
+    decay = _decay(alpha, B, H, d, dev, True)
+    _need(out, "out", torch.float32, (B, H, d), dev)
+    with _on(dev, stream):
+        _check(load().fp32_linear_step(_ptr(pool), S_, H, d, d, _ptr(slot_idx), B, _ptr(q), _ptr(k),
+                                       _ptr(v), dt, _ptr(alpha), decay, _ptr(out), _stream(stream)))
+
+
+def prefill_workspace_bytes(delta: bool, B: int, T: int, H: int, d: int, dtype, decay: int = DAMP_DECAY_SCALAR) -> int:
+    """Bytes of the workspace of fp32_linear_prefill (``delta`` false) or fp32_delta_prefill."""
+    torch = _torch()
+    return load().fp32_prefill_workspace_bytes(int(delta), B, T, H, d,
+                                               DAMP_BF16 if dtype == torch.bfloat16 else DAMP_F32, decay)
+
+
+def _prefill(delta, pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, resume, workspace, stream):
+    torch = _torch()
+    _need(slot_idx, "slot_idx", torch.int32, (slot_idx.numel(),))
+    B, dev = slot_idx.shape[0], slot_idx.device
+    S_, H, d = _fp32_pool(pool, dev)
+    dt = _dtype(q, "q")
+    T = q.shape[0] if q.dim() == 3 else -1
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _need(t, name, q.dtype, (T, H, d), dev)
+    decay = _decay(alpha, T, H, d, dev, not delta)
+    if delta:
+        _need(beta, "beta", torch.float32, (T, H), dev)
+    if resume is not None:
+        _need(resume, "resume", torch.int32, (B,), dev)
+    L = load()
+    with _on(dev, stream):
+        ws, n = _workspace(workspace, L.fp32_prefill_workspace_bytes(delta, B, T, H, d, dt, decay), dev)
+        head = (_ptr(pool), S_, H, d, d, _ptr(slot_idx), _ptr(cu_seqlens),
+                _ptr(resume) if resume is not None else None, B, T, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), decay)
+        if delta:
+            _check(L.fp32_delta_prefill(*head, _ptr(beta), _ptr(out), ws, n, _stream(stream)))
+        else:
+            _check(L.fp32_linear_prefill(*head, _ptr(out), ws, n, _stream(stream)))
+
+
+def fp32_linear_prefill(pool, slot_idx, cu_seqlens, q, k, v, alpha, out, resume=None, workspace=None,
+                        stream=None) -> None:
+    """Linear attention over the prompts of B requests on an fp32 state pool: q, k, v, out bf16 or
+    fp32 [T, H, d], request b's tokens the rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32
+    [B + 1]); alpha fp32 [T, H], [T, H, d] or [H]. Writes the readouts and each request's last
+    state. ``resume`` (int32 [B]): nonzero continues from the slot's state, else from zero.
+    ``workspace`` (uint8, prefill_workspace_bytes) is allocated for the call if not given."""
+    _prefill(0, pool, slot_idx, cu_seqlens, q, k, v, alpha, None, out, resume, workspace, stream)
+
+
+def fp32_delta_prefill(pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, resume=None,
+                       workspace=None, stream=None) -> None:
+    """The gated delta rule over the prompts of B requests, the prompt form of fp32_decode_step:
+    arguments as fp32_linear_prefill with beta fp32 [T, H]; alpha [T, H] or [T, H, d]."""
+    _prefill(1, pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, resume, workspace, stream)
+
+
+# ------------------------------------------------------------------------------------------
+# paged key-value cache
+# ------------------------------------------------------------------------------------------
+def _pages(k_pages, v_pages, dev):
+    torch = _torch()
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a tensor [num_pages, Hkv, page_size, d]")
+    n, Hkv, page, d = k_pages.shape
+    _need(k_pages, "k_pages", torch.bfloat16, (n, Hkv, page, d), dev)
+    _need(v_pages, "v_pages", torch.bfloat16, (n, Hkv, page, d), dev)
+    return n, Hkv, page, d
+
+
+def kv_build_tables(seq_lens, new_lens, free_pages, block_table, page_size: int, slot_map, positions,
+                    cu_new, used, stream=None) -> None:
+    """The tables of one serving step (damp.h): seq_lens, new_lens int32 [B]; free_pages int32;
+    block_table int32 [B, max_blocks], its new entries written; slot_map int64 [T], positions int32
+    [T] (or None), cu_new int32 [B + 1] and used int32 [1] are written."""
+    torch = _torch()
+    _need(seq_lens, "seq_lens", torch.int32, (seq_lens.numel(),))
+    B, dev = seq_lens.shape[0], seq_lens.device
+    _need(new_lens, "new_lens", torch.int32, (B,), dev)
+    _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    blocks = block_table.shape[1]
+    _need(block_table, "block_table", torch.int32, (B, blocks), dev)
+    T = slot_map.numel()
+    _need(slot_map, "slot_map", torch.int64, (T,), dev)
+    if positions is not None:
+        _need(positions, "positions", torch.int32, (T,), dev)
+    _need(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    _need(used, "used", torch.int32, (1,), dev)
+    with _on(dev, stream):
+        _check(load().kv_build_tables(_ptr(seq_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
+                                      page_size, _ptr(block_table), blocks, _ptr(slot_map),
+                                      _ptr(positions) if positions is not None else None, T, _ptr(cu_new),
+                                      _ptr(used), _stream(stream)))
+
+
+def kv_append(k, v, slot_map, k_pages, v_pages, stream=None) -> None:
+    """Stores k, v bf16 [T, Hkv, d] at the cache slots slot_map int64 [T] (outside the cache: skipped)."""
+    torch = _torch()
+    n, Hkv, page, d = _pages(k_pages, v_pages, slot_map.device)
+    T, dev = slot_map.numel(), slot_map.device
+    _need(slot_map, "slot_map", torch.int64, (T,), dev)
+    _need(k, "k", torch.bfloat16, (T, Hkv, d), dev)
+    _need(v, "v", torch.bfloat16, (T, Hkv, d), dev)
+    with _on(dev, stream):
+        _check(load().kv_append(_ptr(k), _ptr(v), _ptr(slot_map), T, Hkv, d, _ptr(k_pages), _ptr(v_pages), n,
+                                page, _stream(stream)))
+
+
+def kv_decode_attention_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int, d: int, max_len: int) -> int:
+    return load().kv_decode_attention_workspace_bytes(B, num_q_heads, num_kv_heads, d, max_len)
+
+
+def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=None, k_new=None, v_new=None,
+                        max_len=None, workspace=None, stream=None) -> None:
+    """Attention of one new token per request: q, out bf16 [B, Hq, d]; pages bf16 [num_pages, Hkv,
+    page_size, d]; block_table int32 [B, max_blocks]; seq_lens int32 [B], the new token included
+    (0: out is 0). ``scale`` defaults to d^-0.5. ``k_new``, ``v_new`` (bf16 [B, Hkv, d]): stored at
+    position seq_lens - 1 first. ``max_len``: an upper bound of seq_lens (the table's by default).
+    ``workspace`` (uint8, kv_decode_attention_workspace_bytes) is allocated for the call if not given."""
+    torch = _torch()
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [B, Hq, d]")
+    B, Hq, d = q.shape
+    dev = q.device
+    n, Hkv, page, dc = _pages(k_pages, v_pages, dev)
+    _need(q, "q", torch.bfloat16, (B, Hq, dc), dev)
+    _need(out, "out", torch.bfloat16, (B, Hq, dc), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    blocks = block_table.shape[1]
+    _need(block_table, "block_table", torch.int32, (B, blocks), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new must be given together")
+    if k_new is not None:
+        _need(k_new, "k_new", torch.bfloat16, (B, Hkv, dc), dev)
+        _need(v_new, "v_new", torch.bfloat16, (B, Hkv, dc), dev)
+    if max_len is None:
+        max_len = blocks * page
+    L = load()
+    with _on(dev, stream):
+        ws, nb = _workspace(workspace, L.kv_decode_attention_workspace_bytes(B, Hq, Hkv, dc, max_len), dev)
+        _check(L.kv_decode_attention(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), B,
+                                     Hq, Hkv, dc, n, page, blocks, max_len, dc ** -0.5 if scale is None else scale,
+                                     _ptr(k_new) if k_new is not None else None,
+                                     _ptr(v_new) if v_new is not None else None, _ptr(out), ws, nb,
+                                     _stream(stream)))
