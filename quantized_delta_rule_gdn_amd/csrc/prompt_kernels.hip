@@ -450,6 +450,352 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
       for (int i = 0; i < 4; ++i) pool[(MD * i + m) * D + 16 * nt] = S[m][nt][i];
 }
 
+// ---- linear attention ------------------------------------------------------------------------
+// One workgroup of 4 waves per (segment of a prompt, head); wave w owns the value columns D / 4 * w
+// .. of the state, the values and the readouts, so between the chunks nothing of the state leaves
+// its registers: as the B operand of Q S it is the accumulator tiles as they stand (k permuted:
+// mfma), and Q is read to match. K, Q and K^T are staged in LDS once per chunk for all waves, P is
+// formed by 16 rows per wave. Long prompts of few heads are cut into segments: a first launch
+// (STATES) sums every segment's own state, a scan turns them into the states before each segment,
+// and the readouts of all segments run at once.
+enum LinearMode : int { LIN_WHOLE = 0, LIN_STATES = 1, LIN_SEGMENTS = 2 };
+
+struct Segments {
+  int len;          // tokens per segment, a multiple of 64; whole prompts: larger than any
+  float* states;    // [segment number][H][D][D]: own states, then the states before
+  float* decays;    // [segment number][H]: log2 of a segment's decay
+};
+
+template <int D, int DECAY, int MODE>
+__global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, const Segments sg) {
+  constexpr int KS = D / 32, MD = D / 64, XT = D / 16, LK = D + 8;
+  constexpr bool kReadout = MODE != LIN_STATES;
+  __shared__ __align__(16) uint16_t qs[kReadout ? kC : 1][LK], ks[kReadout ? kC : 1][LK];
+  __shared__ __align__(16) uint16_t kt[D][kLd];
+  __shared__ __align__(16) uint16_t pp[2][kReadout ? kC : 1][kLd];
+  __shared__ Logs logs[2][kC];
+  __shared__ __align__(16) float eg[2][kC], wc[2][kC];
+  __shared__ double ends[2];
+  const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int unit = __builtin_amdgcn_workgroup_id_x();
+  const int head = unit % a.H, seg = unit / a.H;
+  int b = seg, t_begin, t_end;
+  if constexpr (MODE == LIN_WHOLE) {
+    const Span sp = span_of(a, b);
+    t_begin = sp.begin;
+    t_end = sp.end;
+  } else {
+    const Piece pc = piece_of(a, seg, sg.len);
+    b = pc.b;
+    t_begin = pc.t0;
+    t_end = pc.t0 + pc.n;
+  }
+  if (t_end <= t_begin) return;
+  const bool final = MODE == LIN_WHOLE || t_end == span_of(a, b).end;
+  if (MODE == LIN_STATES && final) return;      // no segment waits for the last one's state
+  const int64_t slot = a.slot_idx[b];
+  if (!slot_in_pool(slot, a.num_slots)) return;
+  const int64_t rstep = int64_t(a.H) * D;
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + int64_t(head) * D;
+  const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(head) * D;
+  const int col = (D / 4) * w + MD * r;           // this lane's first value column
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D + col;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D + col;
+  float* pool = a.pool + ((slot * a.H + head) * D) * int64_t(D) + col;
+  float* states = MODE == LIN_WHOLE ? nullptr : sg.states + int64_t(unit) * D * D + col;
+
+  f32x4 S[XT][MD];   // S[x][m][i]: key channel 16 x + 4 g + i, value column col + m
+  {
+    const float* from = MODE == LIN_SEGMENTS ? states : MODE == LIN_WHOLE && a.resume && a.resume[b] != 0 ? pool : nullptr;
+#pragma unroll
+    for (int x = 0; x < XT; ++x)
+#pragma unroll
+      for (int m = 0; m < MD; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[x][m][i] = from ? from[(16 * x + 4 * g + i) * D + m] : 0.0f;
+  }
+
+  // one chunk's rows, in registers until LDS is free for them: rows past the end are zero
+  constexpr int RW = D / 32;                      // 16-byte pieces of K (and of Q) per thread
+  uint4 kr[RW], qr[RW];
+  uint32_t tr[2][8], vr[2][8];                    // K by columns (64 channel groups x 8 token octets), V
+  const auto load_rows = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      const int x = tid + 256 * j, t = t0 + x / (D / 8), c = x % (D / 8);
+      if constexpr (kReadout) {
+        const bool live = t < t_end;
+        const int64_t at = min(t, t_end - 1) * rstep + c * 8;
+        kr[j] = *reinterpret_cast<const uint4*>(kp + at);
+        qr[j] = *reinterpret_cast<const uint4*>(qp + at);
+        if (!live) kr[j] = qr[j] = make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int x = tid + 256 * j, c = x % 64, o = x / 64;   // channels MD c .., tokens 8 o ..
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = t0 + 8 * o + i;
+        const uint16_t* p = kp + min(t, t_end - 1) * rstep + MD * c;
+        tr[j][i] = MD == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+        if (t >= t_end) tr[j][i] = 0;
+      }
+    }
+  };
+  const auto load_v = [&](int t0) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = t0 + 32 * x + 8 * g + j;
+        const uint16_t* p = vp + min(t, t_end - 1) * rstep;
+        vr[x][j] = MD == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+        if (t >= t_end) vr[x][j] = 0;
+      }
+  };
+  const auto store_logs = [&](int t0, int to) {   // by one wave, a chunk ahead
+    const double gs = chunk_logs<DECAY>(a, t0, min(kC, t_end - t0), head, lane);
+    const double end = __shfl(gs, 63);
+    logs[to][lane] = split_logs(gs);
+    eg[to][lane] = pow2(static_cast<float>(gs));
+    wc[to][lane] = pow2(static_cast<float>(end - gs));
+    if (lane == 0) ends[to] = end;
+  };
+
+  double total = 0.0;
+  load_rows(t_begin);
+  load_v(t_begin);
+  if (w == 0) store_logs(t_begin, 0);
+  int at = 0;
+  for (int t0 = t_begin; t0 < t_end; t0 += kC, at ^= 1) {
+    const bool more = t_end - t0 > kC;
+    if constexpr (kReadout) {
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        const int x = tid + 256 * j;
+        *reinterpret_cast<uint4*>(&ks[x / (D / 8)][(x % (D / 8)) * 8]) = kr[j];
+        *reinterpret_cast<uint4*>(&qs[x / (D / 8)][(x % (D / 8)) * 8]) = qr[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int x = tid + 256 * j, c = x % 64, o = x / 64;
+#pragma unroll
+      for (int m = 0; m < MD; ++m) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_perm(tr[j][2 * i + 1], tr[j][2 * i], m ? 0x07060302u : 0x05040100u);
+        *reinterpret_cast<uint4*>(&kt[MD * c + m][8 * o]) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+    __syncthreads();
+    if (more) load_rows(t0 + kC);
+    if constexpr (kReadout) {
+      Frag qf[KS];
+#pragma unroll
+      for (int x = 0; x < KS; ++x) qf[x] = load_frag(&qs[16 * w + r][x * 32 + g * 8]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+        const int s = 16 * c + r;
+        if (c <= w) {
+#pragma unroll
+          for (int x = 0; x < KS; ++x) p = mfma(qf[x], load_frag(&ks[s][x * 32 + g * 8]), p);
+          const Logs ls = logs[at][s];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 16 * w + 4 * g + i;
+            p[i] = s <= t ? p[i] * decay_between(logs[at][t], ls) : 0.0f;
+          }
+        }
+        if ((c | 1) > (w | 1)) continue;          // no product reads these
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          uint32_t u[2];
+          split_bf16<2>(p[i], p[i + 1], u);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            pp[x][16 * w + 4 * g + i][s] = static_cast<uint16_t>(u[x]);
+            pp[x][16 * w + 4 * g + i + 1][s] = static_cast<uint16_t>(u[x] >> 16);
+          }
+        }
+      }
+      __syncthreads();
+      f32x4 o[4][MD];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int m = 0; m < MD; ++m) o[rt][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        Frag sf[2][MD];
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t u[2];
+            split_bf16<2>(S[2 * x + j / 2][m][2 * (j & 1)], S[2 * x + j / 2][m][2 * (j & 1) + 1], u);
+            sf[0][m].w[j] = u[0];
+            sf[1][m].w[j] = u[1];
+          }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const Frag q = load_frag2(&qs[16 * rt + r][x * 32 + g * 4], &qs[16 * rt + r][x * 32 + 16 + g * 4]);
+#pragma unroll
+          for (int m = 0; m < MD; ++m) {
+            o[rt][m] = mfma(q, sf[0][m], o[rt][m]);
+            o[rt][m] = mfma(q, sf[1][m], o[rt][m]);
+          }
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const float4 e = *reinterpret_cast<const float4*>(&eg[at][16 * rt + 4 * g]);
+#pragma unroll
+        for (int m = 0; m < MD; ++m) {
+          o[rt][m][0] *= e.x; o[rt][m][1] *= e.y; o[rt][m][2] *= e.z; o[rt][m][3] *= e.w;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        Frag vf[MD];
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            vf[m].w[j] = __builtin_amdgcn_perm(vr[x][2 * j + 1], vr[x][2 * j], m ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int rt = 2 * x; rt < 4; ++rt)         // tokens 32 x .. reach rows from 32 x on
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const Frag pf = load_frag(&pp[p][16 * rt + r][x * 32 + g * 8]);
+#pragma unroll
+            for (int m = 0; m < MD; ++m) o[rt][m] = mfma(pf, vf[m], o[rt][m]);
+          }
+      }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = t0 + 16 * rt + 4 * g + i;
+          if (t < t_end) {
+            if constexpr (MD == 2) *reinterpret_cast<uint32_t*>(op + t * rstep) = pack_bf16(o[rt][0][i], o[rt][1][i]);
+            else op[t * rstep] = float_to_bf16_bits(o[rt][0][i]);
+          }
+        }
+    }
+    // S = 2^G_C S + K^T (2^(G_C - G) V)
+    const float last = pow2(static_cast<float>(ends[at]));
+    total += ends[at];
+#pragma unroll
+    for (int x = 0; x < XT; ++x)
+#pragma unroll
+      for (int m = 0; m < MD; ++m) S[x][m] *= last;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      Frag vf[3][MD];
+      const float4 w0 = *reinterpret_cast<const float4*>(&wc[at][32 * x + 8 * g]), w1 = *reinterpret_cast<const float4*>(&wc[at][32 * x + 8 * g + 4]);
+      const float f[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+      for (int m = 0; m < MD; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t lo = vr[x][2 * j], hi = vr[x][2 * j + 1];
+          uint32_t u[3];
+          split_bf16<3>((m ? bf16_hi(lo) : bf16_lo(lo)) * f[2 * j], (m ? bf16_hi(hi) : bf16_lo(hi)) * f[2 * j + 1], u);
+#pragma unroll
+          for (int p = 0; p < 3; ++p) vf[p][m].w[j] = u[p];
+        }
+#pragma unroll
+      for (int y = 0; y < XT; ++y) {
+        const Frag kf = load_frag(&kt[16 * y + r][x * 32 + g * 8]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int m = 0; m < MD; ++m) S[y][m] = mfma(kf, vf[p][m], S[y][m]);
+      }
+    }
+    if (more) {
+      load_v(t0 + kC);
+      if (w == 0) store_logs(t0 + kC, at ^ 1);
+    }
+    __syncthreads();
+  }
+  float* to = MODE == LIN_STATES ? states : final ? pool : nullptr;
+  if (to) {
+#pragma unroll
+    for (int x = 0; x < XT; ++x)
+#pragma unroll
+      for (int m = 0; m < MD; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[(16 * x + 4 * g + i) * D + m] = S[x][m][i];
+  }
+  if (MODE == LIN_STATES && tid == 0) sg.decays[unit] = static_cast<float>(total);
+}
+
+// The segments' own states turned into the states before each segment, 4 values a thread.
+__global__ __launch_bounds__(256) void linear_scan_kernel(const PromptArgs a, const Segments sg, int dd4) {
+  const int64_t x = int64_t(__builtin_amdgcn_workgroup_id_x()) * 256 + __builtin_amdgcn_workitem_id_x();
+  const int64_t u = x / dd4;
+  if (u >= int64_t(a.B) * a.H) return;
+  const int b = static_cast<int>(u / a.H), head = static_cast<int>(u - int64_t(b) * a.H), e = static_cast<int>(x - u * dd4);
+  const int64_t slot = a.slot_idx[b];
+  if (!slot_in_pool(slot, a.num_slots)) return;
+  const Span sp = span_of(a, b);
+  f32x4 in{0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.resume && a.resume[b] != 0 && sp.end > sp.begin)
+    in = reinterpret_cast<const f32x4*>(a.pool + (slot * a.H + head) * dd4 * 4)[e];
+  const int64_t first = sp.begin / sg.len + b;
+  const int n = (sp.end - sp.begin + sg.len - 1) / sg.len;
+  for (int j = 0; j < n; ++j) {
+    const int64_t unit = (first + j) * a.H + head;
+    f32x4* p = reinterpret_cast<f32x4*>(sg.states) + unit * dd4 + e;
+    f32x4 own{0.0f, 0.0f, 0.0f, 0.0f};
+    float f = 0.0f;
+    if (j + 1 < n) {
+      own = *p;
+      f = pow2(sg.decays[unit]);
+    }
+    *p = in;
+    in = in * f + own;
+  }
+}
+
+// Segments of a call: none (whole prompts) where the prompts alone fill the chip.
+int segment_len(int32_t B, int32_t T, int32_t H) {
+  if (int64_t(B) * H >= 512 || T <= 4 * kC) return 0;
+  const int64_t want = (int64_t(T) * H + 1023) / 1024;
+  return static_cast<int>(std::max<int64_t>((want + kC - 1) / kC * kC, 4 * kC));
+}
+
+template <int D, int DECAY>
+void linear_dd(const PromptArgs& a, hipStream_t s) {
+  Segments sg{segment_len(a.B, a.T, a.H), nullptr, nullptr};
+  if (sg.len == 0) {
+    const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H));
+    hipLaunchKernelGGL((linear_chunk_kernel<D, DECAY, LIN_WHOLE>), grid, dim3(256), 0, s, a, sg);
+    return;
+  }
+  const int64_t units = (int64_t(a.T / sg.len) + a.B) * a.H;
+  sg.states = reinterpret_cast<float*>(a.ws);
+  sg.decays = sg.states + units * D * D;
+  const dim3 grid(static_cast<unsigned>(units));
+  hipLaunchKernelGGL((linear_chunk_kernel<D, DECAY, LIN_STATES>), grid, dim3(256), 0, s, a, sg);
+  const int64_t threads = int64_t(a.B) * a.H * (D * D / 4);
+  hipLaunchKernelGGL(linear_scan_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a, sg, D * D / 4);
+  hipLaunchKernelGGL((linear_chunk_kernel<D, DECAY, LIN_SEGMENTS>), grid, dim3(256), 0, s, a, sg);
+}
+
+template <int D>
+hipError_t linear_d(int decay, const PromptArgs& a, hipStream_t s) {
+  if (decay == DECAY_HEAD) linear_dd<D, DECAY_HEAD>(a, s);
+  else linear_dd<D, DECAY_SCALAR>(a, s);
+  return hipGetLastError();
+}
+
 template <int D>
 hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
   const unsigned chunks = static_cast<unsigned>(a.T / kC + a.B) * static_cast<unsigned>(a.H);
@@ -467,11 +813,13 @@ bool chunked(int d, int decay, int bf16) { return bf16 && (d == 64 || d == 128) 
 int64_t prefill_ws_bytes(bool delta, int d, int decay, int bf16, int32_t B, int32_t T, int32_t H) {
   if (!chunked(d, decay, bf16)) return 0;
   if (delta) return (int64_t(T) / kC + B) * H * kDeltaUnit;
-  return 0;
+  const int len = segment_len(B, T, H);
+  return len ? (int64_t(T / len) + B) * H * (int64_t(d) * d + 1) * 4 : 0;
 }
 
 hipError_t launch_prefill(bool delta, int d, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
-  if (!chunked(d, decay, bf16) || !delta) return launch_prompt_token(d, delta, decay, bf16, a, s);
+  if (!chunked(d, decay, bf16)) return launch_prompt_token(d, delta, decay, bf16, a, s);
+  if (!delta) return d == 64 ? linear_d<64>(decay, a, s) : linear_d<128>(decay, a, s);
   return d == 64 ? delta_d<64>(a, s) : delta_d<128>(a, s);
 }
 
