@@ -84,6 +84,18 @@ __device__ __forceinline__ Frag load_frag2(const void* p, const void* p2) {   //
   return Frag{{v.x, v.y, u.x, u.y}};
 }
 
+// ds_read_b64_tr_b16 twice: of a bf16 array in LDS with rows of k and neighbouring columns, 8 rows of
+// one column per lane. Each 16 lanes read 4 rows x 16 columns: lane l passes the address of row l / 4,
+// columns 4 (l % 4) .. + 3, and gets column l of the 4 rows.
+__device__ __forceinline__ Frag load_frag_t(const uint16_t* rows_lo, const uint16_t* rows_hi) {
+  using s16x4 = __attribute__((ext_vector_type(4))) short;
+  using lds_ptr = __attribute__((address_space(3))) s16x4*;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)rows_lo);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)rows_hi);
+  const uint2 u = __builtin_bit_cast(uint2, a), v = __builtin_bit_cast(uint2, b);
+  return Frag{{u.x, u.y, v.x, v.y}};
+}
+
 // 2^x with results below binary32's normal range flushed or subnormal (v_exp_f32).
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 

@@ -63,10 +63,11 @@ __device__ __forceinline__ Logs split_logs(double g) {
 __device__ __forceinline__ float decay_between(Logs t, Logs s) { return pow2((t.hi - s.hi) + (t.lo - s.lo)); }
 
 // ---- the delta rule: what a chunk's keys and gates give -------------------------------------
-// Workspace of one chunk and head: X diag(b) in three bf16 pieces and P in two, [64][64] each, then
-// 2^G_t and 2^(G_C - G_t).
+// Workspace of one chunk and head: X diag(b) in three bf16 pieces and P in two, [64][64] each (the
+// upper right quarter is neither written nor read), then 2^G_t and 2^(G_C - G_t).
 constexpr int kPlane = kC * kC * 2;
-constexpr int kDeltaUnit = 5 * kPlane + 2 * kC * 4;
+constexpr int kGates = 5 * kPlane;
+constexpr int kDeltaUnit = kGates + 2 * kC * 4;
 
 __device__ __forceinline__ f32x4 mul16(const float* A, const float* B, int ld, f32x4 c, int r, int g) {
 #pragma unroll
@@ -119,7 +120,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
     const double end = __shfl(gs, 63);
     logs[lane] = split_logs(gs);
     beta[lane] = lane < pc.n ? a.beta[int64_t(pc.t0 + lane) * a.H + head] : 0.0f;
-    float* sc = reinterpret_cast<float*>(ws + 5 * kPlane);
+    float* sc = reinterpret_cast<float*>(ws + kGates);
     sc[lane] = pow2(static_cast<float>(gs));
     sc[kC + lane] = pow2(static_cast<float>(end - gs));
   }
@@ -197,56 +198,70 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
     }
   }
   __syncthreads();
-  // 16 values of one row per thread: X's columns scaled by beta, in three pieces; P in two
+  // 16 values of one row per thread: X's columns scaled by beta, in three pieces, and P in two
   const int t = tid >> 2, c0 = (tid & 3) * 16;
-  uint32_t px[3][8], pp[2][8];
+  if (t < 32 && c0 >= 32) return;
+  uint32_t px[5][8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     uint32_t u[3];
     split_bf16<3>(xf[t][c0 + 2 * j] * beta[c0 + 2 * j], xf[t][c0 + 2 * j + 1] * beta[c0 + 2 * j + 1], u);
     px[0][j] = u[0]; px[1][j] = u[1]; px[2][j] = u[2];
     split_bf16<2>(pf[t][c0 + 2 * j], pf[t][c0 + 2 * j + 1], u);
-    pp[0][j] = u[0]; pp[1][j] = u[1];
+    px[3][j] = u[0]; px[4][j] = u[1];
   }
   uint4* dst = reinterpret_cast<uint4*>(ws + (t * kC + c0) * 2);
 #pragma unroll
-  for (int p = 0; p < 3; ++p)
+  for (int p = 0; p < 5; ++p)
 #pragma unroll
     for (int h = 0; h < 2; ++h) dst[p * (kPlane / 16) + h] = make_uint4(px[p][4 * h], px[p][4 * h + 1], px[p][4 * h + 2], px[p][4 * h + 3]);
-#pragma unroll
-  for (int p = 0; p < 2; ++p)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) dst[(3 + p) * (kPlane / 16) + h] = make_uint4(pp[p][4 * h], pp[p][4 * h + 1], pp[p][4 * h + 2], pp[p][4 * h + 3]);
 }
 
 // ---- the delta rule: the chain over the chunks ---------------------------------------------
 // One workgroup of 4 waves per (request, head, 16 NT value columns): a chunk's work is split over
 // token rows (16 per wave) and, for the state's update, key channels (D / 4 per wave), so a wave
-// loads only its own rows of K, Q, X and P, straight into operand registers, one chunk ahead; the
-// state, R and E change hands in LDS as [column][k] arrays of bf16 pieces. Three barriers a chunk.
-// What bounds it is the chain's latency: about 50 NT dependent-by-stages matrix instructions a wave.
+// loads only its own rows of Q, X and P, straight into operand registers, one chunk ahead; K is
+// staged in LDS, where it is read by rows and, transposed, by channels; the state, R and E change
+// hands in LDS as [column][k] arrays of bf16 pieces. Three barriers a chunk. S enters K S and Q S in
+// two pieces: K S is a small part of E next to V, so that its 2^-17 stays below a binary32 sum's
+// error of the state.
 template <int D>
 struct DeltaRows {   // one wave's operands of a chunk
-  Frag k[D / 32], q[D / 32];
-  Frag x[3][2], p[2][2];
-  uint32_t kt[2][8];     // keys of tokens 32 x + 8 g + j, this lane's D / 64 channels
-  float4 eg, wc;         // 2^G and 2^(G_C - G) of rows 16 w + 4 g .. + 3
+  Frag q[D / 32], x[3][2], p[2][2];
+  uint4 k[D / 32];       // this thread's share of K, on its way to LDS
+  float eg[4], wc[4];    // 2^G and 2^(G_C - G) of rows 16 w + 4 g .. + 3
   float last;            // 2^G_C
 };
+
+// Blocks go to the 8 XCDs in turn, and each XCD has its own L2: numbers that differ by 8 share one.
+// Of `count` * `group` blocks, the `group` ones of one item get such numbers (whole sets of 8 items;
+// the rest, at the end, as they come).
+struct Place {
+  int item, part;
+};
+
+__device__ __forceinline__ Place place_of(unsigned id, unsigned count, unsigned group) {
+  const unsigned set = id / (8 * group);
+  if ((set + 1) * 8 <= count) {
+    const unsigned k = id - set * 8 * group;
+    return Place{static_cast<int>(set * 8 + k % 8), static_cast<int>(k / 8)};
+  }
+  return Place{static_cast<int>(id / group), static_cast<int>(id % group)};
+}
 
 template <int D, int NT>
 __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, MD = D / 64, LS = D + 8, NC = 16 * NT;
-  __shared__ __align__(16) uint16_t sp[3][NC][LS];
+  __shared__ __align__(16) uint16_t kb[2][kC][LS];
+  __shared__ __align__(16) uint16_t sp[2][NC][LS];
   __shared__ __align__(16) uint16_t rp[3][NC][kLd], ep[2][NC][kLd], wp[3][NC][kLd];
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
   constexpr int slices = D / NC;
-  unsigned id = __builtin_amdgcn_workgroup_id_x();
-  const int c0 = (id % slices) * NC;
-  id /= slices;
-  const int head = id % a.H, b = id / a.H;
+  // the slices of a head read the same K, Q, X and P: one L2 for them
+  const Place at = place_of(__builtin_amdgcn_workgroup_id_x(), static_cast<unsigned>(a.B) * a.H, slices);
+  const int c0 = at.part * NC, head = at.item % a.H, b = at.item / a.H;
   const int64_t slot = a.slot_idx[b];
   if (!slot_in_pool(slot, a.num_slots)) return;
   const Span sp_b = span_of(a, b);
@@ -256,198 +271,266 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(head) * D;
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D + c0;
   uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D + c0;
+  const uint8_t* ws = a.ws + (int64_t(sp_b.begin / kC + b) * a.H + head) * kDeltaUnit;
+  const int64_t ws_step = int64_t(a.H) * kDeltaUnit;
   const int own = (D / 4) * w;                      // this wave's first key channel of the state
-  float* pool = a.pool + ((slot * a.H + head) * D + own + MD * 4 * g) * int64_t(D) + c0 + r;
+  float* pool = a.pool + ((slot * a.H + head) * D + own + 4 * g) * int64_t(D) + c0 + r;
 
-  f32x4 S[MD][NT];   // S[m][nt][i]: key channel own + MD (4 g + i) + m, column c0 + 16 nt + r
+  f32x4 S[MD][NT];   // S[m][nt][i]: key channel own + 16 m + 4 g + i, column c0 + 16 nt + r
   const bool resume = a.resume && a.resume[b] != 0;
 #pragma unroll
   for (int m = 0; m < MD; ++m)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[m][nt][i] = resume ? pool[(MD * i + m) * D + 16 * nt] : 0.0f;
+      for (int i = 0; i < 4; ++i) S[m][nt][i] = resume ? pool[(16 * m + i) * D + 16 * nt] : 0.0f;
 
   const auto share_state = [&]() {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint32_t u[2 * MD][3];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 2 * MD; ++j) {
-        if constexpr (MD == 2) split_bf16<3>(S[0][nt][j], S[1][nt][j], u[j]);
-        else split_bf16<3>(S[0][nt][2 * j], S[0][nt][2 * j + 1], u[j]);
-      }
+      for (int m = 0; m < MD; ++m) {
+        uint32_t u0[2], u1[2];
+        split_bf16<2>(S[m][nt][0], S[m][nt][1], u0);
+        split_bf16<2>(S[m][nt][2], S[m][nt][3], u1);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        uint16_t* dst = &sp[p][16 * nt + r][own + MD * 4 * g];
-        if constexpr (MD == 2) *reinterpret_cast<uint4*>(dst) = make_uint4(u[0][p], u[1][p], u[2][p], u[3][p]);
-        else *reinterpret_cast<uint2*>(dst) = make_uint2(u[0][p], u[1][p]);
+        for (int p = 0; p < 2; ++p) *reinterpret_cast<uint2*>(&sp[p][16 * nt + r][own + 16 * m + 4 * g]) = make_uint2(u0[p], u1[p]);
       }
-    }
   };
+  // A chunk's loads go through buffer resources that end with its last row: what lies past it reads
+  // as 0 (and is not stored). A lane's offsets are the same in every chunk. Every load is made every
+  // time and in the order of use, so that the waits on earlier ones can count the later ones.
+  const uint32_t ostep = static_cast<uint32_t>(rstep) * 2;
+  const uint32_t off_row = (16 * w + r) * ostep + g * 16;                  // rows of Q as operands
+  const uint32_t off_k = (tid / (D / 8)) * ostep + (tid % (D / 8)) * 16;   // rows of K on their way to LDS
+  const uint32_t off_val = (16 * w + 4 * g) * ostep + r * 2;               // rows of V and the readouts
+  const uint32_t off_ws = ((16 * w + r) * kC + g * 8) * 2;                 // rows of X and P
+  const uint32_t off_ws1 = w < 2 ? kDeltaUnit : off_ws + 64;               // their right halves; none above the diagonal
   DeltaRows<D> f;
   uint16_t vv[NT][4];
-  // rows past the last token repeat it: their beta is 0, so E is 0 there
-  const auto load_kqv = [&](int t0) {
-    const int64_t at = min(t0 + 16 * w + r, sp_b.end - 1) * rstep + g * 8;
+  const auto rows = [&](const uint16_t* p, int t0, int width) {
+    return make_rsrc(p + t0 * rstep, (min(sp_b.end - t0, kC) - 1) * ostep + width * 2);
+  };
+  const auto chunk_ws = [&](int t0) { return make_rsrc(ws + (t0 - sp_b.begin) / kC * ws_step, kDeltaUnit); };
+  const auto frag = [](rsrc_t rs, uint32_t off, int imm) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, imm, 0);
+    return Frag{{v[0], v[1], v[2], v[3]}};
+  };
+  const auto load_q = [&](int t0) {
+    const rsrc_t qr = rows(qp, t0, D);
 #pragma unroll
-    for (int x = 0; x < KS; ++x) {
-      f.k[x] = load_frag(kp + at + x * 32);
-      f.q[x] = load_frag(qp + at + x * 32);
+    for (int x = 0; x < KS; ++x) f.q[x] = frag(qr, off_row + x * 64, 0);
+  };
+  const auto load_v = [&](int t0) {
+    const rsrc_t vr = rows(vp, t0, NC), wr = chunk_ws(t0);
+    const auto e = __builtin_amdgcn_raw_buffer_load_b128(wr, kGates + (16 * w + 4 * g) * 4, 0, 0);
+    const auto c = __builtin_amdgcn_raw_buffer_load_b128(wr, kGates + (kC + 16 * w + 4 * g) * 4, 0, 0);
+    f.last = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(wr, kGates + (kC - 1) * 4, 0, 0));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f.eg[i] = __uint_as_float(e[i]);
+      f.wc[i] = __uint_as_float(c[i]);
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vv[nt][i] = vp[min(t0 + 16 * w + 4 * g + i, sp_b.end - 1) * rstep + 16 * nt + r];
-  };
-  const auto unit_ws = [&](int t0) {
-    const int64_t i = sp_b.begin / kC + b + (t0 - sp_b.begin) / kC;
-    return a.ws + (i * a.H + head) * kDeltaUnit;
+      for (int i = 0; i < 4; ++i) vv[nt][i] = __builtin_amdgcn_raw_buffer_load_b16(vr, off_val + i * ostep + 32 * nt, 0, 0);
   };
   const auto load_x = [&](int t0) {
-    const uint8_t* ws = unit_ws(t0) + ((16 * w + r) * kC + g * 8) * 2;
+    const rsrc_t wr = chunk_ws(t0);
 #pragma unroll
-    for (int p = 0; p < 3; ++p)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (x == 0 || w >= 2) f.x[p][x] = load_frag(ws + p * kPlane + x * 64);
+    for (int p = 0; p < 3; ++p) {
+      f.x[p][0] = frag(wr, off_ws + p * kPlane, 0);
+      f.x[p][1] = frag(wr, off_ws1 + p * kPlane, 0);
+    }
   };
-  const auto load_rest = [&](int t0) {
-    const uint8_t* ws = unit_ws(t0) + ((16 * w + r) * kC + g * 8) * 2 + 3 * kPlane;
+  const auto load_p = [&](int t0) {
+    const rsrc_t wr = chunk_ws(t0);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      f.p[p][0] = frag(wr, off_ws + (3 + p) * kPlane, 0);
+      f.p[p][1] = frag(wr, off_ws1 + (3 + p) * kPlane, 0);
+    }
+  };
+  constexpr int kRows = 256 / (D / 8);   // rows of K that the threads' shares are apart
+  const auto load_k = [&](int t0) {
+    const rsrc_t kr = rows(kp, t0, D);
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      const Frag v = frag(kr, off_k + j * kRows * ostep, 0);
+      f.k[j] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    }
+  };
+  const auto store_k = [&](int to) {
+#pragma unroll
+    for (int j = 0; j < KS; ++j) *reinterpret_cast<uint4*>(&kb[to][tid / (D / 8) + j * kRows][(tid % (D / 8)) * 8]) = f.k[j];
+  };
+
+  // O = 2^G Q S + P E of the chunk at t0, from registers alone; off the chain, it fills the wait for
+  // the next chunk's operands (bytes = 0: there is no chunk before the first)
+  f32x4 o[NT];
+  Frag ef[NT][2][2];
+  const auto readout = [&](int t0, bool some) {
+    const rsrc_t out = make_rsrc(op + t0 * rstep, some ? (min(sp_b.end - t0, kC) - 1) * ostep + NC * 2 : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f32x4 pe[2];
+      pe[0] = o[nt];
+      pe[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {   // (the right half of an upper row is zero)
+        pe[0] = mfma(f.p[0][x], ef[nt][0][x], pe[0]);
+        pe[1] = mfma(f.p[1][x], ef[nt][0][x], pe[1]);
+        pe[0] = mfma(f.p[0][x], ef[nt][1][x], pe[0]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(float_to_bf16_bits(pe[0][i] + pe[1][i])), out, off_val + i * ostep + 32 * nt, 0, 0);
+    }
+  };
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    o[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (x == 0 || w >= 2) f.p[p][x] = load_frag(ws + p * kPlane + x * 64);
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint16_t* p = kp + min(t0 + 32 * x + 8 * g + j, sp_b.end - 1) * rstep + own + MD * r;
-        f.kt[x][j] = MD == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
-      }
-  };
-  const auto load_gates = [&](int t0) {
-    const float* sc = reinterpret_cast<const float*>(unit_ws(t0) + 5 * kPlane);
-    f.eg = *reinterpret_cast<const float4*>(sc + 16 * w + 4 * g);
-    f.wc = *reinterpret_cast<const float4*>(sc + kC + 16 * w + 4 * g);
-    f.last = sc[kC - 1];
-  };
+      for (int x = 0; x < 2; ++x) ef[nt][p][x] = Frag{{0, 0, 0, 0}};
+  }
 
-  load_kqv(sp_b.begin);
+  load_k(sp_b.begin);
+  load_v(sp_b.begin);
+  load_p(sp_b.begin);
+  load_q(sp_b.begin);
   load_x(sp_b.begin);
-  load_rest(sp_b.begin);
-  load_gates(sp_b.begin);
   share_state();
+  store_k(0);
   __syncthreads();
-  for (int t0 = sp_b.begin; t0 < sp_b.end; t0 += kC) {
-    const bool more = sp_b.end - t0 > kC;
-    const float eg[4] = {f.eg.x, f.eg.y, f.eg.z, f.eg.w}, wc[4] = {f.wc.x, f.wc.y, f.wc.z, f.wc.w};
-    const float last = f.last;
-    // K S and Q S; R = V - 2^G K S
-    f32x4 ks[NT], o[NT];
+  int cur = 0;
+  for (int t0 = sp_b.begin; t0 < sp_b.end; t0 += kC, cur ^= 1) {
+    const int tn = sp_b.end - t0 > kC ? t0 + kC : t0;   // the chunk to load next
+    // K S; R = V - 2^G K S
+    Frag kf[KS], s[NT][2][KS];
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      kf[x] = load_frag(&kb[cur][16 * w + r][x * 32 + g * 8]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) s[nt][p][x] = load_frag(&sp[p][16 * nt + r][x * 32 + g * 8]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_k(tn);
+    readout(t0 - kC, t0 > sp_b.begin);
+    load_p(t0);
+    __builtin_amdgcn_sched_barrier(0);
+    const float wc[4] = {f.wc[0], f.wc[1], f.wc[2], f.wc[3]}, last = f.last;
+    float eg[4] = {f.eg[0], f.eg[1], f.eg[2], f.eg[3]};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      ks[nt] = o[nt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 ks[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) ks[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int x = 0; x < KS; ++x)
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const Frag s = load_frag(&sp[p][16 * nt + r][x * 32 + g * 8]);
-          ks[nt] = mfma(f.k[x], s, ks[nt]);
-          if (p < 2) o[nt] = mfma(f.q[x], s, o[nt]);
-        }
+        for (int p = 0; p < 2; ++p) ks[p] = mfma(kf[x], s[nt][p][x], ks[p]);
       float rr[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        rr[i] = fmaf(-eg[i], ks[nt][i], __uint_as_float(uint32_t(vv[nt][i]) << 16));
-        o[nt][i] *= eg[i];
-      }
+      for (int i = 0; i < 4; ++i) rr[i] = fmaf(-eg[i], ks[0][i] + ks[1][i], __uint_as_float(uint32_t(vv[nt][i]) << 16));
       uint32_t u0[3], u1[3];
       split_bf16<3>(rr[0], rr[1], u0);
       split_bf16<3>(rr[2], rr[3], u1);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(&rp[p][16 * nt + r][16 * w + 4 * g]) = make_uint2(u0[p], u1[p]);
     }
-    if (more) load_kqv(t0 + kC);
+    load_v(tn);
     __syncthreads();
-    // E = X diag(b) R
+    // E = X diag(b) R; Q S while R comes
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f32x4 e{0.0f, 0.0f, 0.0f, 0.0f};
+      Frag rf[3][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (x == 1 && w < 2) continue;   // X is lower triangular
+      for (int j = 0; j < 3; ++j)
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const Frag rf = load_frag(&rp[j][16 * nt + r][x * 32 + g * 8]);
+        for (int x = 0; x < 2; ++x) rf[j][x] = load_frag(&rp[j][16 * nt + r][x * 32 + g * 8]);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 qs[2];
 #pragma unroll
-          for (int i = 0; i + j < 3; ++i) e = mfma(f.x[i][x], rf, e);
-        }
-      }
+      for (int p = 0; p < 2; ++p) qs[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) qs[p] = mfma(f.q[x], s[nt][p][x], qs[p]);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 ex[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) ex[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < 2; ++x)        // (the right half of an upper row of X is zero)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int j = 0; i + j < 3; ++j) ex[j] = mfma(f.x[i][x], rf[j][x], ex[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[nt][i] = eg[i] * (qs[0][i] + qs[1][i]);
+      const f32x4 e = ex[0] + (ex[1] + ex[2]);
       uint32_t u0[3], u1[3];
-      split_bf16<2>(e[0], e[1], u0);
-      split_bf16<2>(e[2], e[3], u1);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) *reinterpret_cast<uint2*>(&ep[p][16 * nt + r][16 * w + 4 * g]) = make_uint2(u0[p], u1[p]);
       split_bf16<3>(e[0] * wc[0], e[1] * wc[1], u0);
       split_bf16<3>(e[2] * wc[2], e[3] * wc[3], u1);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(&wp[p][16 * nt + r][16 * w + 4 * g]) = make_uint2(u0[p], u1[p]);
+      split_bf16<2>(e[0], e[1], u0);
+      split_bf16<2>(e[2], e[3], u1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) *reinterpret_cast<uint2*>(&ep[p][16 * nt + r][16 * w + 4 * g]) = make_uint2(u0[p], u1[p]);
     }
-    if (more) load_x(t0 + kC);
+    Frag kt[2][MD];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int m = 0; m < MD; ++m) {
+        const uint16_t* from = &kb[cur][32 * x + 8 * g + r / 4][own + 16 * m + 4 * (r % 4)];
+        kt[x][m] = load_frag_t(from, from + 4 * LS);
+      }
+    load_q(tn);
     __syncthreads();
-    // S = 2^G_C S + K^T (2^(G_C - G) E) first: the next chunk waits for it
+    // S = 2^G_C S + K^T (2^(G_C - G) E)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      Frag wf[3][2];
 #pragma unroll
-      for (int m = 0; m < MD; ++m) S[m][nt] *= last;
+      for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        Frag kt[MD];
+        for (int x = 0; x < 2; ++x) wf[p][x] = load_frag(&wp[p][16 * nt + r][x * 32 + g * 8]);
 #pragma unroll
-        for (int m = 0; m < MD; ++m)
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            kt[m].w[j] = __builtin_amdgcn_perm(f.kt[x][2 * j + 1], f.kt[x][2 * j], m ? 0x07060302u : 0x05040100u);
+        for (int x = 0; x < 2; ++x) ef[nt][p][x] = load_frag(&ep[p][16 * nt + r][x * 32 + g * 8]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (nt == 0) load_x(tn);
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const Frag ef = load_frag(&wp[p][16 * nt + r][x * 32 + g * 8]);
+      for (int m = 0; m < MD; ++m) {
+        f32x4 add[3];
+        add[0] = S[m][nt] * last;
+        add[1] = add[2] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int m = 0; m < MD; ++m) S[m][nt] = mfma(kt[m], ef, S[m][nt]);
-        }
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int p = 0; p < 3; ++p) add[p] = mfma(kt[x][m], wf[p][x], add[p]);
+        S[m][nt] = add[0] + (add[1] + add[2]);
       }
     }
     share_state();
-    // O = 2^G Q S + P E
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (x == 1 && w < 2) continue;
-        const Frag e0 = load_frag(&ep[0][16 * nt + r][x * 32 + g * 8]), e1 = load_frag(&ep[1][16 * nt + r][x * 32 + g * 8]);
-        o[nt] = mfma(f.p[0][x], e0, o[nt]);
-        o[nt] = mfma(f.p[1][x], e0, o[nt]);
-        o[nt] = mfma(f.p[0][x], e1, o[nt]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 16 * w + 4 * g + i;
-        if (t < sp_b.end) op[t * rstep + 16 * nt + r] = float_to_bf16_bits(o[nt][i]);
-      }
-    }
-    if (more) {
-      load_rest(t0 + kC);
-      load_gates(t0 + kC);
-    }
+    store_k(cur ^ 1);
     __syncthreads();
   }
+  readout(sp_b.begin + (sp_b.end - sp_b.begin - 1) / kC * kC, true);
 #pragma unroll
   for (int m = 0; m < MD; ++m)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pool[(MD * i + m) * D + 16 * nt] = S[m][nt][i];
+      for (int i = 0; i < 4; ++i) pool[(16 * m + i) * D + 16 * nt] = S[m][nt][i];
 }
 
 // ---- linear attention ------------------------------------------------------------------------
@@ -467,15 +550,15 @@ struct Segments {
 };
 
 template <int D, int DECAY, int MODE>
-__global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, const Segments sg) {
+__global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a, const Segments sg) {
   constexpr int KS = D / 32, MD = D / 64, XT = D / 16, LK = D + 8;
   constexpr bool kReadout = MODE != LIN_STATES;
-  __shared__ __align__(16) uint16_t qs[kReadout ? kC : 1][LK], ks[kReadout ? kC : 1][LK];
-  __shared__ __align__(16) uint16_t kt[D][kLd];
+  __shared__ __align__(16) uint16_t ks[kC][LK];
+  __shared__ __align__(16) uint16_t qs[kReadout ? kC : 1][LK];
   __shared__ __align__(16) uint16_t pp[2][kReadout ? kC : 1][kLd];
-  __shared__ Logs logs[2][kC];
-  __shared__ __align__(16) float eg[2][kC], wc[2][kC];
-  __shared__ double ends[2];
+  __shared__ Logs logs[4][kC];                    // of four chunks
+  __shared__ __align__(16) float eg[4][kC], wc[4][kC];
+  __shared__ double ends[4];
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -498,11 +581,12 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
   const int64_t slot = a.slot_idx[b];
   if (!slot_in_pool(slot, a.num_slots)) return;
   const int64_t rstep = int64_t(a.H) * D;
+  const uint32_t ostep = static_cast<uint32_t>(rstep) * 2;
   const uint16_t* kp = static_cast<const uint16_t*>(a.k) + int64_t(head) * D;
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(head) * D;
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D;
+  uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D;
   const int col = (D / 4) * w + MD * r;           // this lane's first value column
-  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D + col;
-  uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D + col;
   float* pool = a.pool + ((slot * a.H + head) * D) * int64_t(D) + col;
   float* states = MODE == LIN_WHOLE ? nullptr : sg.states + int64_t(unit) * D * D + col;
 
@@ -517,88 +601,76 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
         for (int i = 0; i < 4; ++i) S[x][m][i] = from ? from[(16 * x + 4 * g + i) * D + m] : 0.0f;
   }
 
-  // one chunk's rows, in registers until LDS is free for them: rows past the end are zero
-  constexpr int RW = D / 32;                      // 16-byte pieces of K (and of Q) per thread
-  uint4 kr[RW], qr[RW];
-  uint32_t tr[2][8], vr[2][8];                    // K by columns (64 channel groups x 8 token octets), V
+  // One chunk's rows, in registers until LDS is free for them, through buffer resources that end
+  // with the segment's last row (rows past it read as 0 and are not stored).
+  constexpr int kRows = 256 / (D / 8);            // rows of K that a thread's pieces are apart
+  const uint32_t off_k = (tid / (D / 8)) * ostep + (tid % (D / 8)) * 16;
+  const uint32_t off_v = 8 * g * ostep + col * 2;
+  Frag kr[KS], qr[KS];
+  uint32_t vr[2][8];                              // values of tokens 32 x + 8 g + j, columns col ..
+  const auto rows = [&](const uint16_t* p, int t0) {
+    return make_rsrc(p + t0 * rstep, (min(t_end - t0, kC) - 1) * ostep + D * 2);
+  };
   const auto load_rows = [&](int t0) {
+    const rsrc_t rk = rows(kp, t0), rq = rows(qp, t0);
 #pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      const int x = tid + 256 * j, t = t0 + x / (D / 8), c = x % (D / 8);
+    for (int j = 0; j < KS; ++j) {
+      const auto k4 = __builtin_amdgcn_raw_buffer_load_b128(rk, off_k + j * kRows * ostep, 0, 0);
+      kr[j] = Frag{{k4[0], k4[1], k4[2], k4[3]}};
       if constexpr (kReadout) {
-        const bool live = t < t_end;
-        const int64_t at = min(t, t_end - 1) * rstep + c * 8;
-        kr[j] = *reinterpret_cast<const uint4*>(kp + at);
-        qr[j] = *reinterpret_cast<const uint4*>(qp + at);
-        if (!live) kr[j] = qr[j] = make_uint4(0, 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int x = tid + 256 * j, c = x % 64, o = x / 64;   // channels MD c .., tokens 8 o ..
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = t0 + 8 * o + i;
-        const uint16_t* p = kp + min(t, t_end - 1) * rstep + MD * c;
-        tr[j][i] = MD == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
-        if (t >= t_end) tr[j][i] = 0;
+        const auto q4 = __builtin_amdgcn_raw_buffer_load_b128(rq, off_k + j * kRows * ostep, 0, 0);
+        qr[j] = Frag{{q4[0], q4[1], q4[2], q4[3]}};
       }
     }
   };
+  const auto store_rows = [&]() {
+#pragma unroll
+    for (int j = 0; j < KS; ++j) {
+      const int t = tid / (D / 8) + j * kRows, c = (tid % (D / 8)) * 8;
+      *reinterpret_cast<uint4*>(&ks[t][c]) = make_uint4(kr[j].w[0], kr[j].w[1], kr[j].w[2], kr[j].w[3]);
+      if constexpr (kReadout) *reinterpret_cast<uint4*>(&qs[t][c]) = make_uint4(qr[j].w[0], qr[j].w[1], qr[j].w[2], qr[j].w[3]);
+    }
+  };
   const auto load_v = [&](int t0) {
+    const rsrc_t rv = rows(vp, t0);
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int t = t0 + 32 * x + 8 * g + j;
-        const uint16_t* p = vp + min(t, t_end - 1) * rstep;
-        vr[x][j] = MD == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
-        if (t >= t_end) vr[x][j] = 0;
+        const uint32_t off = off_v + (32 * x + j) * ostep;
+        vr[x][j] = MD == 2 ? __builtin_amdgcn_raw_buffer_load_b32(rv, off, 0, 0) : __builtin_amdgcn_raw_buffer_load_b16(rv, off, 0, 0);
       }
-  };
-  const auto store_logs = [&](int t0, int to) {   // by one wave, a chunk ahead
-    const double gs = chunk_logs<DECAY>(a, t0, min(kC, t_end - t0), head, lane);
-    const double end = __shfl(gs, 63);
-    logs[to][lane] = split_logs(gs);
-    eg[to][lane] = pow2(static_cast<float>(gs));
-    wc[to][lane] = pow2(static_cast<float>(end - gs));
-    if (lane == 0) ends[to] = end;
   };
 
   double total = 0.0;
   load_rows(t_begin);
   load_v(t_begin);
-  if (w == 0) store_logs(t_begin, 0);
   int at = 0;
-  for (int t0 = t_begin; t0 < t_end; t0 += kC, at ^= 1) {
-    const bool more = t_end - t0 > kC;
-    if constexpr (kReadout) {
-#pragma unroll
-      for (int j = 0; j < RW; ++j) {
-        const int x = tid + 256 * j;
-        *reinterpret_cast<uint4*>(&ks[x / (D / 8)][(x % (D / 8)) * 8]) = kr[j];
-        *reinterpret_cast<uint4*>(&qs[x / (D / 8)][(x % (D / 8)) * 8]) = qr[j];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int x = tid + 256 * j, c = x % 64, o = x / 64;
-#pragma unroll
-      for (int m = 0; m < MD; ++m) {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = __builtin_amdgcn_perm(tr[j][2 * i + 1], tr[j][2 * i], m ? 0x07060302u : 0x05040100u);
-        *reinterpret_cast<uint4*>(&kt[MD * c + m][8 * o]) = make_uint4(u[0], u[1], u[2], u[3]);
-      }
+  for (int t0 = t_begin; t0 < t_end; t0 += kC, at = (at + 1) & 3) {
+    const int tn = t_end - t0 > kC ? t0 + kC : t0;   // the chunk to load next
+    store_rows();
+    if (at == 0) {   // the decays of this chunk and the next three, one a wave
+      const int tw = min(t0 + kC * w, t_end);
+      const double gs = chunk_logs<DECAY>(a, tw, min(kC, t_end - tw), head, lane);
+      const double end = __shfl(gs, 63);
+      logs[w][lane] = split_logs(gs);
+      eg[w][lane] = pow2(static_cast<float>(gs));
+      wc[w][lane] = pow2(static_cast<float>(end - gs));
+      if (lane == 0) ends[w] = end;
     }
     __syncthreads();
-    if (more) load_rows(t0 + kC);
+    load_rows(tn);
+    f32x4 o[kReadout ? 4 : 1][MD];
     if constexpr (kReadout) {
       Frag qf[KS];
 #pragma unroll
       for (int x = 0; x < KS; ++x) qf[x] = load_frag(&qs[16 * w + r][x * 32 + g * 8]);
+      Logs lt[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lt[i] = logs[at][16 * w + 4 * g + i];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
+        if ((c | 1) > (w | 1)) continue;          // above the diagonal: no product reads these
         f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
         const int s = 16 * c + r;
         if (c <= w) {
@@ -606,12 +678,8 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
           for (int x = 0; x < KS; ++x) p = mfma(qf[x], load_frag(&ks[s][x * 32 + g * 8]), p);
           const Logs ls = logs[at][s];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = 16 * w + 4 * g + i;
-            p[i] = s <= t ? p[i] * decay_between(logs[at][t], ls) : 0.0f;
-          }
+          for (int i = 0; i < 4; ++i) p[i] = s <= 16 * w + 4 * g + i ? p[i] * decay_between(lt[i], ls) : 0.0f;
         }
-        if ((c | 1) > (w | 1)) continue;          // no product reads these
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           uint32_t u[2];
@@ -623,8 +691,6 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
           }
         }
       }
-      __syncthreads();
-      f32x4 o[4][MD];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
@@ -645,10 +711,9 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
         for (int rt = 0; rt < 4; ++rt) {
           const Frag q = load_frag2(&qs[16 * rt + r][x * 32 + g * 4], &qs[16 * rt + r][x * 32 + 16 + g * 4]);
 #pragma unroll
-          for (int m = 0; m < MD; ++m) {
-            o[rt][m] = mfma(q, sf[0][m], o[rt][m]);
-            o[rt][m] = mfma(q, sf[1][m], o[rt][m]);
-          }
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int m = 0; m < MD; ++m) o[rt][m] = mfma(q, sf[p][m], o[rt][m]);
         }
       }
 #pragma unroll
@@ -659,6 +724,8 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
           o[rt][m][0] *= e.x; o[rt][m][1] *= e.y; o[rt][m][2] *= e.z; o[rt][m][3] *= e.w;
         }
       }
+      __syncthreads();
+      const rsrc_t out = rows(op, t0);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         Frag vf[MD];
@@ -680,11 +747,9 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = t0 + 16 * rt + 4 * g + i;
-          if (t < t_end) {
-            if constexpr (MD == 2) *reinterpret_cast<uint32_t*>(op + t * rstep) = pack_bf16(o[rt][0][i], o[rt][1][i]);
-            else op[t * rstep] = float_to_bf16_bits(o[rt][0][i]);
-          }
+          const uint32_t off = (16 * rt + 4 * g + i) * ostep + col * 2;
+          if constexpr (MD == 2) __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(o[rt][0][i], o[rt][1][i]), out, off, 0, 0);
+          else __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(float_to_bf16_bits(o[rt][0][i])), out, off, 0, 0);
         }
     }
     // S = 2^G_C S + K^T (2^(G_C - G) V)
@@ -711,17 +776,15 @@ __global__ __launch_bounds__(256) void linear_chunk_kernel(const PromptArgs a, c
         }
 #pragma unroll
       for (int y = 0; y < XT; ++y) {
-        const Frag kf = load_frag(&kt[16 * y + r][x * 32 + g * 8]);
+        const uint16_t* from = &ks[32 * x + 8 * g + r / 4][16 * y + 4 * (r % 4)];
+        const Frag kf = load_frag_t(from, from + 4 * LK);
 #pragma unroll
         for (int p = 0; p < 3; ++p)
 #pragma unroll
           for (int m = 0; m < MD; ++m) S[y][m] = mfma(kf, vf[p][m], S[y][m]);
       }
     }
-    if (more) {
-      load_v(t0 + kC);
-      if (w == 0) store_logs(t0 + kC, at ^ 1);
-    }
+    load_v(tn);
     __syncthreads();
   }
   float* to = MODE == LIN_STATES ? states : final ? pool : nullptr;
@@ -801,7 +864,13 @@ hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
   const unsigned chunks = static_cast<unsigned>(a.T / kC + a.B) * static_cast<unsigned>(a.H);
   hipLaunchKernelGGL((delta_chunk_kernel<D>), dim3(chunks), dim3(256), 0, s, a);
   const unsigned units = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H);
-  hipLaunchKernelGGL((delta_chain_kernel<D, 1>), dim3(units * (D / 16)), dim3(256), 0, s, a);
+  // 32 columns a workgroup read K, Q, X and P half as often, 16 give twice the workgroups. On one
+  // MI355X, d = 128, 32 heads, 8,192 tokens in all: 64 heads' states and more 267-361 us with 32
+  // columns against 329-446 us with 16; 32 states (one prompt) 448 us against 345 us.
+  if (units * (D / 32) >= 256)
+    hipLaunchKernelGGL((delta_chain_kernel<D, 2>), dim3(units * (D / 32)), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((delta_chain_kernel<D, 1>), dim3(units * (D / 16)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
