@@ -43,6 +43,21 @@ __device__ __forceinline__ Piece piece_of(const PromptArgs& a, int i, int len) {
   return Piece{lo, static_cast<int>(t0), min(len, static_cast<int>(sp.end - t0))};
 }
 
+// Segments: numbered likewise by the most tokens one may hold, but a request's are of even length (a
+// multiple of 64).
+__device__ __forceinline__ int even_len(int tokens, int most) {
+  const int n = (tokens + most - 1) / most;
+  return ((tokens + n - 1) / n + kC - 1) / kC * kC;
+}
+
+__device__ __forceinline__ Piece segment_of(const PromptArgs& a, int i, int most) {
+  const Piece pc = piece_of(a, i, most);
+  if (pc.n <= 0) return pc;
+  const Span sp = span_of(a, pc.b);
+  const int len = even_len(sp.end - sp.begin, most), t0 = sp.begin + (pc.t0 - sp.begin) / most * len;
+  return Piece{pc.b, t0, max(0, min(len, sp.end - t0))};
+}
+
 // One lane's running sum of log2 decays over a chunk (lane = token; tokens past n add nothing).
 template <int DECAY>
 __device__ __forceinline__ double chunk_logs(const PromptArgs& a, int t0, int n, int head, int lane) {
@@ -60,7 +75,10 @@ __device__ __forceinline__ Logs split_logs(double g) {
   return Logs{hi, static_cast<float>(g - hi)};
 }
 
-__device__ __forceinline__ float decay_between(Logs t, Logs s) { return pow2((t.hi - s.hi) + (t.lo - s.lo)); }
+// 2^(G_t - G_s) where `live`, else 0, without a branch.
+__device__ __forceinline__ float decay_between(Logs t, Logs s, bool live) {
+  return pow2(live ? (t.hi - s.hi) + (t.lo - s.lo) : -4000.0f);
+}
 
 // ---- the delta rule: what a chunk's keys and gates give -------------------------------------
 // Workspace of one chunk and head: X diag(b) in three bf16 pieces and P in two, [64][64] each (the
@@ -142,9 +160,9 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 16 * w + 4 * g + i;
-      const float f = decay_between(logs[t], ls);
-      kk[c][i] = s < t ? beta[t] * f * kk[c][i] : 0.0f;
-      qk[c][i] = s <= t ? f * qk[c][i] : 0.0f;
+      const float f = decay_between(logs[t], ls, s <= t);
+      kk[c][i] *= s == t ? 0.0f : beta[t] * f;
+      qk[c][i] *= f;
     }
   }
 #pragma unroll
@@ -544,7 +562,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
 enum LinearMode : int { LIN_WHOLE = 0, LIN_STATES = 1, LIN_SEGMENTS = 2 };
 
 struct Segments {
-  int len;          // tokens per segment, a multiple of 64; whole prompts: larger than any
+  int len;          // most tokens per segment, a multiple of 64; 0: whole prompts
   float* states;    // [segment number][H][D][D]: own states, then the states before
   float* decays;    // [segment number][H]: log2 of a segment's decay
 };
@@ -570,7 +588,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
     t_begin = sp.begin;
     t_end = sp.end;
   } else {
-    const Piece pc = piece_of(a, seg, sg.len);
+    const Piece pc = segment_of(a, seg, sg.len);
     b = pc.b;
     t_begin = pc.t0;
     t_end = pc.t0 + pc.n;
@@ -587,18 +605,22 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D;
   uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D;
   const int col = (D / 4) * w + MD * r;           // this lane's first value column
-  float* pool = a.pool + ((slot * a.H + head) * D) * int64_t(D) + col;
-  float* states = MODE == LIN_WHOLE ? nullptr : sg.states + int64_t(unit) * D * D + col;
+  float* pool = a.pool + (slot * a.H + head) * int64_t(D * D);
+  float* states = MODE == LIN_WHOLE ? nullptr : sg.states + int64_t(unit) * (D * D);
+  const uint32_t off_state = (4 * g * D + col) * 4;
 
   f32x4 S[XT][MD];   // S[x][m][i]: key channel 16 x + 4 g + i, value column col + m
   {
-    const float* from = MODE == LIN_SEGMENTS ? states : MODE == LIN_WHOLE && a.resume && a.resume[b] != 0 ? pool : nullptr;
+    // (a resource of no bytes reads as 0)
+    const bool some = MODE == LIN_SEGMENTS || (MODE == LIN_WHOLE && a.resume && a.resume[b] != 0);
+    const rsrc_t from = make_rsrc(MODE == LIN_SEGMENTS ? states : pool, some ? D * D * 4 : 0);
 #pragma unroll
     for (int x = 0; x < XT; ++x)
 #pragma unroll
       for (int m = 0; m < MD; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[x][m][i] = from ? from[(16 * x + 4 * g + i) * D + m] : 0.0f;
+        for (int i = 0; i < 4; ++i)
+          S[x][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, off_state + 4 * m, (16 * x + i) * D * 4, 0));
   }
 
   // One chunk's rows, in registers until LDS is free for them, through buffer resources that end
@@ -642,7 +664,20 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
       }
   };
 
+  if constexpr (kReadout) {   // the tiles above the diagonal that a product reads
+    for (int x = tid; x < 2 * 2 * 16 * 2; x += 256) {
+      const int row = (x >> 1 & 15) + 32 * (x >> 5 & 1);
+      *reinterpret_cast<uint4*>(&pp[x >> 6][row][16 + (row & 32) + 8 * (x & 1)]) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  float ahead;   // this lane's decay of the wave's chunk among the next four (1 past the end)
+  const auto load_decays = [&](int t0) {
+    const int t = t0 + kC * w + lane;
+    ahead = a.alpha[DECAY == DECAY_HEAD ? head : (int64_t(min(t, t_end - 1)) * a.H + head)];
+    if (t >= t_end) ahead = 1.0f;
+  };
   double total = 0.0;
+  load_decays(t_begin);
   load_rows(t_begin);
   load_v(t_begin);
   int at = 0;
@@ -650,8 +685,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
     const int tn = t_end - t0 > kC ? t0 + kC : t0;   // the chunk to load next
     store_rows();
     if (at == 0) {   // the decays of this chunk and the next three, one a wave
-      const int tw = min(t0 + kC * w, t_end);
-      const double gs = chunk_logs<DECAY>(a, tw, min(kC, t_end - tw), head, lane);
+      const double gs = wave_scan(static_cast<double>(log2_decay(ahead)), lane);
       const double end = __shfl(gs, 63);
       logs[w][lane] = split_logs(gs);
       eg[w][lane] = pow2(static_cast<float>(gs));
@@ -660,34 +694,30 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
     }
     __syncthreads();
     load_rows(tn);
+    if (at == 0) load_decays(t0 + 4 * kC);
     f32x4 o[kReadout ? 4 : 1][MD];
     if constexpr (kReadout) {
-      Frag qf[KS];
+      // P: the 10 tiles on and below the diagonal, 2 or 3 a wave
+      const unsigned tiles = w == 0 ? 0xc0f : w == 1 ? 0x54d : w == 2 ? 0x98e : 0xaff;   // row, column: 2 bits each
 #pragma unroll
-      for (int x = 0; x < KS; ++x) qf[x] = load_frag(&qs[16 * w + r][x * 32 + g * 8]);
-      Logs lt[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lt[i] = logs[at][16 * w + 4 * g + i];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if ((c | 1) > (w | 1)) continue;          // above the diagonal: no product reads these
+      for (int j = 0; j < 3; ++j) {
+        const int rt = tiles >> (4 * (2 - j) + 2) & 3, c = tiles >> (4 * (2 - j)) & 3;
+        if (j == 2 && (w == 0 || w == 3)) break;
         f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
         const int s = 16 * c + r;
-        if (c <= w) {
 #pragma unroll
-          for (int x = 0; x < KS; ++x) p = mfma(qf[x], load_frag(&ks[s][x * 32 + g * 8]), p);
-          const Logs ls = logs[at][s];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[i] = s <= 16 * w + 4 * g + i ? p[i] * decay_between(lt[i], ls) : 0.0f;
-        }
+        for (int x = 0; x < KS; ++x)
+          p = mfma(load_frag(&qs[16 * rt + r][x * 32 + g * 8]), load_frag(&ks[s][x * 32 + g * 8]), p);
+        const Logs ls = logs[at][s];
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
+          const int t = 16 * rt + 4 * g + i;
           uint32_t u[2];
-          split_bf16<2>(p[i], p[i + 1], u);
+          split_bf16<2>(p[i] * decay_between(logs[at][t], ls, s <= t), p[i + 1] * decay_between(logs[at][t + 1], ls, s <= t + 1), u);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            pp[x][16 * w + 4 * g + i][s] = static_cast<uint16_t>(u[x]);
-            pp[x][16 * w + 4 * g + i + 1][s] = static_cast<uint16_t>(u[x] >> 16);
+            pp[x][t][s] = static_cast<uint16_t>(u[x]);
+            pp[x][t + 1][s] = static_cast<uint16_t>(u[x] >> 16);
           }
         }
       }
@@ -695,26 +725,40 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
         for (int m = 0; m < MD; ++m) o[rt][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        Frag sf[2][MD];
+      Frag sf[2][2][MD];
+      const auto split_state = [&](int x) {
 #pragma unroll
         for (int m = 0; m < MD; ++m)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t u[2];
             split_bf16<2>(S[2 * x + j / 2][m][2 * (j & 1)], S[2 * x + j / 2][m][2 * (j & 1) + 1], u);
-            sf[0][m].w[j] = u[0];
-            sf[1][m].w[j] = u[1];
+            sf[x & 1][0][m].w[j] = u[0];
+            sf[x & 1][1][m].w[j] = u[1];
           }
+      };
+      split_state(0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const Frag q = load_frag2(&qs[16 * rt + r][x * 32 + g * 4], &qs[16 * rt + r][x * 32 + 16 + g * 4]);
+      for (int x = 0; x < KS; ++x) {
+        if (x + 1 < KS) split_state(x + 1);   // the next pieces between this step's products
+        Frag q[4];
 #pragma unroll
-          for (int p = 0; p < 2; ++p)
+        for (int rt = 0; rt < 4; ++rt) q[rt] = load_frag2(&qs[16 * rt + r][x * 32 + g * 4], &qs[16 * rt + r][x * 32 + 16 + g * 4]);
+        // (a product that continues a sum comes 4 MD products after the last of that sum)
 #pragma unroll
-            for (int m = 0; m < MD; ++m) o[rt][m] = mfma(q, sf[p][m], o[rt][m]);
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int m = 0; m < MD; ++m) o[rt][m] = mfma(q[rt], sf[x & 1][p][m], o[rt][m]);
+#pragma unroll
+        for (int j = 0; j < 8 * MD; ++j) {
+          if (j == 0) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+          __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x2, 3, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
@@ -726,6 +770,8 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
       }
       __syncthreads();
       const rsrc_t out = rows(op, t0);
+      uint32_t step = ostep;
+      asm volatile("" : "+s"(step));   // (offsets formed here, not held in registers over the loop)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         Frag vf[MD];
@@ -747,7 +793,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t off = (16 * rt + 4 * g + i) * ostep + col * 2;
+          const uint32_t off = (16 * rt + 4 * g + i) * step + col * 2;
           if constexpr (MD == 2) __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(o[rt][0][i], o[rt][1][i]), out, off, 0, 0);
           else __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(float_to_bf16_bits(o[rt][0][i])), out, off, 0, 0);
         }
@@ -775,26 +821,33 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
           for (int p = 0; p < 3; ++p) vf[p][m].w[j] = u[p];
         }
 #pragma unroll
-      for (int y = 0; y < XT; ++y) {
-        const uint16_t* from = &ks[32 * x + 8 * g + r / 4][16 * y + 4 * (r % 4)];
-        const Frag kf = load_frag_t(from, from + 4 * LK);
+      for (int y = 0; y < XT; y += 2) {
+        Frag kf[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint16_t* from = &ks[32 * x + 8 * g + r / 4][16 * (y + h) + 4 * (r % 4)];
+          kf[h] = load_frag_t(from, from + 4 * LK);
+        }
 #pragma unroll
         for (int p = 0; p < 3; ++p)
 #pragma unroll
-          for (int m = 0; m < MD; ++m) S[y][m] = mfma(kf, vf[p][m], S[y][m]);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MD; ++m) S[y + h][m] = mfma(kf[h], vf[p][m], S[y + h][m]);
       }
     }
     load_v(tn);
     __syncthreads();
   }
-  float* to = MODE == LIN_STATES ? states : final ? pool : nullptr;
-  if (to) {
+  if (MODE == LIN_STATES || final) {
+    const rsrc_t to = make_rsrc(MODE == LIN_STATES ? states : pool, D * D * 4);
 #pragma unroll
     for (int x = 0; x < XT; ++x)
 #pragma unroll
       for (int m = 0; m < MD; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[(16 * x + 4 * g + i) * D + m] = S[x][m][i];
+        for (int i = 0; i < 4; ++i)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[x][m][i]), to, off_state + 4 * m, (16 * x + i) * D * 4, 0);
   }
   if (MODE == LIN_STATES && tid == 0) sg.decays[unit] = static_cast<float>(total);
 }
@@ -829,8 +882,8 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const PromptArgs a, co
 
 // Segments of a call: none (whole prompts) where the prompts alone fill the chip.
 int segment_len(int32_t B, int32_t T, int32_t H) {
-  if (int64_t(B) * H >= 512 || T <= 4 * kC) return 0;
-  const int64_t want = (int64_t(T) * H + 1023) / 1024;
+  if (int64_t(B) * H >= 256 || T <= 4 * kC) return 0;
+  const int64_t want = (int64_t(T) * H + 511) / 512;
   return static_cast<int>(std::max<int64_t>((want + kC - 1) / kC * kC, 4 * kC));
 }
 
@@ -847,6 +900,7 @@ void linear_dd(const PromptArgs& a, hipStream_t s) {
   sg.decays = sg.states + units * D * D;
   const dim3 grid(static_cast<unsigned>(units));
   hipLaunchKernelGGL((linear_chunk_kernel<D, DECAY, LIN_STATES>), grid, dim3(256), 0, s, a, sg);
+  // (the scan goes by the numbers, so the segments' lengths do not matter to it)
   const int64_t threads = int64_t(a.B) * a.H * (D * D / 4);
   hipLaunchKernelGGL(linear_scan_kernel, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, s, a, sg, D * D / 4);
   hipLaunchKernelGGL((linear_chunk_kernel<D, DECAY, LIN_SEGMENTS>), grid, dim3(256), 0, s, a, sg);
