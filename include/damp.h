@@ -551,7 +551,7 @@ damp_status fp32_delta_prefill(float* pool, int32_t num_slots, int32_t num_heads
 /* ---------------------------------------------------------------------------------------
  * Paged key-value cache, for the full-attention layers between the recurrent ones: keys and values
  * in pages, bf16 [num_pages][num_kv_heads][page_size][d] each, d in {64, 128}, page_size a power of
- * two up to 32,768. Request b's token at position p lies in page block_table[b][p / page_size], row
+ * two up to 32,768, num_pages * num_kv_heads * page_size below 2^32 - 1. Request b's token at position p lies in page block_table[b][p / page_size], row
  * p mod page_size; its cache slot is page * page_size + row.
  * ------------------------------------------------------------------------------------- */
 

@@ -487,6 +487,8 @@ damp_status check_cache(int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_
     return fail(DAMP_ERR_UNSUPPORTED, "d = %d: the paged cache supports d in {64, 128}", d);
   if (page_log2(page_size) < 0)
     return fail(DAMP_ERR_UNSUPPORTED, "page_size %d is not a power of two in [1, 32768]", page_size);
+  if ((static_cast<int64_t>(num_pages) << page_log2(page_size)) > 0xfffffffeLL / Hkv)
+    return fail(DAMP_ERR_UNSUPPORTED, "num_pages * num_kv_heads * page_size must stay below 2^32 - 1");
   return DAMP_OK;
 }
 
@@ -1252,7 +1254,8 @@ damp_status kv_append(const void* k, const void* v, const int64_t* slot_map, int
 size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t num_kv_heads, int32_t d,
                                            int32_t max_len) {
   if (B <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || (d != 64 && d != 128) ||
-      max_len < 0 || max_len > (1 << 30))
+      max_len < 0 || max_len > (1 << 30) ||
+      damp::kv_attention_grid(B, num_q_heads, num_kv_heads, d, max_len) > 0x7fffffffLL)
     return 0;
   return damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);
 }
@@ -1275,7 +1278,7 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages, con
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_new, 16) ||
       !aligned(v_new, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages, k_new, v_new and out must be 16-byte, block_table and seq_lens 4-byte aligned");
-  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > 0x7fffffffLL ||
+  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, d, max_len) > 0x7fffffffLL ||
       static_cast<int64_t>(B) * num_q_heads > 0x7fffffffLL)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_len = %d exceeds the grid limit", B, max_len);
   const size_t need = damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);

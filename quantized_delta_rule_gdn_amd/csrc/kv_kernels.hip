@@ -124,9 +124,9 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const AppendArgs a) {
 
 // ---- attention of one new token ------------------------------------------------------------------
 // o = sum_t p_t v_t / sum_t p_t, p_t = exp(scale q.k_t - m), in one pass over the cache with a
-// running maximum m and sum. A request's tokens are cut into chunks, one workgroup per (request,
-// key-value head, 16 query heads, chunk), joined by a second kernel; each of the 4 waves takes
-// every fourth tile of 32 tokens and the waves meet in LDS at the end. It is bound by the stream
+// running maximum m and sum. A request's tokens are cut into items, one workgroup per (item,
+// key-value head, 16 query heads), joined by a second kernel; each of the 4 waves takes every
+// fourth tile of 32 tokens and the waves meet in LDS at the end. It is bound by the stream
 // of the cache's bytes (4 Hkv d per token): the matrix instructions serve up to 16 query heads of
 // one key-value head for the same bytes. Nothing is staged in LDS on the way:
 //   scores^T [token][head] = K Q^T: a lane's operand is 16 bytes of one token's key as stored;
@@ -139,76 +139,114 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const AppendArgs a) {
 // and the accumulators are binary32.
 constexpr int kAttnTile = 32;
 
+// The work is shared out on the device, by the requests' actual lengths: with `per_unit` workgroups
+// for each (key-value head, 16 query heads), an item is a run of at most
+// chunk = max(128, total tokens / per_unit) tokens of one request, so there are at most per_unit + B
+// items whatever the lengths, they are of much the same length, and those of full length fill the
+// chip once. (Cut by the longest length the host knows of instead, 64 requests of 128 to 8,192
+// tokens took 244-260 us against 186-197 us of as many bytes in even lengths.)
 struct AttnPlan {
-  int tiles;    // groups of 16 query heads per key-value head
-  int chunk;    // tokens per workgroup
-  int splits;   // chunks of the longest request
+  int tiles;      // groups of 16 query heads per key-value head
+  int heads;      // query heads of a full group
+  int per_unit;
+  int items;      // per_unit + B, or B where no request is cut
 };
 
-AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
+constexpr int kAttnLeast = 4 * kAttnTile;    // tokens: no item is shorter unless its request is
+
+AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len) {
   AttnPlan p;
   p.tiles = (Hq / Hkv + 15) / 16;
-  const int64_t units = int64_t(B) * Hkv * p.tiles;
-  p.chunk = 128;
-  while (p.chunk < 1024 && units * ((max_len + p.chunk - 1) / p.chunk) > 4096) p.chunk *= 2;
-  p.splits = (max_len + p.chunk - 1) / p.chunk;
-  if (p.splits < 1) p.splits = 1;
+  p.heads = std::min(Hq / Hkv, 16);
+  // workgroups that are resident at once: 4 a CU by registers and LDS at d = 128, 6 at d = 64
+  const int64_t units = int64_t(Hkv) * p.tiles, resident = 256 * (d == 128 ? 4 : 6);
+  const int64_t most = (int64_t(max_len) + kAttnLeast - 1) / kAttnLeast * B;   // no more are ever cut
+  p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(resident / units, 1), std::max<int64_t>(most, 1)));
+  p.items = max_len <= kAttnLeast ? B : p.per_unit + B;
   return p;
 }
 
-constexpr int kAttnMaxChunk = 1024;
+// Tokens of request b that are read.
+__device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
+  const int64_t cap = int64_t(a.max_blocks) << a.page_log2;
+  return static_cast<int>(min(int64_t(min(max(a.seq_lens[b], 0), a.max_len)), cap));
+}
 
-template <int D>
-__global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, const AttnPlan plan) {
+__device__ __forceinline__ int items_of(int len, int chunk) { return max((len + chunk - 1) / chunk, 1); }
+
+// Sums over the 256 threads of a workgroup (the same in every thread).
+__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  __syncthreads();
+  if ((__builtin_amdgcn_workitem_id_x() & 63) == 0) sh[__builtin_amdgcn_workitem_id_x() >> 6] = x;
+  __syncthreads();
+  return (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
+__device__ __forceinline__ int chunk_of(const AttnArgs& a, const AttnPlan& plan, int64_t* sh) {
+  int64_t total = 0;
+  for (int b = __builtin_amdgcn_workitem_id_x(); b < a.B; b += 256) total += length_of(a, b);
+  total = block_sum(total, sh);
+  const int64_t chunk = (total + plan.per_unit - 1) / plan.per_unit;
+  return static_cast<int>(max((chunk + kAttnLeast - 1) / kAttnLeast * kAttnLeast, int64_t(kAttnLeast)));
+}
+
+constexpr int kAttnPages = 1024;   // page addresses held in LDS at a time
+
+// P16: pages of 16 tokens or more, so that a half tile lies in one page and its address is the same
+// for the whole wave; smaller pages are looked up for every row.
+template <int D, bool P16>
+__global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, const AttnPlan plan) {
   constexpr int KS = D / 32;       // k steps of the score product
   constexpr int DPL = D / 16;      // value channels per lane
   constexpr int VW = DPL / 2;      // dwords of them
-  __shared__ int pages[kAttnMaxChunk + 1];
-  __shared__ int bad;
+  constexpr uint32_t kNone = 0xffffffffu;
+  __shared__ uint32_t first_row[kAttnPages];          // of a page, in rows of this key-value head
+  __shared__ int bad, found_b, found_s;
+  __shared__ int64_t sh[4];
+  __shared__ int wave_items[4];
   __shared__ float part_m[4][16], part_l[4][16];
   __shared__ __align__(16) float part_o[4][16][D + 4];
 
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  unsigned id = __builtin_amdgcn_workgroup_id_x();
-  const int split = id % plan.splits; id /= plan.splits;
-  const int tile = id % plan.tiles; id /= plan.tiles;
-  const int kvh = id % a.Hkv;
-  const int b = id / a.Hkv;
+  const unsigned id = __builtin_amdgcn_workgroup_id_x();
+  const int units = a.Hkv * plan.tiles;
+  const int item = id / units, unit = id % units, tile = unit % plan.tiles, kvh = unit / plan.tiles;
   const int G = a.Hq / a.Hkv;
-  const int whole = a.seq_lens[b];
-  const int64_t cap = int64_t(a.max_blocks) << a.page_log2;
-  const int len = static_cast<int>(min(int64_t(min(max(whole, 0), a.max_len)), cap));
-  const int begin = split * plan.chunk;
-  if (begin >= len && !(split == 0 && plan.splits == 1)) return;
-  const int end = min(begin + plan.chunk, len);
-  const int64_t page_rows = int64_t(1) << a.page_log2;
 
-  const int p0 = begin >> a.page_log2;
-  const int np = end > begin ? ((end - 1) >> a.page_log2) - p0 + 1 : 0;
-  if (tid == 0) bad = 0;
-  __syncthreads();
-  for (int i = tid; i < np; i += 256) {
-    const int pid = a.table[int64_t(b) * a.max_blocks + p0 + i];
-    const bool fine = pid >= 0 && pid < a.num_pages;
-    pages[i] = fine ? pid : -1;
-    if (!fine) bad = 1;
-  }
-  __syncthreads();
-  // this call's key and value go into the cache first; the workgroup then reads them from there
-  if (a.k_new && whole > 0 && whole == len && end == len && end > begin) {
-    const int pos = len - 1, pid = pages[(pos >> a.page_log2) - p0];
-    if (pid >= 0 && tid < D / 4) {
-      const int64_t row = (int64_t(pid) * a.Hkv + kvh) * page_rows + (pos & (page_rows - 1));
-      const int64_t from = int64_t(b) * a.Hkv + kvh;
-      const int piece = tid % (D / 8);
-      if (tid < D / 8) reinterpret_cast<uint4*>(a.k_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.k_new)[from * (D / 8) + piece];
-      else reinterpret_cast<uint4*>(a.v_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.v_new)[from * (D / 8) + piece];
+  // the request this item belongs to
+  const int chunk = chunk_of(a, plan, sh);
+  if (tid == 0) found_b = -1;
+  for (int b0 = 0, before = 0; b0 < a.B; b0 += 256) {
+    const int n = b0 + tid < a.B ? items_of(length_of(a, b0 + tid), chunk) : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(incl, o);
+      if (lane >= o) incl += y;
     }
+    if (lane == 63) wave_items[wv] = incl;
     __syncthreads();
+    int first = before + incl - n;
+    for (int i = 0; i < wv; ++i) first += wave_items[i];
+    if (item >= first && item < first + n) {
+      found_b = b0 + tid;
+      found_s = item - first;
+    }
+    before += (wave_items[0] + wave_items[1]) + (wave_items[2] + wave_items[3]);
+    __syncthreads();
+    if (before > item) break;
   }
-  const bool clean = bad == 0;
+  const int b = __builtin_amdgcn_readfirstlane(found_b), split = __builtin_amdgcn_readfirstlane(found_s);
+  if (b < 0) return;
+  const int whole = a.seq_lens[b], len = length_of(a, b), splits = items_of(len, chunk);
+  // its tokens: an even share of the request's, in whole tiles
+  const int share = ((len + splits - 1) / splits + kAttnTile - 1) / kAttnTile * kAttnTile;
+  const int begin = min(split * share, len), end = min(begin + share, len);
+  const int in_page = (1 << a.page_log2) - 1;
 
   const int head0 = tile * 16, heads = min(16, G - head0);
   Frag qf[KS];
@@ -217,32 +255,48 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, con
 #pragma unroll
     for (int x = 0; x < KS; ++x) qf[x] = load_frag(qp + x * 64);
   }
-  const auto row_of = [&](int pos) -> int64_t {   // cache row of a position, -1 where there is none
-    const int pid = pages[(pos >> a.page_log2) - p0];
-    return pid < 0 ? -1 : (int64_t(pid) * a.Hkv + kvh) * page_rows + (pos & (page_rows - 1));
-  };
 
   f32x4 o[DPL];
 #pragma unroll
   for (int m = 0; m < DPL; ++m) o[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   float mx = -INFINITY, sum = 0.0f;
-  for (int t0 = begin + wv * kAttnTile; t0 < end; t0 += 4 * kAttnTile) {
-    // (positions past the end read the last row; what they give is masked)
+  const uint32_t k_off = r * (D * 2) + g * 16;                  // a half tile's K rows as operands
+  const uint32_t v_off = 4 * g * (D * 2) + r * (DPL * 2);       // and its V rows
+  // page addresses for as many tokens at a time as LDS holds (4 tiles at least)
+  constexpr int kRun = P16 ? kAttnPages * 16 : kAttnPages;
+  for (int from = begin; from < end; from += kRun) {
+  const int to = min(from + kRun, end);
+  const int p0 = from >> a.page_log2, np = ((to - 1) >> a.page_log2) - p0 + 1;
+  __syncthreads();
+  if (tid == 0) bad = 0;
+  __syncthreads();
+  for (int i = tid; i < np; i += 256) {
+    const int pid = a.table[int64_t(b) * a.max_blocks + p0 + i];
+    const bool fine = pid >= 0 && pid < a.num_pages;
+    first_row[i] = fine ? (static_cast<uint32_t>(pid) * a.Hkv + kvh) << a.page_log2 : kNone;
+    if (!fine) bad = 1;
+  }
+  __syncthreads();
+  // this call's key and value go into the cache first; the workgroup then reads them from there
+  if (a.k_new && whole == len && to == len) {
+    const int pos = len - 1;
+    const uint32_t page = first_row[(pos >> a.page_log2) - p0];
+    if (page != kNone && tid < D / 4) {
+      const int64_t row = int64_t(page) + (pos & in_page);
+      const int64_t src = int64_t(b) * a.Hkv + kvh;
+      const int piece = tid % (D / 8);
+      if (tid < D / 8) reinterpret_cast<uint4*>(a.k_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.k_new)[src * (D / 8) + piece];
+      else reinterpret_cast<uint4*>(a.v_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.v_new)[src * (D / 8) + piece];
+    }
+    __syncthreads();
+  }
+  const bool clean = bad == 0;
+  for (int t0 = from + wv * kAttnTile; t0 < to; t0 += 4 * kAttnTile) {
+    // (rows past the end lie in the last page or repeat its last row; what they give is masked)
     Frag kf[2][KS];
     uint32_t vr[8][VW];
     uint32_t dead = 0;   // bit i: this lane's value row i is not part of the request
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t row = max(row_of(min(t0 + 16 * h + r, end - 1)), int64_t(0));
-#pragma unroll
-      for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(a.k_pages + row * (D * 2) + x * 64 + g * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int pos = t0 + 16 * (i >> 2) + 4 * g + (i & 3);
-      const int64_t row = row_of(min(pos, end - 1));
-      if (pos >= end || row < 0) dead |= 1u << i;
-      const uint8_t* vp = a.v_pages + max(row, int64_t(0)) * (D * 2) + r * (DPL * 2);
+    const auto load_v = [&](const uint8_t* vp, int i) {
       if constexpr (VW == 4) {
         const uint4 w = *reinterpret_cast<const uint4*>(vp);
         vr[i][0] = w.x; vr[i][1] = w.y; vr[i][2] = w.z; vr[i][3] = w.w;
@@ -250,21 +304,55 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, con
         const uint2 w = *reinterpret_cast<const uint2*>(vp);
         vr[i][0] = w.x; vr[i][1] = w.y;
       }
+    };
+    if constexpr (P16) {
+      int64_t base[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int pos = t0 + 16 * h;
+        const uint32_t page = __builtin_amdgcn_readfirstlane(first_row[min((pos >> a.page_log2) - p0, np - 1)]);
+        if (page == kNone) dead |= 0xfu << (4 * h);
+        base[h] = int64_t(page == kNone ? 0 : page + (pos & in_page)) * (D * 2);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(a.k_pages + base[h] + k_off + x * 64);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) load_v(a.v_pages + base[i >> 2] + v_off + (i & 3) * (D * 2), i);
+    } else {
+      const auto row_of = [&](int pos) -> uint32_t {   // cache row of a position, kNone where there is none
+        const uint32_t page = first_row[(pos >> a.page_log2) - p0];
+        return page == kNone ? kNone : page + (pos & in_page);
+      };
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t row = row_of(min(t0 + 16 * h + r, to - 1));
+        const uint8_t* kp = a.k_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + g * 16;
+#pragma unroll
+        for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(kp + x * 64);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t row = row_of(min(t0 + 16 * (i >> 2) + 4 * g + (i & 3), to - 1));
+        if (row == kNone) dead |= 1u << i;
+        load_v(a.v_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + r * (DPL * 2), i);
+      }
     }
     f32x4 s[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int h = 0; h < 2; ++h) s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int x = 0; x < KS; ++x) s[h] = mfma(kf[h][x], qf[x], s[h]);
-    }
+    for (int x = 0; x < KS; ++x)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[h] = mfma(kf[h][x], qf[x], s[h]);
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * a.scale_log2;
-    if (!clean || t0 + kAttnTile > end) {
+    if (!clean || t0 + kAttnTile > to) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (dead >> i & 1) {
+        if ((dead >> i & 1) || t0 + 16 * (i >> 2) + 4 * g + (i & 3) >= to) {
           p[i] = -INFINITY;
 #pragma unroll
           for (int w = 0; w < VW; ++w) vr[i][w] = 0;   // whatever lies there: 0 * NaN is NaN
@@ -276,12 +364,14 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, con
     for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i]);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float base = top == -INFINITY ? 0.0f : top;
-    const float shrink = pow2(mx - base);
-    mx = top;
-    sum *= shrink;
+    if (__any(top > mx)) {               // (the maximum settles after a few tiles)
+      const float shrink = top == -INFINITY ? 1.0f : pow2(mx - top);
+      mx = top;
+      sum *= shrink;
 #pragma unroll
-    for (int m = 0; m < DPL; ++m) o[m] *= shrink;
+      for (int m = 0; m < DPL; ++m) o[m] *= shrink;
+    }
+    const float base = mx == -INFINITY ? 0.0f : mx;
     Frag pf;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -299,6 +389,7 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, con
       o[m] = mfma(vf, pf, o[m]);
     }
   }
+  }
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);
   if (g == 0) {
@@ -311,7 +402,6 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, con
     for (int m = 0; m < DPL; ++m) part_o[wv][r][DPL * (4 * g + i) + m] = o[m][i];
   __syncthreads();
 
-  const int64_t units = int64_t(a.B) * a.Hq;
   for (int x = tid; x < heads * D; x += 256) {
     const int h = x / D, c = x % D;
     const float m0 = fmaxf(fmaxf(part_m[0][h], part_m[1][h]), fmaxf(part_m[2][h], part_m[3][h]));
@@ -323,48 +413,89 @@ __global__ __launch_bounds__(256) void kv_attention_kernel(const AttnArgs a, con
       acc = fmaf(f, part_o[w][h][c], acc);
       l = fmaf(f, part_l[w][h], l);
     }
-    const int64_t unit = int64_t(b) * a.Hq + kvh * G + head0 + h;
-    if (plan.splits == 1) {
-      reinterpret_cast<uint16_t*>(a.out)[unit * D + c] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc / l);
+    if (splits == 1) {
+      const int64_t at = (int64_t(b) * a.Hq + kvh * G + head0 + h) * D + c;
+      reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc / l);
     } else {
-      a.ws[(unit * plan.splits + split) * D + c] = acc;
-      if (c == 0) reinterpret_cast<float2*>(a.ws + units * plan.splits * D)[unit * plan.splits + split] = make_float2(m0, l);
+      const int64_t at = int64_t(id) * plan.heads + h;
+      a.ws[at * D + c] = acc;
+      if (c == 0) reinterpret_cast<float2*>(a.ws + int64_t(plan.items) * units * plan.heads * D)[at] = make_float2(m0, l);
     }
   }
 }
 
-// The chunks of one (request, query head) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s,
-// in the order of the chunks. A request of no tokens gets zeros.
+// The items of one (request, query head) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, 256
+// items at a time: a thread takes one item's weight, then every channel's sum runs over the items
+// in 256 / D interleaved parts (each in order, joined in order). What bounds it is the latency of its
+// few loads. A request that was not cut has its readout already.
 template <int D>
-__global__ __launch_bounds__(D) void kv_join_kernel(const AttnArgs a, const AttnPlan plan) {
-  const int c = __builtin_amdgcn_workitem_id_x();
+__global__ __launch_bounds__(256) void kv_join_kernel(const AttnArgs a, const AttnPlan plan) {
+  constexpr int P = 256 / D;
+  __shared__ float f[256], part[P][D], top[4], low[4];
+  const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63, wv = tid >> 6;
+  const int c = tid % D, part0 = tid / D;
   const int64_t unit = __builtin_amdgcn_workgroup_id_x();
-  const int b = static_cast<int>(unit / a.Hq);
-  const int64_t cap = int64_t(a.max_blocks) << a.page_log2;
-  const int len = static_cast<int>(min(int64_t(min(max(a.seq_lens[b], 0), a.max_len)), cap));
-  const int n = (len + plan.chunk - 1) / plan.chunk;
-  const float* po = a.ws + unit * plan.splits * D + c;
-  const float2* ml = reinterpret_cast<const float2*>(a.ws + int64_t(a.B) * a.Hq * plan.splits * D) + unit * plan.splits;
-  float m = -INFINITY;
-  for (int s = 0; s < n; ++s) m = fmaxf(m, ml[s].x);
-  const float base = m == -INFINITY ? 0.0f : m;
-  float acc = 0.0f, l = 0.0f;
-  for (int s = 0; s < n; ++s) {
-    const float2 x = ml[s];
-    const float f = pow2(x.x - base);
-    acc = fmaf(f, po[int64_t(s) * D], acc);
-    l = fmaf(f, x.y, l);
+  const int b = static_cast<int>(unit / a.Hq), hq = static_cast<int>(unit - int64_t(b) * a.Hq);
+  __shared__ int64_t sh[4];
+  const int chunk = chunk_of(a, plan, sh);
+  const int n = items_of(length_of(a, b), chunk);
+  if (n == 1) return;
+  int64_t before = 0;
+  for (int x = tid; x < b; x += 256) before += items_of(length_of(a, x), chunk);
+  before = block_sum(before, sh);
+  const int G = a.Hq / a.Hkv, units = a.Hkv * plan.tiles;
+  const int64_t step = int64_t(units) * plan.heads;      // between a unit's items
+  const int64_t first = (before * units + hq / G * plan.tiles + hq % G / 16) * plan.heads + hq % G % 16;
+  const float* po = a.ws + first * D + c;
+  const float2* ml = reinterpret_cast<const float2*>(a.ws + int64_t(plan.items) * step * D) + first;
+  float m = -INFINITY, acc = 0.0f, l = 0.0f;
+  for (int s0 = 0; s0 < n; s0 += 256) {
+    const float2 x = s0 + tid < n ? ml[(s0 + tid) * step] : make_float2(-INFINITY, 0.0f);
+    float t = x.x;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) t = fmaxf(t, __shfl_xor(t, o));
+    __syncthreads();                     // the last round's reads are over
+    if (lane == 0) top[wv] = t;
+    __syncthreads();
+    const float m0 = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), m);
+    const float base = m0 == -INFINITY ? 0.0f : m0;
+    const float shrink = pow2(m - base), w = pow2(x.x - base);
+    f[tid] = w;
+    float sum = w * x.y;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sum += __shfl_xor(sum, o);
+    if (lane == 0) low[wv] = sum;
+    __syncthreads();
+    l = fmaf(l, shrink, (low[0] + low[1]) + (low[2] + low[3]));
+    acc *= shrink;
+    m = m0;
+    const int stop = min(256, n - s0);
+    float more[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int s = part0;
+    for (; s + 3 * P < stop; s += 4 * P)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) more[i] = fmaf(f[s + i * P], po[(s0 + s + i * P) * step * D], more[i]);
+    for (; s < stop; s += P) more[0] = fmaf(f[s], po[(s0 + s) * step * D], more[0]);
+    acc += (more[0] + more[1]) + (more[2] + more[3]);
   }
-  reinterpret_cast<uint16_t*>(a.out)[unit * D + c] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc / l);
+  part[part0][c] = acc;
+  __syncthreads();
+  if (tid < D) {
+    float o = part[0][c];
+#pragma unroll
+    for (int i = 1; i < P; ++i) o += part[i][c];
+    reinterpret_cast<uint16_t*>(a.out)[unit * D + c] = float_to_bf16_bits(l == 0.0f ? 0.0f : o / l);
+  }
 }
 
 template <int D>
 hipError_t attention_d(const AttnArgs& a, hipStream_t s) {
-  const AttnPlan p = attn_plan(a.B, a.Hq, a.Hkv, a.max_len);
-  const unsigned grid = static_cast<unsigned>(kv_attention_grid(a.B, a.Hq, a.Hkv, a.max_len));
-  hipLaunchKernelGGL((kv_attention_kernel<D>), dim3(grid), dim3(256), 0, s, a, p);
-  if (p.splits > 1)
-    hipLaunchKernelGGL((kv_join_kernel<D>), dim3(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.Hq)), dim3(D), 0, s, a, p);
+  const AttnPlan p = attn_plan(a.B, a.Hq, a.Hkv, D, a.max_len);
+  const dim3 grid(static_cast<unsigned>(p.items) * a.Hkv * p.tiles);
+  if (a.page_log2 >= 4) hipLaunchKernelGGL((kv_attention_kernel<D, true>), grid, dim3(256), 0, s, a, p);
+  else hipLaunchKernelGGL((kv_attention_kernel<D, false>), grid, dim3(256), 0, s, a, p);
+  if (p.items > a.B)
+    hipLaunchKernelGGL((kv_join_kernel<D>), dim3(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.Hq)), dim3(256), 0, s, a, p);
   return hipGetLastError();
 }
 
@@ -386,15 +517,15 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
-  const AttnPlan p = attn_plan(B, Hq, Hkv, max_len);
-  return int64_t(B) * Hkv * p.tiles * p.splits;
+int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len) {
+  const AttnPlan p = attn_plan(B, Hq, Hkv, d, max_len);
+  return (int64_t(p.per_unit) + B) * Hkv * p.tiles;
 }
 
 size_t kv_attention_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len) {
-  const AttnPlan p = attn_plan(B, Hq, Hkv, max_len);
-  if (p.splits == 1) return 0;
-  return static_cast<size_t>(B) * Hq * p.splits * (static_cast<size_t>(d) + 2) * 4;
+  const AttnPlan p = attn_plan(B, Hq, Hkv, d, max_len);
+  if (p.items == B) return 0;
+  return static_cast<size_t>(p.items) * Hkv * p.tiles * p.heads * (static_cast<size_t>(d) + 2) * 4;
 }
 
 hipError_t launch_kv_attention(int d, const AttnArgs& a, hipStream_t s) {

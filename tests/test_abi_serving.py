@@ -104,7 +104,7 @@ ATT_OK = dict(q=X, kp=X, vp=X, table=X, lens=X, B=1, Hq=4, Hkv=2, d=64, pages=3,
     (dict(Hq=3), BAD, "multiple"), (dict(Hq=0), BAD, "multiple"), (dict(Hkv=0), BAD, "num_kv_heads"), (dict(d=32), UNSUP, "supports"),
     (dict(page=12), UNSUP, "power"), (dict(q=None), BAD, "NULL"), (dict(table=None), BAD, "NULL"), (dict(kn=X), BAD, "together"), (dict(vn=X), BAD, "together"),
     (dict(out=X + 8), BAD, "16-byte"), (dict(kn=X, vn=X + 2), BAD, "16-byte"), (dict(lens=X + 2), BAD, "4-byte"),
-    (dict(B=2 ** 24, max_len=2 ** 30), BAD, "grid limit"), (dict(max_len=1 << 20, ws=None), BAD, "workspace"), (dict(max_len=1 << 20, wsn=16), BAD, "workspace"),
+    (dict(B=2 ** 30), BAD, "grid limit"), (dict(max_len=1 << 20, ws=None), BAD, "workspace"), (dict(max_len=1 << 20, wsn=16), BAD, "workspace"),
     (dict(max_len=1 << 20, ws=X + 4), BAD, "workspace")])
 def test_attention_refusals(change, status, text):
     assert _call("kv_decode_attention", ATT, ATT_OK, **change) == status and text in lib.last_error()
