@@ -1255,7 +1255,7 @@ size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32
                                            int32_t max_len) {
   if (B <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || (d != 64 && d != 128) ||
       max_len < 0 || max_len > (1 << 30) ||
-      damp::kv_attention_grid(B, num_q_heads, num_kv_heads, d, max_len) > 0x7fffffffLL)
+      damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > 0x7fffffffLL)
     return 0;
   return damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);
 }
@@ -1278,7 +1278,7 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages, con
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_new, 16) ||
       !aligned(v_new, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages, k_new, v_new and out must be 16-byte, block_table and seq_lens 4-byte aligned");
-  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, d, max_len) > 0x7fffffffLL ||
+  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > 0x7fffffffLL ||
       static_cast<int64_t>(B) * num_q_heads > 0x7fffffffLL)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_len = %d exceeds the grid limit", B, max_len);
   const size_t need = damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);

@@ -154,12 +154,13 @@ struct AttnPlan {
 
 constexpr int kAttnLeast = 4 * kAttnTile;    // tokens: no item is shorter unless its request is
 
-AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len) {
+AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
   AttnPlan p;
   p.tiles = (Hq / Hkv + 15) / 16;
   p.heads = std::min(Hq / Hkv, 16);
-  // workgroups that are resident at once: 4 a CU by registers and LDS at d = 128, 6 at d = 64
-  const int64_t units = int64_t(Hkv) * p.tiles, resident = 256 * (d == 128 ? 4 : 6);
+  // 4 workgroups a CU: at d = 128 that many are resident by registers and LDS; at d = 64 6 would be,
+  // and 64 requests of 8,192 tokens took 208 us shared out among 6 a CU against 197 us among 4
+  const int64_t units = int64_t(Hkv) * p.tiles, resident = 256 * 4;
   const int64_t most = (int64_t(max_len) + kAttnLeast - 1) / kAttnLeast * B;   // no more are ever cut
   p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(resident / units, 1), std::max<int64_t>(most, 1)));
   p.items = max_len <= kAttnLeast ? B : p.per_unit + B;
@@ -490,7 +491,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const AttnArgs a, const At
 
 template <int D>
 hipError_t attention_d(const AttnArgs& a, hipStream_t s) {
-  const AttnPlan p = attn_plan(a.B, a.Hq, a.Hkv, D, a.max_len);
+  const AttnPlan p = attn_plan(a.B, a.Hq, a.Hkv, a.max_len);
   const dim3 grid(static_cast<unsigned>(p.items) * a.Hkv * p.tiles);
   if (a.page_log2 >= 4) hipLaunchKernelGGL((kv_attention_kernel<D, true>), grid, dim3(256), 0, s, a, p);
   else hipLaunchKernelGGL((kv_attention_kernel<D, false>), grid, dim3(256), 0, s, a, p);
@@ -517,13 +518,13 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len) {
-  const AttnPlan p = attn_plan(B, Hq, Hkv, d, max_len);
+int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
+  const AttnPlan p = attn_plan(B, Hq, Hkv, max_len);
   return (int64_t(p.per_unit) + B) * Hkv * p.tiles;
 }
 
 size_t kv_attention_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len) {
-  const AttnPlan p = attn_plan(B, Hq, Hkv, d, max_len);
+  const AttnPlan p = attn_plan(B, Hq, Hkv, max_len);
   if (p.items == B) return 0;
   return static_cast<size_t>(p.items) * Hkv * p.tiles * p.heads * (static_cast<size_t>(d) + 2) * 4;
 }

@@ -174,7 +174,7 @@ int kv_tables_max_requests();
 hipError_t launch_kv_tables(const TableArgs& a, hipStream_t s);
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
 size_t kv_attention_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len);
-int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_len);
+int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len);
 hipError_t launch_kv_attention(int d, const AttnArgs& a, hipStream_t s);
 
 // Calibration (calib_kernels.hip). Sizes are validated by the caller: d in {16, 32, 64, 128},

@@ -605,15 +605,49 @@ class StqState:
 # ------------------------------------------------------------------------------------------
 # linear attention and prompts
 # ------------------------------------------------------------------------------------------
-def _on(device, stream):
-    """A context in which ``device`` is current and ``stream`` (or that device's current stream)
-    runs the call: workspaces allocated inside belong to that stream."""
-    torch = _torch()
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(device)
+class _On:
+    """The device and stream of a call: ``stream``, or the current stream of ``device``. Inside,
+    both are current, so that a workspace allocated there belongs to that stream. Where they are
+    already (the usual case), entering does nothing."""
+
+    __slots__ = ("ctx", "stream")
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            self.ctx, self.stream = torch.cuda.stream(stream), stream.cuda_stream
+            return
+        self.ctx = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = torch._C._cuda_getCurrentRawStream(device.index)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _fit(t, name, dtype, shape, device):
+    """_need, with one test where nothing is wrong (these calls are often shorter than their checks)."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape, device)
+
+
+def _first(t, name, dtype, dim=1):
+    """The tensor whose device and leading size the others go by."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda or t.dim() != dim:
+        raise ValueError(f"{name} must be a {dim}-dimensional device tensor")
+    _fit(t, name, dtype, t.shape, t.device)
+    return t.device
 
 
 def _fp32_pool(pool, dev):
@@ -621,7 +655,7 @@ def _fp32_pool(pool, dev):
     if not isinstance(pool, torch.Tensor) or pool.dim() != 4:
         raise ValueError("pool must be a tensor [num_slots, H, d, d]")
     S_, H, d, d2 = pool.shape
-    _need(pool, "pool", torch.float32, (S_, H, d, d2), dev)
+    _fit(pool, "pool", torch.float32, (S_, H, d, d2), dev)
     if d != d2:
         raise ValueError("pool must be square per head")
     return S_, H, d
@@ -644,12 +678,12 @@ def _decay(alpha, n, H, d, dev, fixed):
     if not isinstance(alpha, torch.Tensor):
         raise TypeError("alpha must be a torch.Tensor")
     if alpha.dim() == 3:
-        _need(alpha, "alpha", torch.float32, (n, H, d), dev)
+        _fit(alpha, "alpha", torch.float32, (n, H, d), dev)
         return DAMP_DECAY_PER_KEY
     if fixed and alpha.dim() == 1:
-        _need(alpha, "alpha", torch.float32, (H,), dev)
+        _fit(alpha, "alpha", torch.float32, (H,), dev)
         return DAMP_DECAY_PER_HEAD
-    _need(alpha, "alpha", torch.float32, (n, H), dev)
+    _fit(alpha, "alpha", torch.float32, (n, H), dev)
     return DAMP_DECAY_SCALAR
 
 
@@ -659,7 +693,7 @@ def _workspace(workspace, nbytes, dev):
         return 0, 0
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    _fit(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace has {workspace.numel()} bytes, {nbytes} needed")
     return _ptr(workspace), workspace.numel()
@@ -670,17 +704,17 @@ def fp32_linear_step(pool, slot_idx, q, k, v, alpha, out, stream=None) -> None:
     S <- alpha S + k v^T, out = S^T q. q, k, v bf16 or fp32 [B, H, d]; alpha fp32 [B, H],
     [B, H, d] (per key channel) or [H] (fixed per head); out fp32 [B, H, d]."""
     torch = _torch()
-    _need(slot_idx, "slot_idx", torch.int32, (slot_idx.numel(),))
-    B, dev = slot_idx.shape[0], slot_idx.device
+    dev = _first(slot_idx, "slot_idx", torch.int32)
+    B = slot_idx.shape[0]
     S_, H, d = _fp32_pool(pool, dev)
     dt = _dtype(q, "q")
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, q.dtype, (B, H, d), dev)
+        _fit(t, name, q.dtype, (B, H, d), dev)
     decay = _decay(alpha, B, H, d, dev, True)
-    _need(out, "out", torch.float32, (B, H, d), dev)
-    with _on(dev, stream):
+    _fit(out, "out", torch.float32, (B, H, d), dev)
+    with _On(dev, stream) as s:
         _check(load().fp32_linear_step(_ptr(pool), S_, H, d, d, _ptr(slot_idx), B, _ptr(q), _ptr(k),
-                                       _ptr(v), dt, _ptr(alpha), decay, _ptr(out), _stream(stream)))
+                                       _ptr(v), dt, _ptr(alpha), decay, _ptr(out), s))
 
 
 def prefill_workspace_bytes(delta: bool, B: int, T: int, H: int, d: int, dtype, decay: int = DAMP_DECAY_SCALAR) -> int:
@@ -692,28 +726,28 @@ def prefill_workspace_bytes(delta: bool, B: int, T: int, H: int, d: int, dtype, 
 
 def _prefill(delta, pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, resume, workspace, stream):
     torch = _torch()
-    _need(slot_idx, "slot_idx", torch.int32, (slot_idx.numel(),))
-    B, dev = slot_idx.shape[0], slot_idx.device
+    dev = _first(slot_idx, "slot_idx", torch.int32)
+    B = slot_idx.shape[0]
     S_, H, d = _fp32_pool(pool, dev)
     dt = _dtype(q, "q")
     T = q.shape[0] if q.dim() == 3 else -1
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    _fit(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _need(t, name, q.dtype, (T, H, d), dev)
+        _fit(t, name, q.dtype, (T, H, d), dev)
     decay = _decay(alpha, T, H, d, dev, not delta)
     if delta:
-        _need(beta, "beta", torch.float32, (T, H), dev)
+        _fit(beta, "beta", torch.float32, (T, H), dev)
     if resume is not None:
-        _need(resume, "resume", torch.int32, (B,), dev)
+        _fit(resume, "resume", torch.int32, (B,), dev)
     L = load()
-    with _on(dev, stream):
+    with _On(dev, stream) as s:
         ws, n = _workspace(workspace, L.fp32_prefill_workspace_bytes(delta, B, T, H, d, dt, decay), dev)
         head = (_ptr(pool), S_, H, d, d, _ptr(slot_idx), _ptr(cu_seqlens),
                 _ptr(resume) if resume is not None else None, B, T, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), decay)
         if delta:
-            _check(L.fp32_delta_prefill(*head, _ptr(beta), _ptr(out), ws, n, _stream(stream)))
+            _check(L.fp32_delta_prefill(*head, _ptr(beta), _ptr(out), ws, n, s))
         else:
-            _check(L.fp32_linear_prefill(*head, _ptr(out), ws, n, _stream(stream)))
+            _check(L.fp32_linear_prefill(*head, _ptr(out), ws, n, s))
 
 
 def fp32_linear_prefill(pool, slot_idx, cu_seqlens, q, k, v, alpha, out, resume=None, workspace=None,
@@ -741,8 +775,8 @@ def _pages(k_pages, v_pages, dev):
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must be a tensor [num_pages, Hkv, page_size, d]")
     n, Hkv, page, d = k_pages.shape
-    _need(k_pages, "k_pages", torch.bfloat16, (n, Hkv, page, d), dev)
-    _need(v_pages, "v_pages", torch.bfloat16, (n, Hkv, page, d), dev)
+    _fit(k_pages, "k_pages", torch.bfloat16, (n, Hkv, page, d), dev)
+    _fit(v_pages, "v_pages", torch.bfloat16, (n, Hkv, page, d), dev)
     return n, Hkv, page, d
 
 
@@ -752,38 +786,38 @@ def kv_build_tables(seq_lens, new_lens, free_pages, block_table, page_size: int,
     block_table int32 [B, max_blocks], its new entries written; slot_map int64 [T], positions int32
     [T] (or None), cu_new int32 [B + 1] and used int32 [1] are written."""
     torch = _torch()
-    _need(seq_lens, "seq_lens", torch.int32, (seq_lens.numel(),))
-    B, dev = seq_lens.shape[0], seq_lens.device
-    _need(new_lens, "new_lens", torch.int32, (B,), dev)
-    _need(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
+    dev = _first(seq_lens, "seq_lens", torch.int32)
+    B = seq_lens.shape[0]
+    _fit(new_lens, "new_lens", torch.int32, (B,), dev)
+    _fit(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     blocks = block_table.shape[1]
-    _need(block_table, "block_table", torch.int32, (B, blocks), dev)
+    _fit(block_table, "block_table", torch.int32, (B, blocks), dev)
     T = slot_map.numel()
-    _need(slot_map, "slot_map", torch.int64, (T,), dev)
+    _fit(slot_map, "slot_map", torch.int64, (T,), dev)
     if positions is not None:
-        _need(positions, "positions", torch.int32, (T,), dev)
-    _need(cu_new, "cu_new", torch.int32, (B + 1,), dev)
-    _need(used, "used", torch.int32, (1,), dev)
-    with _on(dev, stream):
+        _fit(positions, "positions", torch.int32, (T,), dev)
+    _fit(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    _fit(used, "used", torch.int32, (1,), dev)
+    with _On(dev, stream) as s:
         _check(load().kv_build_tables(_ptr(seq_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
                                       page_size, _ptr(block_table), blocks, _ptr(slot_map),
                                       _ptr(positions) if positions is not None else None, T, _ptr(cu_new),
-                                      _ptr(used), _stream(stream)))
+                                      _ptr(used), s))
 
 
 def kv_append(k, v, slot_map, k_pages, v_pages, stream=None) -> None:
     """Stores k, v bf16 [T, Hkv, d] at the cache slots slot_map int64 [T] (outside the cache: skipped)."""
     torch = _torch()
-    n, Hkv, page, d = _pages(k_pages, v_pages, slot_map.device)
-    T, dev = slot_map.numel(), slot_map.device
-    _need(slot_map, "slot_map", torch.int64, (T,), dev)
-    _need(k, "k", torch.bfloat16, (T, Hkv, d), dev)
-    _need(v, "v", torch.bfloat16, (T, Hkv, d), dev)
-    with _on(dev, stream):
+    dev = _first(slot_map, "slot_map", torch.int64)
+    T = slot_map.shape[0]
+    n, Hkv, page, d = _pages(k_pages, v_pages, dev)
+    _fit(k, "k", torch.bfloat16, (T, Hkv, d), dev)
+    _fit(v, "v", torch.bfloat16, (T, Hkv, d), dev)
+    with _On(dev, stream) as s:
         _check(load().kv_append(_ptr(k), _ptr(v), _ptr(slot_map), T, Hkv, d, _ptr(k_pages), _ptr(v_pages), n,
-                                page, _stream(stream)))
+                                page, s))
 
 
 def kv_decode_attention_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int, d: int, max_len: int) -> int:
@@ -798,30 +832,29 @@ def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=N
     position seq_lens - 1 first. ``max_len``: an upper bound of seq_lens (the table's by default).
     ``workspace`` (uint8, kv_decode_attention_workspace_bytes) is allocated for the call if not given."""
     torch = _torch()
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a tensor [B, Hq, d]")
-    B, Hq, d = q.shape
-    dev = q.device
-    n, Hkv, page, dc = _pages(k_pages, v_pages, dev)
-    _need(q, "q", torch.bfloat16, (B, Hq, dc), dev)
-    _need(out, "out", torch.bfloat16, (B, Hq, dc), dev)
+    dev = _first(q, "q", torch.bfloat16, 3)
+    B, Hq, dc = q.shape
+    n, Hkv, page, d = _pages(k_pages, v_pages, dev)
+    if d != dc:
+        raise ValueError(f"q has {dc} channels, the pages {d}")
+    _fit(out, "out", torch.bfloat16, (B, Hq, dc), dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     blocks = block_table.shape[1]
-    _need(block_table, "block_table", torch.int32, (B, blocks), dev)
-    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _fit(block_table, "block_table", torch.int32, (B, blocks), dev)
+    _fit(seq_lens, "seq_lens", torch.int32, (B,), dev)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new must be given together")
     if k_new is not None:
-        _need(k_new, "k_new", torch.bfloat16, (B, Hkv, dc), dev)
-        _need(v_new, "v_new", torch.bfloat16, (B, Hkv, dc), dev)
+        _fit(k_new, "k_new", torch.bfloat16, (B, Hkv, dc), dev)
+        _fit(v_new, "v_new", torch.bfloat16, (B, Hkv, dc), dev)
     if max_len is None:
         max_len = blocks * page
     L = load()
-    with _on(dev, stream):
+    with _On(dev, stream) as s:
         ws, nb = _workspace(workspace, L.kv_decode_attention_workspace_bytes(B, Hq, Hkv, dc, max_len), dev)
         _check(L.kv_decode_attention(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), B,
                                      Hq, Hkv, dc, n, page, blocks, max_len, dc ** -0.5 if scale is None else scale,
                                      _ptr(k_new) if k_new is not None else None,
                                      _ptr(v_new) if v_new is not None else None, _ptr(out), ws, nb,
-                                     _stream(stream)))
+                                     s))
