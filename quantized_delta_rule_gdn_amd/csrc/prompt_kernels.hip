@@ -268,9 +268,9 @@ __device__ __forceinline__ Place place_of(unsigned id, unsigned count, unsigned 
 }
 
 template <int D, int NT>
-__global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
+__global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, MD = D / 64, LS = D + 8, NC = 16 * NT;
-  __shared__ __align__(16) uint16_t kb[2][kC][LS];
+  __shared__ __align__(16) uint16_t kb[kC][LS];
   __shared__ __align__(16) uint16_t sp[2][NC][LS];
   __shared__ __align__(16) uint16_t rp[3][NC][kLd], ep[2][NC][kLd], wp[3][NC][kLd];
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
@@ -379,9 +379,9 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
       f.k[j] = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
     }
   };
-  const auto store_k = [&](int to) {
+  const auto store_k = [&]() {
 #pragma unroll
-    for (int j = 0; j < KS; ++j) *reinterpret_cast<uint4*>(&kb[to][tid / (D / 8) + j * kRows][(tid % (D / 8)) * 8]) = f.k[j];
+    for (int j = 0; j < KS; ++j) *reinterpret_cast<uint4*>(&kb[tid / (D / 8) + j * kRows][(tid % (D / 8)) * 8]) = f.k[j];
   };
 
   // O = 2^G Q S + P E of the chunk at t0, from registers alone; off the chain, it fills the wait for
@@ -421,16 +421,15 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
   load_q(sp_b.begin);
   load_x(sp_b.begin);
   share_state();
-  store_k(0);
+  store_k();
   __syncthreads();
-  int cur = 0;
-  for (int t0 = sp_b.begin; t0 < sp_b.end; t0 += kC, cur ^= 1) {
+  for (int t0 = sp_b.begin; t0 < sp_b.end; t0 += kC) {
     const int tn = sp_b.end - t0 > kC ? t0 + kC : t0;   // the chunk to load next
     // K S; R = V - 2^G K S
     Frag kf[KS], s[NT][2][KS];
 #pragma unroll
     for (int x = 0; x < KS; ++x) {
-      kf[x] = load_frag(&kb[cur][16 * w + r][x * 32 + g * 8]);
+      kf[x] = load_frag(&kb[16 * w + r][x * 32 + g * 8]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -507,7 +506,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
     for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int m = 0; m < MD; ++m) {
-        const uint16_t* from = &kb[cur][32 * x + 8 * g + r / 4][own + 16 * m + 4 * (r % 4)];
+        const uint16_t* from = &kb[32 * x + 8 * g + r / 4][own + 16 * m + 4 * (r % 4)];
         kt[x][m] = load_frag_t(from, from + 4 * LS);
       }
     load_q(tn);
@@ -539,7 +538,7 @@ __global__ __launch_bounds__(256) void delta_chain_kernel(const PromptArgs a) {
       }
     }
     share_state();
-    store_k(cur ^ 1);
+    store_k();   // (K was last read before the barrier)
     __syncthreads();
   }
   readout(sp_b.begin + (sp_b.end - sp_b.begin - 1) / kC * kC, true);
