@@ -326,21 +326,26 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   const uint32_t off_ws1 = w < 2 ? kDeltaUnit : off_ws + 64;               // their right halves; none above the diagonal
   DeltaRows<D> f;
   uint16_t vv[NT][4];
-  const auto rows = [&](const uint16_t* p, int t0, int width) {
-    return make_rsrc(p + t0 * rstep, (min(sp_b.end - t0, kC) - 1) * ostep + width * 2);
+  struct Chunk {        // a chunk's place: byte offsets of its rows and workspace, rows from there on
+    int64_t row, ws;
+    int left;
   };
-  const auto chunk_ws = [&](int t0) { return make_rsrc(ws + (t0 - sp_b.begin) / kC * ws_step, kDeltaUnit); };
+  Chunk now{sp_b.begin * rstep * 2, 0, sp_b.end - sp_b.begin}, last_chunk = now;
+  const auto rows = [&](const uint16_t* p, const Chunk& c, int width) {
+    return make_rsrc(reinterpret_cast<const uint8_t*>(p) + c.row, (min(c.left, kC) - 1) * ostep + width * 2);
+  };
+  const auto chunk_ws = [&](const Chunk& c) { return make_rsrc(ws + c.ws, kDeltaUnit); };
   const auto frag = [](rsrc_t rs, uint32_t off, int imm) {
     const auto v = __builtin_amdgcn_raw_buffer_load_b128(rs, off, imm, 0);
     return Frag{{v[0], v[1], v[2], v[3]}};
   };
-  const auto load_q = [&](int t0) {
-    const rsrc_t qr = rows(qp, t0, D);
+  const auto load_q = [&](const Chunk& at) {
+    const rsrc_t qr = rows(qp, at, D);
 #pragma unroll
     for (int x = 0; x < KS; ++x) f.q[x] = frag(qr, off_row + x * 64, 0);
   };
-  const auto load_v = [&](int t0) {
-    const rsrc_t vr = rows(vp, t0, NC), wr = chunk_ws(t0);
+  const auto load_v = [&](const Chunk& at) {
+    const rsrc_t vr = rows(vp, at, NC), wr = chunk_ws(at);
     const auto e = __builtin_amdgcn_raw_buffer_load_b128(wr, kGates + (16 * w + 4 * g) * 4, 0, 0);
     const auto c = __builtin_amdgcn_raw_buffer_load_b128(wr, kGates + (kC + 16 * w + 4 * g) * 4, 0, 0);
     f.last = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(wr, kGates + (kC - 1) * 4, 0, 0));
@@ -354,16 +359,16 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
 #pragma unroll
       for (int i = 0; i < 4; ++i) vv[nt][i] = __builtin_amdgcn_raw_buffer_load_b16(vr, off_val + i * ostep + 32 * nt, 0, 0);
   };
-  const auto load_x = [&](int t0) {
-    const rsrc_t wr = chunk_ws(t0);
+  const auto load_x = [&](const Chunk& at) {
+    const rsrc_t wr = chunk_ws(at);
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
       f.x[p][0] = frag(wr, off_ws + p * kPlane, 0);
       f.x[p][1] = frag(wr, off_ws1 + p * kPlane, 0);
     }
   };
-  const auto load_p = [&](int t0) {
-    const rsrc_t wr = chunk_ws(t0);
+  const auto load_p = [&](const Chunk& at) {
+    const rsrc_t wr = chunk_ws(at);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       f.p[p][0] = frag(wr, off_ws + (3 + p) * kPlane, 0);
@@ -371,8 +376,8 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
     }
   };
   constexpr int kRows = 256 / (D / 8);   // rows of K that the threads' shares are apart
-  const auto load_k = [&](int t0) {
-    const rsrc_t kr = rows(kp, t0, D);
+  const auto load_k = [&](const Chunk& at) {
+    const rsrc_t kr = rows(kp, at, D);
 #pragma unroll
     for (int j = 0; j < KS; ++j) {
       const Frag v = frag(kr, off_k + j * kRows * ostep, 0);
@@ -388,8 +393,8 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   // the next chunk's operands (bytes = 0: there is no chunk before the first)
   f32x4 o[NT];
   Frag ef[NT][2][2];
-  const auto readout = [&](int t0, bool some) {
-    const rsrc_t out = make_rsrc(op + t0 * rstep, some ? (min(sp_b.end - t0, kC) - 1) * ostep + NC * 2 : 0);
+  const auto readout = [&](const Chunk& at, bool some) {
+    const rsrc_t out = make_rsrc(reinterpret_cast<uint8_t*>(op) + at.row, some ? (min(at.left, kC) - 1) * ostep + NC * 2 : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       f32x4 pe[2];
@@ -415,16 +420,17 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
       for (int x = 0; x < 2; ++x) ef[nt][p][x] = Frag{{0, 0, 0, 0}};
   }
 
-  load_k(sp_b.begin);
-  load_v(sp_b.begin);
-  load_p(sp_b.begin);
-  load_q(sp_b.begin);
-  load_x(sp_b.begin);
+  load_k(now);
+  load_v(now);
+  load_p(now);
+  load_q(now);
+  load_x(now);
   share_state();
   store_k();
   __syncthreads();
   for (int t0 = sp_b.begin; t0 < sp_b.end; t0 += kC) {
-    const int tn = sp_b.end - t0 > kC ? t0 + kC : t0;   // the chunk to load next
+    Chunk next = now;     // the chunk to load next; the last one once more
+    if (now.left > kC) next = Chunk{now.row + int64_t(kC) * ostep, now.ws + ws_step, now.left - kC};
     // K S; R = V - 2^G K S
     Frag kf[KS], s[NT][2][KS];
 #pragma unroll
@@ -436,9 +442,9 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
         for (int p = 0; p < 2; ++p) s[nt][p][x] = load_frag(&sp[p][16 * nt + r][x * 32 + g * 8]);
     }
     __builtin_amdgcn_sched_barrier(0);
-    load_k(tn);
-    readout(t0 - kC, t0 > sp_b.begin);
-    load_p(t0);
+    load_k(next);
+    readout(last_chunk, t0 > sp_b.begin);
+    load_p(now);
     __builtin_amdgcn_sched_barrier(0);
     const float wc[4] = {f.wc[0], f.wc[1], f.wc[2], f.wc[3]}, last = f.last;
     float eg[4] = {f.eg[0], f.eg[1], f.eg[2], f.eg[3]};
@@ -460,7 +466,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(&rp[p][16 * nt + r][16 * w + 4 * g]) = make_uint2(u0[p], u1[p]);
     }
-    load_v(tn);
+    load_v(next);
     __syncthreads();
     // E = X diag(b) R; Q S while R comes
 #pragma unroll
@@ -509,7 +515,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
         const uint16_t* from = &kb[32 * x + 8 * g + r / 4][own + 16 * m + 4 * (r % 4)];
         kt[x][m] = load_frag_t(from, from + 4 * LS);
       }
-    load_q(tn);
+    load_q(next);
     __syncthreads();
     // S = 2^G_C S + K^T (2^(G_C - G) E)
 #pragma unroll
@@ -524,7 +530,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
 #pragma unroll
         for (int x = 0; x < 2; ++x) ef[nt][p][x] = load_frag(&ep[p][16 * nt + r][x * 32 + g * 8]);
       __builtin_amdgcn_sched_barrier(0);
-      if (nt == 0) load_x(tn);
+      if (nt == 0) load_x(next);
 #pragma unroll
       for (int m = 0; m < MD; ++m) {
         f32x4 add[3];
@@ -539,9 +545,11 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
     }
     share_state();
     store_k();   // (K was last read before the barrier)
+    last_chunk = now;
+    now = next;
     __syncthreads();
   }
-  readout(sp_b.begin + (sp_b.end - sp_b.begin - 1) / kC * kC, true);
+  readout(last_chunk, true);
 #pragma unroll
   for (int m = 0; m < MD; ++m)
 #pragma unroll
