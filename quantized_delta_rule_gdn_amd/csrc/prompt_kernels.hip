@@ -240,9 +240,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
 // token rows (16 per wave) and, for the state's update, key channels (D / 4 per wave), so a wave
 // loads only its own rows of Q, X and P, straight into operand registers, one chunk ahead; K is
 // staged in LDS, where it is read by rows and, transposed, by channels; the state, R and E change
-// hands in LDS as [column][k] arrays of bf16 pieces. Three barriers a chunk. S enters K S and Q S in
-// two pieces: K S is a small part of E next to V, so that its 2^-17 stays below a binary32 sum's
-// error of the state.
+// hands in LDS as [column][k] arrays of bf16 pieces. Three barriers a chunk.
 template <int D>
 struct DeltaRows {   // one wave's operands of a chunk
   Frag q[D / 32], x[3][2], p[2][2];
@@ -271,7 +269,7 @@ template <int D, int NT>
 __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, MD = D / 64, LS = D + 8, NC = 16 * NT;
   __shared__ __align__(16) uint16_t kb[kC][LS];
-  __shared__ __align__(16) uint16_t sp[2][NC][LS];
+  __shared__ __align__(16) uint16_t sp[3][NC][LS];
   __shared__ __align__(16) uint16_t rp[3][NC][kLd], ep[2][NC][kLd], wp[3][NC][kLd];
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -308,11 +306,11 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int m = 0; m < MD; ++m) {
-        uint32_t u0[2], u1[2];
-        split_bf16<2>(S[m][nt][0], S[m][nt][1], u0);
-        split_bf16<2>(S[m][nt][2], S[m][nt][3], u1);
+        uint32_t u0[3], u1[3];
+        split_bf16<3>(S[m][nt][0], S[m][nt][1], u0);
+        split_bf16<3>(S[m][nt][2], S[m][nt][3], u1);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) *reinterpret_cast<uint2*>(&sp[p][16 * nt + r][own + 16 * m + 4 * g]) = make_uint2(u0[p], u1[p]);
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<uint2*>(&sp[p][16 * nt + r][own + 16 * m + 4 * g]) = make_uint2(u0[p], u1[p]);
       }
   };
   // A chunk's loads go through buffer resources that end with its last row: what lies past it reads
@@ -450,16 +448,19 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
     float eg[4] = {f.eg[0], f.eg[1], f.eg[2], f.eg[3]};
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      f32x4 ks[2];
+      Frag s2[KS];   // the third piece, which the readout does without
 #pragma unroll
-      for (int p = 0; p < 2; ++p) ks[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int x = 0; x < KS; ++x) s2[x] = load_frag(&sp[2][16 * nt + r][x * 32 + g * 8]);
+      f32x4 ks[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) ks[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int x = 0; x < KS; ++x)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) ks[p] = mfma(kf[x], s[nt][p][x], ks[p]);
+        for (int p = 0; p < 3; ++p) ks[p] = mfma(kf[x], p < 2 ? s[nt][p][x] : s2[x], ks[p]);
       float rr[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) rr[i] = fmaf(-eg[i], ks[0][i] + ks[1][i], __uint_as_float(uint32_t(vv[nt][i]) << 16));
+      for (int i = 0; i < 4; ++i) rr[i] = fmaf(-eg[i], ks[0][i] + (ks[1][i] + ks[2][i]), __uint_as_float(uint32_t(vv[nt][i]) << 16));
       uint32_t u0[3], u1[3];
       split_bf16<3>(rr[0], rr[1], u0);
       split_bf16<3>(rr[2], rr[3], u1);
