@@ -81,8 +81,9 @@ __device__ __forceinline__ float decay_between(Logs t, Logs s, bool live) {
 }
 
 // ---- the delta rule: what a chunk's keys and gates give -------------------------------------
-// Workspace of one chunk and head: X diag(b) in three bf16 pieces and P in two, [64][64] each (the
-// upper right quarter is neither written nor read), then 2^G_t and 2^(G_C - G_t).
+// Workspace of one chunk and head: X diag(b) in three bf16 pieces and P in two, then 2^G_t and
+// 2^(G_C - G_t). A piece [64][64] lies as the chain's waves load it: for each 16 rows and 32 columns the
+// 64 lanes' 16 bytes in a row (whole cache lines; the upper right quarter is neither written nor read).
 constexpr int kPlane = kC * kC * 2;
 constexpr int kGates = 5 * kPlane;
 constexpr int kDeltaUnit = kGates + 2 * kC * 4;
@@ -228,11 +229,11 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
     split_bf16<2>(pf[t][c0 + 2 * j], pf[t][c0 + 2 * j + 1], u);
     px[3][j] = u[0]; px[4][j] = u[1];
   }
-  uint4* dst = reinterpret_cast<uint4*>(ws + (t * kC + c0) * 2);
+  uint4* dst = reinterpret_cast<uint4*>(ws) + (t / 16 * 2 + c0 / 32) * 64 + c0 % 32 / 8 * 16 + t % 16;
 #pragma unroll
   for (int p = 0; p < 5; ++p)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) dst[p * (kPlane / 16) + h] = make_uint4(px[p][4 * h], px[p][4 * h + 1], px[p][4 * h + 2], px[p][4 * h + 3]);
+    for (int h = 0; h < 2; ++h) dst[p * (kPlane / 16) + 16 * h] = make_uint4(px[p][4 * h], px[p][4 * h + 1], px[p][4 * h + 2], px[p][4 * h + 3]);
 }
 
 // ---- the delta rule: the chain over the chunks ---------------------------------------------
@@ -320,8 +321,8 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   const uint32_t off_row = (16 * w + r) * ostep + g * 16;                  // rows of Q as operands
   const uint32_t off_k = (tid / (D / 8)) * ostep + (tid % (D / 8)) * 16;   // rows of K on their way to LDS
   const uint32_t off_val = (16 * w + 4 * g) * ostep + r * 2;               // rows of V and the readouts
-  const uint32_t off_ws = ((16 * w + r) * kC + g * 8) * 2;                 // rows of X and P
-  const uint32_t off_ws1 = w < 2 ? kDeltaUnit : off_ws + 64;               // their right halves; none above the diagonal
+  const uint32_t off_ws = (w * 128 + lane) * 16;                           // rows of X and P
+  const uint32_t off_ws1 = w < 2 ? kDeltaUnit : off_ws + 1024;             // their right halves; none above the diagonal
   DeltaRows<D> f;
   uint16_t vv[NT][4];
   struct Chunk {        // a chunk's place: byte offsets of its rows and workspace, rows from there on
