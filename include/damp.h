@@ -525,7 +525,8 @@ size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t
  *   alpha      dev fp32 [T][num_heads], [T][num_heads][d] or [num_heads] (by decay), each in [0, 1]
  *   out        dev [T][num_heads][d] of qkv_dtype (the next layer's input type), 16-byte aligned
  *   workspace  dev, 256-byte aligned, fp32_prefill_workspace_bytes
- * A request of no tokens keeps its state. B == 0 or T == 0 is a no-op. bf16 inputs with d in
+ * Inputs must be finite: a NaN or infinity may reach any readout of its 64-token chunk. At most
+ * 65,536 heads. A request of no tokens keeps its state. B == 0 or T == 0 is a no-op. bf16 inputs with d in
  * {64, 128} and a decay per head (SCALAR, PER_HEAD) run chunk by chunk on the matrix cores, with
  * binary32 states, sums and decays; other forms token by token in binary32.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (d), SLOT_INDEX (debug), HIP. */

@@ -442,6 +442,7 @@ damp_status run_prefill(bool delta, float* pool, int32_t num_slots, int32_t H, i
     return fail(DAMP_ERR_INVALID_ARGUMENT, "q, k, v and out must be 16-byte aligned");
   if (!aligned(slot_idx, 4) || !aligned(cu, 4) || !aligned(resume, 4) || !aligned(alpha, 4) || !aligned(beta, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned input pointer (need natural alignment)");
+  if (H > 65536) return fail(DAMP_ERR_UNSUPPORTED, "num_heads = %d: prompts take at most 65,536 heads", H);
   if ((static_cast<int64_t>(T) / 64 + B) * H > 0x7fffffffLL / 8)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "T = %d tokens of %d requests with %d heads exceed the grid limit", T, B, H);
   const int64_t need = damp::prefill_ws_bytes(delta, d_k, decay, dt == DAMP_BF16, B, T, H);

@@ -86,7 +86,8 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
   constexpr int RPL = D / 4;
   __shared__ __align__(16) float sk[kTokBlock][D], sq[kTokBlock][D];
   __shared__ __align__(16) float sa[DECAY == DECAY_KEY ? kTokBlock : 1][DECAY == DECAY_KEY ? D : 4];
-  __shared__ float sg[kTokBlock], sb[kTokBlock], sv[kTokBlock][16];
+  __shared__ float sg[kTokBlock], sb[kTokBlock];
+  __shared__ __align__(16) float sv[kTokBlock][16];
   const int lane = __builtin_amdgcn_workitem_id_x();
   const int unit = __builtin_amdgcn_workgroup_id_x() / (D / 16), c0 = (__builtin_amdgcn_workgroup_id_x() % (D / 16)) * 16;
   const int b = unit / a.H, head = unit - b * a.H;
@@ -101,24 +102,89 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
 #pragma unroll
   for (int i = 0; i < RPL; ++i) S[i] = resume ? pool[i * D] : 0.0f;
 
+  // A block of tokens is on its way in registers while the one before is computed: 16-byte pieces of k
+  // and q (and of per-key gates), through resources that end with the request's last row.
+  constexpr int E = BF16 ? 2 : 4, PR = D * E / 16, NP = (kTokBlock * PR + 63) / 64;      // pieces per row, per lane
+  constexpr int PA = D / 4, NA = DECAY == DECAY_KEY ? (kTokBlock * PA + 63) / 64 : 0;
+  const uint32_t ostep = static_cast<uint32_t>(a.H) * D * E;
+  struct Block {
+    uint4 k[NP], q[NP], al[NA ? NA : 1];
+    uint32_t v[4];
+    float gate, beta;
+  } in;
+  const auto load = [&](int t0) {
+    const int rows = min(kTokBlock, sp.end - t0);
+    const int64_t at = (int64_t(t0) * a.H + head) * D;
+    const auto region = [&](const void* p, int e) {
+      return make_rsrc(static_cast<const uint8_t*>(p) + at * e, (rows - 1) * (a.H * D * e) + D * e);
+    };
+    const rsrc_t kr = region(a.k, E), qr = region(a.q, E), vr = region(a.v, E);
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int x = lane + 64 * j;
+      const uint32_t off = x / PR * ostep + x % PR * 16;
+      const auto kk = __builtin_amdgcn_raw_buffer_load_b128(kr, off, 0, 0), qq = __builtin_amdgcn_raw_buffer_load_b128(qr, off, 0, 0);
+      in.k[j] = make_uint4(kk[0], kk[1], kk[2], kk[3]);
+      in.q[j] = make_uint4(qq[0], qq[1], qq[2], qq[3]);
+    }
+    if constexpr (NA > 0) {
+      const rsrc_t ar = region(a.alpha, 4);
+#pragma unroll
+      for (int j = 0; j < NA; ++j) {
+        const int x = lane + 64 * j;
+        const auto aa = __builtin_amdgcn_raw_buffer_load_b128(ar, x / PA * (a.H * D * 4) + x % PA * 16, 0, 0);
+        in.al[j] = make_uint4(aa[0], aa[1], aa[2], aa[3]);
+      }
+    }
+    // 4 value columns of token lane / 4
+    const uint32_t voff = lane / 4 * ostep + (c0 + lane % 4 * 4) * E;
+    if constexpr (BF16) {
+      const auto vv = __builtin_amdgcn_raw_buffer_load_b64(vr, voff, 0, 0);
+      in.v[0] = vv[0] << 16; in.v[1] = vv[0] & 0xffff0000u; in.v[2] = vv[1] << 16; in.v[3] = vv[1] & 0xffff0000u;
+    } else {
+      const auto vv = __builtin_amdgcn_raw_buffer_load_b128(vr, voff, 0, 0);
+      in.v[0] = vv[0]; in.v[1] = vv[1]; in.v[2] = vv[2]; in.v[3] = vv[3];
+    }
+    const int64_t tok = int64_t(t0 + min(lane, rows - 1)) * a.H + head;
+    if constexpr (DECAY != DECAY_KEY) in.gate = a.alpha[DECAY == DECAY_HEAD ? head : tok];
+    if constexpr (DELTA) in.beta = a.beta[tok];
+  };
+  const auto spread = [](float* to, uint4 v) {   // 16 bytes of k or q as binary32
+    if constexpr (BF16) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        reinterpret_cast<float4*>(to)[h] = make_float4(bf16_lo(w[2 * h]), bf16_hi(w[2 * h]), bf16_lo(w[2 * h + 1]), bf16_hi(w[2 * h + 1]));
+    } else {
+      *reinterpret_cast<uint4*>(to) = v;
+    }
+  };
+  load(sp.begin);
   for (int t0 = sp.begin; t0 < sp.end; t0 += kTokBlock) {
     const int n = min(kTokBlock, sp.end - t0);
     __syncthreads();
-    for (int x = lane; x < n * D; x += 64) {
-      const int t = x / D, i = x % D;
-      const int64_t at = (int64_t(t0 + t) * a.H + head) * D + i;
-      sk[t][i] = load_in<BF16>(a.k, at);
-      sq[t][i] = load_in<BF16>(a.q, at);
-      if constexpr (DECAY == DECAY_KEY) sa[t][i] = a.alpha[at];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int x = lane + 64 * j;
+      if (NP * 64 == kTokBlock * PR || x < kTokBlock * PR) {
+        spread(&sk[x / PR][x % PR * (16 / E)], in.k[j]);
+        spread(&sq[x / PR][x % PR * (16 / E)], in.q[j]);
+      }
     }
-    for (int x = lane; x < n * 16; x += 64)
-      sv[x >> 4][x & 15] = load_in<BF16>(a.v, (int64_t(t0 + (x >> 4)) * a.H + head) * D + c0 + (x & 15));
-    if (lane < n) {
-      const int64_t at = int64_t(t0 + lane) * a.H + head;
-      if constexpr (DECAY != DECAY_KEY) sg[lane] = a.alpha[DECAY == DECAY_HEAD ? head : at];
-      if constexpr (DELTA) sb[lane] = a.beta[at];
+    if constexpr (NA > 0) {
+#pragma unroll
+      for (int j = 0; j < NA; ++j) {
+        const int x = lane + 64 * j;
+        if (NA * 64 == kTokBlock * PA || x < kTokBlock * PA) *reinterpret_cast<uint4*>(&sa[x / PA][x % PA * 4]) = in.al[j];
+      }
+    }
+    *reinterpret_cast<uint4*>(&sv[lane / 4][lane % 4 * 4]) = make_uint4(in.v[0], in.v[1], in.v[2], in.v[3]);
+    if (lane < kTokBlock) {
+      if constexpr (DECAY != DECAY_KEY) sg[lane] = in.gate;
+      if constexpr (DELTA) sb[lane] = in.beta;
     }
     __syncthreads();
+    if (sp.end - t0 > kTokBlock) load(t0 + kTokBlock);
     for (int t = 0; t < n; ++t) {
       float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (DECAY == DECAY_KEY) {

@@ -620,16 +620,21 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
 
   f32x4 S[XT][MD];   // S[x][m][i]: key channel 16 x + 4 g + i, value column col + m
   {
-    // (a resource of no bytes reads as 0)
     const bool some = MODE == LIN_SEGMENTS || (MODE == LIN_WHOLE && a.resume && a.resume[b] != 0);
-    const rsrc_t from = make_rsrc(MODE == LIN_SEGMENTS ? states : pool, some ? D * D * 4 : 0);
+    const rsrc_t from = make_rsrc(MODE == LIN_SEGMENTS ? states : pool, D * D * 4);
 #pragma unroll
     for (int x = 0; x < XT; ++x)
 #pragma unroll
-      for (int m = 0; m < MD; ++m)
+      for (int m = 0; m < MD; ++m) S[x][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (some) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          S[x][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, off_state + 4 * m, (16 * x + i) * D * 4, 0));
+      for (int x = 0; x < XT; ++x)
+#pragma unroll
+        for (int m = 0; m < MD; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            S[x][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, off_state + 4 * m, (16 * x + i) * D * 4, 0));
+    }
   }
 
   // One chunk's rows, in registers until LDS is free for them, through buffer resources that end

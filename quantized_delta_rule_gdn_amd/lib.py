@@ -802,7 +802,7 @@ def kv_build_tables(seq_lens, new_lens, free_pages, block_table, page_size: int,
     _fit(used, "used", torch.int32, (1,), dev)
     with _On(dev, stream) as s:
         _check(load().kv_build_tables(_ptr(seq_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
-                                      page_size, _ptr(block_table), blocks, _ptr(slot_map),
+                                      min(page_size, 1 << 30), _ptr(block_table), blocks, _ptr(slot_map),
                                       _ptr(positions) if positions is not None else None, T, _ptr(cu_new),
                                       _ptr(used), s))
 
@@ -848,8 +848,7 @@ def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=N
     if k_new is not None:
         _fit(k_new, "k_new", torch.bfloat16, (B, Hkv, dc), dev)
         _fit(v_new, "v_new", torch.bfloat16, (B, Hkv, dc), dev)
-    if max_len is None:
-        max_len = blocks * page
+    max_len = min(blocks * page if max_len is None else max_len, 1 << 30)
     L = load()
     with _On(dev, stream) as s:
         ws, nb = _workspace(workspace, L.kv_decode_attention_workspace_bytes(B, Hq, Hkv, dc, max_len), dev)
