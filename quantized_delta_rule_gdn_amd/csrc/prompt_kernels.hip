@@ -22,7 +22,11 @@ namespace damp {
 namespace {
 
 constexpr int kC = 64;         // tokens per chunk
-constexpr int kLd = kC + 8;    // LDS row of a chunk-wide bf16 array: 144 bytes, 16-byte aligned
+// LDS rows, measured on gfx950 (cycles of a wave's access on a busy CU): 16-byte operand reads of 16
+// rows take 4 where the row is an odd number of 32-byte units and 8 where it is an odd number of
+// 16-byte ones; 8-byte writes and reads of them take 16 and 4 against 8 and 2.4. Arrays that are
+// written by 16-byte rows or 2-byte values and read as operands have the former, the others the latter.
+constexpr int kLd = kC + 8;
 
 // Chunks (or segments of `len` tokens) are numbered without a table: those of request b start at
 // begin_b / len + b, which leaves room for each request's last, short one; some numbers are unused.
@@ -578,11 +582,11 @@ struct Segments {
 
 template <int D, int DECAY, int MODE>
 __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a, const Segments sg) {
-  constexpr int KS = D / 32, MD = D / 64, XT = D / 16, LK = D + 8;
+  constexpr int KS = D / 32, MD = D / 64, XT = D / 16, LK = D + 8, LR = D + 16, LP = kC + 16;
   constexpr bool kReadout = MODE != LIN_STATES;
-  __shared__ __align__(16) uint16_t ks[kC][LK];
+  __shared__ __align__(16) uint16_t ks[kC][LR];
   __shared__ __align__(16) uint16_t qs[kReadout ? kC : 1][LK];
-  __shared__ __align__(16) uint16_t pp[2][kReadout ? kC : 1][kLd];
+  __shared__ __align__(16) uint16_t pp[2][kReadout ? kC : 1][LP];
   __shared__ Logs logs[4][kC];                    // of four chunks
   __shared__ __align__(16) float eg[4][kC], wc[4][kC];
   __shared__ double ends[4];
@@ -840,7 +844,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint16_t* from = &ks[32 * x + 8 * g + r / 4][16 * (y + h) + 4 * (r % 4)];
-          kf[h] = load_frag_t(from, from + 4 * LK);
+          kf[h] = load_frag_t(from, from + 4 * LR);
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p)
