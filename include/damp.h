@@ -525,10 +525,12 @@ size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t
  *   alpha      dev fp32 [T][num_heads], [T][num_heads][d] or [num_heads] (by decay), each in [0, 1]
  *   out        dev [T][num_heads][d] of qkv_dtype (the next layer's input type), 16-byte aligned
  *   workspace  dev, 256-byte aligned, fp32_prefill_workspace_bytes
- * Inputs must be finite: a NaN or infinity may reach any readout of its 64-token chunk. At most
- * 65,536 heads. A request of no tokens keeps its state. B == 0 or T == 0 is a no-op. bf16 inputs with d in
- * {64, 128} and a decay per head (SCALAR, PER_HEAD) run chunk by chunk on the matrix cores, with
- * binary32 states, sums and decays; other forms token by token in binary32.
+ * out must not overlap the inputs. Inputs must be finite: a NaN or infinity may reach any readout
+ * of its 64-token chunk (but no other request). A request of no tokens keeps its state. B == 0 or
+ * T == 0 is a no-op. At most 65,536 heads, and (T / 64 + B) * num_heads below 2^24, B * num_heads
+ * below 2^21. bf16 inputs with d in {64, 128} and a decay per head (SCALAR, PER_HEAD) run chunk by
+ * chunk on the matrix cores, with binary32 states, sums and decays; other forms token by token in
+ * binary32.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (d), SLOT_INDEX (debug), HIP. */
 damp_status fp32_linear_prefill(float* pool, int32_t num_slots, int32_t num_heads, int32_t d_k,
                                 int32_t d_v, const int32_t* slot_idx, const int32_t* cu_seqlens,
@@ -552,8 +554,9 @@ damp_status fp32_delta_prefill(float* pool, int32_t num_slots, int32_t num_heads
 /* ---------------------------------------------------------------------------------------
  * Paged key-value cache, for the full-attention layers between the recurrent ones: keys and values
  * in pages, bf16 [num_pages][num_kv_heads][page_size][d] each, d in {64, 128}, page_size a power of
- * two up to 32,768, num_pages * num_kv_heads * page_size below 2^32 - 1. Request b's token at position p lies in page block_table[b][p / page_size], row
- * p mod page_size; its cache slot is page * page_size + row.
+ * two up to 32,768, num_pages * num_kv_heads * page_size below 2^32 - 1. Request b's token at
+ * position p lies in page block_table[b][p / page_size], row p mod page_size; its cache slot is
+ * page * page_size + row.
  * ------------------------------------------------------------------------------------- */
 
 /* The tables of one serving step, in one launch: request b has seq_lens[b] tokens with this step, of
@@ -600,7 +603,7 @@ size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32
  *               at position seq_lens[b] - 1 before the attention reads it (NULL: already stored).
  *               That position's page must be the request's alone; other pages may be shared.
  * Scores, softmax statistics and sums are binary32; the softmax weights are rounded to bf16 for the
- * product with V. B == 0 is a no-op. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
+ * product with V. B * num_q_heads stays below 2^24. B == 0 is a no-op. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
 damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages,
                                 const int32_t* block_table, const int32_t* seq_lens, int32_t B,
                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t d,

@@ -396,6 +396,8 @@ damp_status scratch_for(hipStream_t stream, int32_t** out) {
 }
 
 // ---- linear attention, prompts and the paged cache --------------------------------------------
+constexpr int64_t kMaxGroups = 0xffffff;   // workgroups of 256 threads in a launch
+
 damp_status check_fp32_pool(const float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v) {
   if (num_slots <= 0 || H <= 0)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "num_slots (%d) and num_heads (%d) must be positive", num_slots, H);
@@ -443,7 +445,8 @@ damp_status run_prefill(bool delta, float* pool, int32_t num_slots, int32_t H, i
   if (!aligned(slot_idx, 4) || !aligned(cu, 4) || !aligned(resume, 4) || !aligned(alpha, 4) || !aligned(beta, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned input pointer (need natural alignment)");
   if (H > 65536) return fail(DAMP_ERR_UNSUPPORTED, "num_heads = %d: prompts take at most 65,536 heads", H);
-  if ((static_cast<int64_t>(T) / 64 + B) * H > 0x7fffffffLL / 8)
+  // (a launch takes less than 2^32 threads: 256 a chunk, and 8 workgroups of 256 a state)
+  if ((static_cast<int64_t>(T) / 64 + B) * H > kMaxGroups || static_cast<int64_t>(B) * H > kMaxGroups / 8)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "T = %d tokens of %d requests with %d heads exceed the grid limit", T, B, H);
   const int64_t need = damp::prefill_ws_bytes(delta, d_k, decay, dt == DAMP_BF16, B, T, H);
   if (need > 0 && (!workspace || !aligned(workspace, kBlockAlign) || workspace_bytes < static_cast<size_t>(need)))
@@ -1256,7 +1259,7 @@ size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32
                                            int32_t max_len) {
   if (B <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || (d != 64 && d != 128) ||
       max_len < 0 || max_len > (1 << 30) ||
-      damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > 0x7fffffffLL)
+      damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > kMaxGroups)
     return 0;
   return damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);
 }
@@ -1279,8 +1282,8 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages, con
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_new, 16) ||
       !aligned(v_new, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages, k_new, v_new and out must be 16-byte, block_table and seq_lens 4-byte aligned");
-  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > 0x7fffffffLL ||
-      static_cast<int64_t>(B) * num_q_heads > 0x7fffffffLL)
+  if (damp::kv_attention_grid(B, num_q_heads, num_kv_heads, max_len) > kMaxGroups ||
+      static_cast<int64_t>(B) * num_q_heads > kMaxGroups)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_len = %d exceeds the grid limit", B, max_len);
   const size_t need = damp::kv_attention_ws_bytes(B, num_q_heads, num_kv_heads, d, max_len);
   if (need > 0 && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))

@@ -77,9 +77,9 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(const TableArgs 
   const int first = __builtin_amdgcn_workgroup_id_x() * kTabThreads + tid, step = __builtin_amdgcn_grid_size_x();
   for (int b = first; b <= a.B; b += step) a.cu_new[b] = b < a.B ? tok[b] : tokens;
   if (first == 0) a.used[0] = pages;
-  for (int p = first; p < pages; p += step) {
-    const int b = owner_of(pg, a.B, p);
-    const int j = request_of(a, b).have + p - pg[b];
+  for (int64_t p = first; p < pages; p += step) {
+    const int b = owner_of(pg, a.B, static_cast<int>(p));
+    const int j = request_of(a, b).have + static_cast<int>(p) - pg[b];
     if (j >= 0 && j < a.max_blocks) a.table[int64_t(b) * a.max_blocks + j] = p < a.num_free ? a.free_pages[p] : -1;
   }
   // a token's page comes from the table where the request had it before and from the free list
@@ -94,7 +94,10 @@ __global__ __launch_bounds__(kTabThreads) void kv_tables_kernel(const TableArgs 
       const int j = pos >> a.page_log2;
       int id = -1;
       if (j >= 0 && j < r.have) id = a.table[int64_t(b) * a.max_blocks + j];
-      else if (j >= r.have && j < r.have + r.need && pg[b] + j - r.have < a.num_free) id = a.free_pages[pg[b] + j - r.have];
+      else if (j >= r.have && j < r.have + r.need) {
+        const int p = pg[b] + j - r.have;
+        if (p >= 0 && p < a.num_free) id = a.free_pages[p];
+      }
       if (id >= 0) slot = (int64_t(id) << a.page_log2) + (pos & ((1 << a.page_log2) - 1));
     }
     a.slot_map[t] = slot;
@@ -190,7 +193,8 @@ __device__ __forceinline__ int chunk_of(const AttnArgs& a, const AttnPlan& plan,
   for (int b = __builtin_amdgcn_workitem_id_x(); b < a.B; b += 256) total += length_of(a, b);
   total = block_sum(total, sh);
   const int64_t chunk = (total + plan.per_unit - 1) / plan.per_unit;
-  return static_cast<int>(max((chunk + kAttnLeast - 1) / kAttnLeast * kAttnLeast, int64_t(kAttnLeast)));
+  // (no request is longer than 2^30: a longer chunk would be the same)
+  return static_cast<int>(min(max((chunk + kAttnLeast - 1) / kAttnLeast * kAttnLeast, int64_t(kAttnLeast)), int64_t(1) << 30));
 }
 
 constexpr int kAttnPages = 1024;   // page addresses held in LDS at a time
@@ -266,130 +270,130 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
   // page addresses for as many tokens at a time as LDS holds (4 tiles at least)
   constexpr int kRun = P16 ? kAttnPages * 16 : kAttnPages;
   for (int from = begin; from < end; from += kRun) {
-  const int to = min(from + kRun, end);
-  const int p0 = from >> a.page_log2, np = ((to - 1) >> a.page_log2) - p0 + 1;
-  __syncthreads();
-  if (tid == 0) bad = 0;
-  __syncthreads();
-  for (int i = tid; i < np; i += 256) {
-    const int pid = a.table[int64_t(b) * a.max_blocks + p0 + i];
-    const bool fine = pid >= 0 && pid < a.num_pages;
-    first_row[i] = fine ? (static_cast<uint32_t>(pid) * a.Hkv + kvh) << a.page_log2 : kNone;
-    if (!fine) bad = 1;
-  }
-  __syncthreads();
-  // this call's key and value go into the cache first; the workgroup then reads them from there
-  if (a.k_new && whole == len && to == len) {
-    const int pos = len - 1;
-    const uint32_t page = first_row[(pos >> a.page_log2) - p0];
-    if (page != kNone && tid < D / 4) {
-      const int64_t row = int64_t(page) + (pos & in_page);
-      const int64_t src = int64_t(b) * a.Hkv + kvh;
-      const int piece = tid % (D / 8);
-      if (tid < D / 8) reinterpret_cast<uint4*>(a.k_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.k_new)[src * (D / 8) + piece];
-      else reinterpret_cast<uint4*>(a.v_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.v_new)[src * (D / 8) + piece];
+    const int to = min(from + kRun, end);
+    const int p0 = from >> a.page_log2, np = ((to - 1) >> a.page_log2) - p0 + 1;
+    __syncthreads();
+    if (tid == 0) bad = 0;
+    __syncthreads();
+    for (int i = tid; i < np; i += 256) {
+      const int pid = a.table[int64_t(b) * a.max_blocks + p0 + i];
+      const bool fine = pid >= 0 && pid < a.num_pages;
+      first_row[i] = fine ? (static_cast<uint32_t>(pid) * a.Hkv + kvh) << a.page_log2 : kNone;
+      if (!fine) bad = 1;
     }
     __syncthreads();
-  }
-  const bool clean = bad == 0;
-  for (int t0 = from + wv * kAttnTile; t0 < to; t0 += 4 * kAttnTile) {
-    // (rows past the end lie in the last page or repeat its last row; what they give is masked)
-    Frag kf[2][KS];
-    uint32_t vr[8][VW];
-    uint32_t dead = 0;   // bit i: this lane's value row i is not part of the request
-    const auto load_v = [&](const uint8_t* vp, int i) {
-      if constexpr (VW == 4) {
-        const uint4 w = *reinterpret_cast<const uint4*>(vp);
-        vr[i][0] = w.x; vr[i][1] = w.y; vr[i][2] = w.z; vr[i][3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(vp);
-        vr[i][0] = w.x; vr[i][1] = w.y;
+    // this call's key and value go into the cache first; the workgroup then reads them from there
+    if (a.k_new && whole == len && to == len) {
+      const int pos = len - 1;
+      const uint32_t page = first_row[(pos >> a.page_log2) - p0];
+      if (page != kNone && tid < D / 4) {
+        const int64_t row = int64_t(page) + (pos & in_page);
+        const int64_t src = int64_t(b) * a.Hkv + kvh;
+        const int piece = tid % (D / 8);
+        if (tid < D / 8) reinterpret_cast<uint4*>(a.k_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.k_new)[src * (D / 8) + piece];
+        else reinterpret_cast<uint4*>(a.v_pages)[row * (D / 8) + piece] = reinterpret_cast<const uint4*>(a.v_new)[src * (D / 8) + piece];
       }
-    };
-    if constexpr (P16) {
-      int64_t base[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int pos = t0 + 16 * h;
-        const uint32_t page = __builtin_amdgcn_readfirstlane(first_row[min((pos >> a.page_log2) - p0, np - 1)]);
-        if (page == kNone) dead |= 0xfu << (4 * h);
-        base[h] = int64_t(page == kNone ? 0 : page + (pos & in_page)) * (D * 2);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(a.k_pages + base[h] + k_off + x * 64);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) load_v(a.v_pages + base[i >> 2] + v_off + (i & 3) * (D * 2), i);
-    } else {
-      const auto row_of = [&](int pos) -> uint32_t {   // cache row of a position, kNone where there is none
-        const uint32_t page = first_row[(pos >> a.page_log2) - p0];
-        return page == kNone ? kNone : page + (pos & in_page);
-      };
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t row = row_of(min(t0 + 16 * h + r, to - 1));
-        const uint8_t* kp = a.k_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + g * 16;
-#pragma unroll
-        for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(kp + x * 64);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t row = row_of(min(t0 + 16 * (i >> 2) + 4 * g + (i & 3), to - 1));
-        if (row == kNone) dead |= 1u << i;
-        load_v(a.v_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + r * (DPL * 2), i);
-      }
+      __syncthreads();
     }
-    f32x4 s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int x = 0; x < KS; ++x)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] = mfma(kf[h][x], qf[x], s[h]);
-    float p[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * a.scale_log2;
-    if (!clean || t0 + kAttnTile > to) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if ((dead >> i & 1) || t0 + 16 * (i >> 2) + 4 * g + (i & 3) >= to) {
-          p[i] = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vr[i][w] = 0;   // whatever lies there: 0 * NaN is NaN
+    const bool clean = bad == 0;
+    for (int t0 = from + wv * kAttnTile; t0 < to; t0 += 4 * kAttnTile) {
+      // (rows past the end lie in the last page or repeat its last row; what they give is masked)
+      Frag kf[2][KS];
+      uint32_t vr[8][VW];
+      uint32_t dead = 0;   // bit i: this lane's value row i is not part of the request
+      const auto load_v = [&](const uint8_t* vp, int i) {
+        if constexpr (VW == 4) {
+          const uint4 w = *reinterpret_cast<const uint4*>(vp);
+          vr[i][0] = w.x; vr[i][1] = w.y; vr[i][2] = w.z; vr[i][3] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(vp);
+          vr[i][0] = w.x; vr[i][1] = w.y;
+        }
+      };
+      if constexpr (P16) {
+        int64_t base[2];
+  #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int pos = t0 + 16 * h;
+          const uint32_t page = __builtin_amdgcn_readfirstlane(first_row[min((pos >> a.page_log2) - p0, np - 1)]);
+          if (page == kNone) dead |= 0xfu << (4 * h);
+          base[h] = int64_t(page == kNone ? 0 : page + (pos & in_page)) * (D * 2);
+        }
+  #pragma unroll
+        for (int h = 0; h < 2; ++h)
+  #pragma unroll
+          for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(a.k_pages + base[h] + k_off + x * 64);
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) load_v(a.v_pages + base[i >> 2] + v_off + (i & 3) * (D * 2), i);
+      } else {
+        const auto row_of = [&](int pos) -> uint32_t {   // cache row of a position, kNone where there is none
+          const uint32_t page = first_row[(pos >> a.page_log2) - p0];
+          return page == kNone ? kNone : page + (pos & in_page);
+        };
+  #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t row = row_of(min(t0 + 16 * h + r, to - 1));
+          const uint8_t* kp = a.k_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + g * 16;
+  #pragma unroll
+          for (int x = 0; x < KS; ++x) kf[h][x] = load_frag(kp + x * 64);
+        }
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t row = row_of(min(t0 + 16 * (i >> 2) + 4 * g + (i & 3), to - 1));
+          if (row == kNone) dead |= 1u << i;
+          load_v(a.v_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + r * (DPL * 2), i);
         }
       }
+      f32x4 s[2];
+  #pragma unroll
+      for (int h = 0; h < 2; ++h) s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  #pragma unroll
+      for (int x = 0; x < KS; ++x)
+  #pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = mfma(kf[h][x], qf[x], s[h]);
+      float p[8];
+  #pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * a.scale_log2;
+      if (!clean || t0 + kAttnTile > to) {
+  #pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if ((dead >> i & 1) || t0 + 16 * (i >> 2) + 4 * g + (i & 3) >= to) {
+            p[i] = -INFINITY;
+  #pragma unroll
+            for (int w = 0; w < VW; ++w) vr[i][w] = 0;   // whatever lies there: 0 * NaN is NaN
+          }
+        }
+      }
+      float top = mx;
+  #pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__any(top > mx)) {               // (the maximum settles after a few tiles)
+        const float shrink = top == -INFINITY ? 1.0f : pow2(mx - top);
+        mx = top;
+        sum *= shrink;
+  #pragma unroll
+        for (int m = 0; m < DPL; ++m) o[m] *= shrink;
+      }
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      Frag pf;
+  #pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = pow2(p[i] - base);
+        sum += p[i];
+      }
+  #pragma unroll
+      for (int j = 0; j < 4; ++j) pf.w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
+  #pragma unroll
+      for (int m = 0; m < DPL; ++m) {
+        Frag vf;
+  #pragma unroll
+        for (int j = 0; j < 4; ++j)
+          vf.w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][m / 2], vr[2 * j][m / 2], m % 2 ? 0x07060302u : 0x05040100u);
+        o[m] = mfma(vf, pf, o[m]);
+      }
     }
-    float top = mx;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i]);
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    if (__any(top > mx)) {               // (the maximum settles after a few tiles)
-      const float shrink = top == -INFINITY ? 1.0f : pow2(mx - top);
-      mx = top;
-      sum *= shrink;
-#pragma unroll
-      for (int m = 0; m < DPL; ++m) o[m] *= shrink;
-    }
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    Frag pf;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[i] = pow2(p[i] - base);
-      sum += p[i];
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) pf.w[j] = pack_bf16(p[2 * j], p[2 * j + 1]);
-#pragma unroll
-    for (int m = 0; m < DPL; ++m) {
-      Frag vf;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        vf.w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][m / 2], vr[2 * j][m / 2], m % 2 ? 0x07060302u : 0x05040100u);
-      o[m] = mfma(vf, pf, o[m]);
-    }
-  }
   }
   sum += __shfl_xor(sum, 16);
   sum += __shfl_xor(sum, 32);

@@ -99,8 +99,8 @@ __device__ __forceinline__ Frag load_frag_t(const uint16_t* rows_lo, const uint1
 // 2^x with results below binary32's normal range flushed or subnormal (v_exp_f32).
 __device__ __forceinline__ float pow2(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// log2 of a decay; 0 (or a negative or subnormal value) counts as 2^-4000, whose products are 0.
-__device__ __forceinline__ float log2_decay(float a) { return a >= 0x1p-126f ? __builtin_amdgcn_logf(a) : -4000.0f; }
+// log2 of a decay; 0 (or a negative or subnormal value) counts as 2^-4000, whose products are 0. NaN stays NaN.
+__device__ __forceinline__ float log2_decay(float a) { return a < 0x1p-126f ? -4000.0f : __builtin_amdgcn_logf(a); }
 
 // Running sums over the 64 lanes of a wave, in binary64.
 __device__ __forceinline__ double wave_scan(double x, int lane) {

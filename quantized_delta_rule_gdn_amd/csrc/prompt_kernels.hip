@@ -84,10 +84,9 @@ __device__ __forceinline__ int request_by_length(const PromptArgs& a, int i) {
 }
 
 // One lane's running sum of log2 decays over a chunk (lane = token; tokens past n add nothing).
-template <int DECAY>
 __device__ __forceinline__ double chunk_logs(const PromptArgs& a, int t0, int n, int head, int lane) {
   float l = 0.0f;
-  if (lane < n) l = log2_decay(a.alpha[DECAY == DECAY_HEAD ? head : (int64_t(t0 + lane) * a.H + head)]);
+  if (lane < n) l = log2_decay(a.alpha[int64_t(t0 + lane) * a.H + head]);
   return wave_scan(static_cast<double>(l), lane);
 }
 
@@ -160,7 +159,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
 #pragma unroll
   for (int x = 0; x < KS; ++x) qf[x] = load_frag(qp + row0 + min(16 * w + r, pc.n - 1) * rstep + x * 32 + g * 8);
   if (w == 0) {
-    const double gs = chunk_logs<DECAY_SCALAR>(a, pc.t0, pc.n, head, lane);
+    const double gs = chunk_logs(a, pc.t0, pc.n, head, lane);
     const double end = __shfl(gs, 63);
     logs[lane] = split_logs(gs);
     beta[lane] = lane < pc.n ? a.beta[int64_t(pc.t0 + lane) * a.H + head] : 0.0f;

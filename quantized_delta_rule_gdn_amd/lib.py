@@ -693,6 +693,8 @@ def _workspace(workspace, nbytes, dev):
         return 0, 0
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     _fit(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace has {workspace.numel()} bytes, {nbytes} needed")
@@ -789,8 +791,11 @@ def kv_build_tables(seq_lens, new_lens, free_pages, block_table, page_size: int,
     dev = _first(seq_lens, "seq_lens", torch.int32)
     B = seq_lens.shape[0]
     _fit(new_lens, "new_lens", torch.int32, (B,), dev)
+    for name, t in (("free_pages", free_pages), ("slot_map", slot_map)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
     _fit(free_pages, "free_pages", torch.int32, (free_pages.numel(),), dev)
-    if block_table.dim() != 2:
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     blocks = block_table.shape[1]
     _fit(block_table, "block_table", torch.int32, (B, blocks), dev)
@@ -838,7 +843,7 @@ def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=N
     if d != dc:
         raise ValueError(f"q has {dc} channels, the pages {d}")
     _fit(out, "out", torch.bfloat16, (B, Hq, dc), dev)
-    if block_table.dim() != 2:
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     blocks = block_table.shape[1]
     _fit(block_table, "block_table", torch.int32, (B, blocks), dev)

@@ -42,7 +42,8 @@ REFUSED = [
     (dict(B=-1), BAD, "B"), (dict(T=-1), BAD, "T"), (dict(dt=2), BAD, "qkv_dtype"), (dict(decay=3), BAD, "decay"), (dict(pool=None), BAD, "pool"),
     (dict(slots=0), BAD, "num_slots"), (dict(dk=8, dv=8), UNSUP, "supported"), (dict(dk=64, dv=32), UNSUP, "supported"), (dict(cu=None), BAD, "NULL"),
     (dict(out=None), BAD, "NULL"), (dict(q=X + 8), BAD, "16-byte"), (dict(out=X + 2), BAD, "16-byte"), (dict(cu=X + 2), BAD, "misaligned"),
-    (dict(resume=X + 1), BAD, "misaligned"), (dict(alpha=X + 1), BAD, "misaligned"), (dict(B=2 ** 28, H=64), BAD, "grid limit")]
+    (dict(resume=X + 1), BAD, "misaligned"), (dict(alpha=X + 1), BAD, "misaligned"), (dict(B=2 ** 28, H=64), BAD, "grid limit"),
+    (dict(H=65537), UNSUP, "65,536"), (dict(B=2 ** 21, H=1), BAD, "grid limit"), (dict(T=2 ** 31 - 1, H=1), BAD, "grid limit"), (dict(T=2 ** 30, H=2), BAD, "grid limit")]
 
 
 @pytest.mark.parametrize("change,status,text", REFUSED)
@@ -88,7 +89,8 @@ APP_OK = dict(k=X, v=X, slots=X, T=1, H=2, d=64, kp=X, vp=X, pages=3, page=16, s
 
 @pytest.mark.parametrize("change,status,text", [
     (dict(T=-1), BAD, "T"), (dict(H=0), BAD, "num_kv_heads"), (dict(pages=0), BAD, "num_pages"), (dict(d=96), UNSUP, "supports"), (dict(page=3), UNSUP, "power"),
-    (dict(k=None), BAD, "NULL"), (dict(vp=None), BAD, "NULL"), (dict(kp=X + 8), BAD, "16-byte"), (dict(slots=X + 4), BAD, "8-byte")])
+    (dict(k=None), BAD, "NULL"), (dict(vp=None), BAD, "NULL"), (dict(kp=X + 8), BAD, "16-byte"), (dict(slots=X + 4), BAD, "8-byte"),
+    (dict(pages=2 ** 17, page=32768, H=1), UNSUP, "2^32"), (dict(pages=2 ** 31 - 1, page=32768), UNSUP, "2^32")])
 def test_append_refusals(change, status, text):
     assert _call("kv_append", APP, APP_OK, **change) == status and text in lib.last_error()
     assert _call("kv_append", APP, APP_OK, T=0) == OK
@@ -104,7 +106,8 @@ ATT_OK = dict(q=X, kp=X, vp=X, table=X, lens=X, B=1, Hq=4, Hkv=2, d=64, pages=3,
     (dict(Hq=3), BAD, "multiple"), (dict(Hq=0), BAD, "multiple"), (dict(Hkv=0), BAD, "num_kv_heads"), (dict(d=32), UNSUP, "supports"),
     (dict(page=12), UNSUP, "power"), (dict(q=None), BAD, "NULL"), (dict(table=None), BAD, "NULL"), (dict(kn=X), BAD, "together"), (dict(vn=X), BAD, "together"),
     (dict(out=X + 8), BAD, "16-byte"), (dict(kn=X, vn=X + 2), BAD, "16-byte"), (dict(lens=X + 2), BAD, "4-byte"),
-    (dict(B=2 ** 30), BAD, "grid limit"), (dict(max_len=1 << 20, ws=None), BAD, "workspace"), (dict(max_len=1 << 20, wsn=16), BAD, "workspace"),
+    (dict(B=2 ** 30), BAD, "grid limit"), (dict(B=2 ** 20, Hq=16, Hkv=1), BAD, "grid limit"), (dict(pages=2 ** 20, page=4096), UNSUP, "2^32"),
+    (dict(max_len=1 << 20, ws=None), BAD, "workspace"), (dict(max_len=1 << 20, wsn=16), BAD, "workspace"),
     (dict(max_len=1 << 20, ws=X + 4), BAD, "workspace")])
 def test_attention_refusals(change, status, text):
     assert _call("kv_decode_attention", ATT, ATT_OK, **change) == status and text in lib.last_error()

@@ -250,6 +250,83 @@ def test_prompt_in_parts_equals_steps(delta):
     assert float((out.float() - out2.float()).abs().max()) <= 2.0 ** -7 * float(out.float().abs().max())
 
 
+@RULES
+@pytest.mark.parametrize("d,heads", [(64, 90), (128, 33)])
+def test_prompts_of_many_heads(delta, d, heads):
+    """More states than fill the chip: 32 value columns a workgroup in the delta rule's chain (and whole prompts of linear attention)."""
+    _run(delta, [70, 130, 3], heads, d, "bf16", "token", resume=[1, 0, 1], seed=heads)
+
+
+@RULES
+@pytest.mark.parametrize("heads", [2, 8])
+@pytest.mark.parametrize("requests", [32, 33, 70])
+def test_many_prompts(delta, requests, heads):
+    """Up to 32 requests start the longest first, more as they come; several of the same length, some without tokens."""
+    rng = np.random.default_rng([requests, heads])
+    lens = [int(x) for x in rng.choice([0, 1, 17, 64, 65, 90], requests)]
+    _run(delta, lens, heads, 64, "bf16", "token", resume=[i % 2 for i in range(requests)], seed=requests)
+
+
+@RULES
+@pytest.mark.parametrize("dtype,d,form", [("bf16", 64, "token"), ("bf16", 128, "token"), ("fp32", 32, "token"), ("bf16", 32, "key")])
+def test_nan_in_one_prompt_stays_there(delta, dtype, d, form):
+    """A NaN gate, key or value makes the states of its own request NaN and leaves the other requests' results as they were."""
+    H, lens = 2, [70, 40, 66]
+    T = sum(lens)
+    cu = torch.tensor([0, 70, 110, 176], dtype=torch.int32, device="cuda")
+    sl = torch.arange(3, dtype=torch.int32, device="cuda")
+    x = [y.cuda() for y in _inputs(51, T, H, d, dtype, form)]
+
+    def call(q, k, v, a, b):
+        pool, out = torch.zeros((3, H, d, d), device="cuda"), torch.zeros_like(v)
+        if delta:
+            lib.fp32_delta_prefill(pool, sl, cu, q, k, v, a, b, out)
+        else:
+            lib.fp32_linear_prefill(pool, sl, cu, q, k, v, a, out)
+        torch.cuda.synchronize()
+        return pool, out
+
+    pool, out = call(*x)
+    for which in (1, 2, 3):                        # k, v, alpha of the middle request's first and last token
+        for row in (70, 109):
+            y = [z.clone() for z in x]
+            y[which][row] = float("nan")
+            p, o = call(*y)
+            assert bool(p[1].isnan().all()), f"input {which}, row {row}"
+            assert torch.equal(p[[0, 2]], pool[[0, 2]]) and torch.equal(o[:70], out[:70]) and torch.equal(o[110:], out[110:])
+
+
+@RULES
+def test_cut_prompts_in_a_graph(delta):
+    """Long prompts of few heads (linear attention in segments, over three launches), replayed."""
+    H, d, T = 2, 64, 1600
+    q, k, v, a, b = (x.cuda() for x in _inputs(61, T, H, d, "bf16", "token"))
+    cu = torch.tensor([0, 1300, 1600], dtype=torch.int32, device="cuda")
+    sl, one = torch.tensor([1, 0], dtype=torch.int32, device="cuda"), torch.ones(2, dtype=torch.int32, device="cuda")
+    start = torch.randn((2, H, d, d), generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    eager, graphed, oe, og = start.clone(), start.clone(), torch.empty_like(v), torch.empty_like(v)
+
+    def call(pool, out):
+        if delta:
+            lib.fp32_delta_prefill(pool, sl, cu, q, k, v, a, b, out, resume=one)
+        else:
+            lib.fp32_linear_prefill(pool, sl, cu, q, k, v, a, out, resume=one)
+
+    call(start, og)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(graphed, og)
+    noise = torch.zeros(1 << 20, device="cuda")
+    for i in range(4):
+        cu.copy_(torch.tensor([0, 1300 - 257 * i, 1600], dtype=torch.int32))
+        call(eager, oe)
+        g.replay()
+        noise.add_(1.0)
+        torch.cuda.synchronize()
+        assert torch.equal(oe, og) and torch.equal(eager, graphed), f"replay {i}"
+
+
 def test_prompt_refusals():
     H, d, T = 2, 64, 10
     q, k, v, a, b = (x.cuda() for x in _inputs(1, T, H, d, "bf16", "token"))
