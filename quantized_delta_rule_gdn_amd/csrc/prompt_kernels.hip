@@ -129,6 +129,8 @@ __device__ __forceinline__ f32x4 mul16_tile(const float* A, f32x4 m, int ld, f32
 // 16: each wave inverts its diagonal block by forward substitution (a column per lane), then
 // blocks are joined two by two, [[X, 0], [Y, Z]]^-1 = [[X', 0], [-Z' Y X', Z']], with binary32
 // matrix instructions: no power of A is formed, so the result is as good as forward substitution.
+// Bound by its stream: q and k in, 40.5 KB of workspace a chunk and head out. 16,384 tokens x 32 heads,
+// d = 128: 138 us for 558 MB moved (302 read, 256 written), 4.0 TB/s of the 4.8 a copy reaches.
 template <int D>
 __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, LK = D + 8, LF = kC + 4;
@@ -266,6 +268,11 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
 // loads only its own rows of Q, X and P, straight into operand registers, one chunk ahead; K is
 // staged in LDS, where it is read by rows and, transposed, by channels; the state, R and E change
 // hands in LDS as [column][k] arrays of bf16 pieces. Three barriers a chunk.
+// It is bound by the latency of a chunk's way from state to state, and by the state's many products
+// with nothing to overlap them: 1.9 us a chunk (d = 128, 16 columns, one workgroup a CU). One prompt
+// of 16,384 tokens x 32 heads 470-488 us; 8,191 ragged tokens of 16 prompts x 32 heads 181 us. Wider
+// workgroups (8 waves) took as long or longer, and two state pieces instead of three in K S gained 2%
+// and lost the state's last bits.
 template <int D>
 struct DeltaRows {   // one wave's operands of a chunk
   Frag q[D / 32], x[3][2], p[2][2];
@@ -589,9 +596,13 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
 // .. of the state, the values and the readouts, so between the chunks nothing of the state leaves
 // its registers: as the B operand of Q S it is the accumulator tiles as they stand (k permuted:
 // mfma), and Q is read to match. K, Q and K^T are staged in LDS once per chunk for all waves, P is
-// formed by 16 rows per wave. Long prompts of few heads are cut into segments: a first launch
-// (STATES) sums every segment's own state, a scan turns them into the states before each segment,
-// and the readouts of all segments run at once.
+// formed tile by tile by the waves in turn. Long prompts of few heads are cut into segments: a first
+// launch (STATES) sums every segment's own state, a scan turns them into the states before each
+// segment, and the readouts of all segments run at once.
+// Bound by issue (splitting the state and the weights into pieces, their products, the LDS reads):
+// 4.1 us a chunk with one workgroup a CU. 8,191 ragged tokens of 12 prompts x 32 heads, d = 128: 160 us,
+// 71 us where 16 prompts are even, against 64 us of its 307 MB at the rate of a copy; the longest
+// prompt's chain sets the ragged time. 8 waves a workgroup took 84 us where 4 took 72-74.
 enum LinearMode : int { LIN_WHOLE = 0, LIN_STATES = 1, LIN_SEGMENTS = 2 };
 
 struct Segments {
@@ -891,7 +902,8 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
   if (MODE == LIN_STATES && tid == 0) sg.decays[unit] = static_cast<float>(total);
 }
 
-// The segments' own states turned into the states before each segment, 4 values a thread.
+// The segments' own states turned into the states before each segment, 4 values a thread, read and
+// written once: bound by that stream.
 __global__ __launch_bounds__(256) void linear_scan_kernel(const PromptArgs a, const Segments sg, int dd4) {
   const int64_t x = int64_t(__builtin_amdgcn_workgroup_id_x()) * 256 + __builtin_amdgcn_workitem_id_x();
   const int64_t u = x / dd4;
@@ -919,9 +931,13 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const PromptArgs a, co
   }
 }
 
-// Segments of a call: none (whole prompts) where the prompts alone fill the chip.
+// Segments of a call: none (whole prompts) where the prompts alone fill the chip, or where all
+// together are so short that three launches cost more. d = 128, 32 heads, on one MI355X: 8 prompts of
+// 1,024 tokens 83 us whole, 115 us cut; 4 of 2,048 147 and 119 us; one of 8,192 531 and 126 us; one of
+// 512 35 and 38 us. (Between 4 and 8 even prompts whole ones are faster, 95 against 131 us for 7, but the
+// lengths are on the device, and one long prompt among them would take as long as alone.)
 int segment_len(int32_t B, int32_t T, int32_t H) {
-  if (int64_t(B) * H >= 256 || T <= 4 * kC) return 0;
+  if (int64_t(B) * H >= 256 || T <= 8 * kC) return 0;
   const int64_t want = (int64_t(T) * H + 511) / 512;
   return static_cast<int>(std::max<int64_t>((want + kC - 1) / kC * kC, 4 * kC));
 }
@@ -958,8 +974,9 @@ hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
   hipLaunchKernelGGL((delta_chunk_kernel<D>), dim3(chunks), dim3(256), 0, s, a);
   const unsigned units = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H);
   // 32 columns a workgroup read K, Q, X and P half as often, 16 give twice the workgroups. On one
-  // MI355X, d = 128, 32 heads, 8,192 tokens in all: 64 heads' states and more 267-361 us with 32
-  // columns against 329-446 us with 16; 32 states (one prompt) 448 us against 345 us.
+  // MI355X, d = 128, 32 heads, 8,192 tokens in all, with 32 columns against 16: 64 states 264 against
+  // 289 us, 128 states 229 against 288, 2,048 states 287 against 378; 32 states (one prompt) 431
+  // against 321. d = 64: 128 states 138 against 143 us, 64 states 201 against 154.
   if (units * (D / 32) >= 256)
     hipLaunchKernelGGL((delta_chain_kernel<D, 2>), dim3(units * (D / 32)), dim3(256), 0, s, a);
   else
