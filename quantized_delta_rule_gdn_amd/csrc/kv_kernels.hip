@@ -181,10 +181,15 @@ __device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
 
 __device__ __forceinline__ int items_of(int len, int chunk) { return max((len + chunk - 1) / chunk, 1); }
 
-// Sums over the 256 threads of a workgroup (the same in every thread).
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
+// What a workgroup adds up over the requests: up to 64 of them each wave takes for itself, one per lane;
+// more are taken by all 256 threads, and the waves meet in LDS. (One request of 700 tokens 10.6 us
+// against 11.3 with the waves meeting; 1,000 of 100 to 1,500 tokens 133 against 153 us without.)
+__device__ __forceinline__ int requests_step(const AttnArgs& a) { return a.B <= 64 ? 64 : 256; }
+
+__device__ __forceinline__ int64_t requests_sum(const AttnArgs& a, int64_t x, int64_t* sh) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+  if (a.B <= 64) return x;
   __syncthreads();
   if ((__builtin_amdgcn_workitem_id_x() & 63) == 0) sh[__builtin_amdgcn_workitem_id_x() >> 6] = x;
   __syncthreads();
@@ -192,12 +197,54 @@ __device__ __forceinline__ int64_t block_sum(int64_t x, int64_t* sh) {
 }
 
 __device__ __forceinline__ int chunk_of(const AttnArgs& a, const AttnPlan& plan, int64_t* sh) {
+  const int step = requests_step(a);
   int64_t total = 0;
-  for (int b = __builtin_amdgcn_workitem_id_x(); b < a.B; b += 256) total += length_of(a, b);
-  total = block_sum(total, sh);
+  for (int b = __builtin_amdgcn_workitem_id_x() & (step - 1); b < a.B; b += step) total += length_of(a, b);
+  total = requests_sum(a, total, sh);
   const int64_t chunk = (total + plan.per_unit - 1) / plan.per_unit;
   // (no request is longer than 2^30: a longer chunk would be the same)
   return static_cast<int>(min(max((chunk + kAttnLeast - 1) / kAttnLeast * kAttnLeast, int64_t(kAttnLeast)), int64_t(1) << 30));
+}
+
+struct Item {   // part `split` of `splits` of request b; b < 0: none
+  int b, split, splits;
+};
+
+__device__ __forceinline__ Item item_of(const AttnArgs& a, const AttnPlan& plan, int item, int64_t* sh) {
+  if (plan.items == a.B) return Item{item, 0, 1};   // none is cut (4,000 requests of 60 tokens: 30 us, 95 with the search)
+  const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63, wv = tid >> 6;
+  const int chunk = chunk_of(a, plan, sh), step = requests_step(a);
+  int* wave_items = reinterpret_cast<int*>(sh + 4);
+  int* found = wave_items + 4;
+  if (step > 64 && tid == 0) found[0] = -1;
+  for (int b0 = 0, before = 0; b0 < a.B && before <= item; b0 += step) {
+    const int b = b0 + (tid & (step - 1));
+    const int n = b < a.B ? items_of(length_of(a, b), chunk) : 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(incl, o);
+      if (lane >= o) incl += y;
+    }
+    int first = before + incl - n;
+    if (step > 64) {
+      if (lane == 63) wave_items[wv] = incl;
+      __syncthreads();
+      for (int i = 0; i < wv; ++i) first += wave_items[i];
+      if (item >= first && item < first + n) {
+        found[0] = b;
+        found[1] = item - first;
+        found[2] = n;
+      }
+      before += (wave_items[0] + wave_items[1]) + (wave_items[2] + wave_items[3]);
+      __syncthreads();
+    } else if (const uint64_t mine = __ballot(item >= first && item < first + n); mine != 0) {
+      const int l = __builtin_ctzll(mine);
+      return Item{l, item - __builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(n, l)};
+    }
+  }
+  if (step == 64) return Item{-1, 0, 1};
+  return Item{__builtin_amdgcn_readfirstlane(found[0]), __builtin_amdgcn_readfirstlane(found[1]), __builtin_amdgcn_readfirstlane(found[2])};
 }
 
 constexpr int kAttnPages = 1024;   // page addresses held in LDS at a time
@@ -211,9 +258,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
   constexpr int VW = DPL / 2;      // dwords of them
   constexpr uint32_t kNone = 0xffffffffu;
   __shared__ uint32_t first_row[kAttnPages];          // of a page, in rows of this key-value head
-  __shared__ int bad, found_b, found_s;
-  __shared__ int64_t sh[4];
-  __shared__ int wave_items[4];
+  __shared__ int64_t sh[8];
   __shared__ float part_m[4][16], part_l[4][16];
   __shared__ __align__(16) float part_o[4][16][D + 4];
 
@@ -226,31 +271,10 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
   const int G = a.Hq / a.Hkv;
 
   // the request this item belongs to
-  const int chunk = chunk_of(a, plan, sh);
-  if (tid == 0) found_b = -1;
-  for (int b0 = 0, before = 0; b0 < a.B; b0 += 256) {
-    const int n = b0 + tid < a.B ? items_of(length_of(a, b0 + tid), chunk) : 0;
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 63) wave_items[wv] = incl;
-    __syncthreads();
-    int first = before + incl - n;
-    for (int i = 0; i < wv; ++i) first += wave_items[i];
-    if (item >= first && item < first + n) {
-      found_b = b0 + tid;
-      found_s = item - first;
-    }
-    before += (wave_items[0] + wave_items[1]) + (wave_items[2] + wave_items[3]);
-    __syncthreads();
-    if (before > item) break;
-  }
-  const int b = __builtin_amdgcn_readfirstlane(found_b), split = __builtin_amdgcn_readfirstlane(found_s);
+  const Item it = item_of(a, plan, item, sh);
+  const int b = it.b, split = it.split, splits = it.splits;
   if (b < 0) return;
-  const int whole = a.seq_lens[b], len = length_of(a, b), splits = items_of(len, chunk);
+  const int whole = a.seq_lens[b], len = length_of(a, b);
   // its tokens: an even share of the request's, in whole tiles
   const int share = ((len + splits - 1) / splits + kAttnTile - 1) / kAttnTile * kAttnTile;
   const int begin = min(split * share, len), end = min(begin + share, len);
@@ -275,14 +299,11 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
   for (int from = begin; from < end; from += kRun) {
     const int to = min(from + kRun, end);
     const int p0 = from >> a.page_log2, np = ((to - 1) >> a.page_log2) - p0 + 1;
-    __syncthreads();
-    if (tid == 0) bad = 0;
-    __syncthreads();
+    if (from > begin) __syncthreads();       // the last addresses are no longer read
     for (int i = tid; i < np; i += 256) {
       const int pid = a.table[int64_t(b) * a.max_blocks + p0 + i];
       const bool fine = pid >= 0 && pid < a.num_pages;
       first_row[i] = fine ? (static_cast<uint32_t>(pid) * a.Hkv + kvh) << a.page_log2 : kNone;
-      if (!fine) bad = 1;
     }
     __syncthreads();
     // this call's key and value go into the cache first; the workgroup then reads them from there
@@ -298,7 +319,6 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
       }
       __syncthreads();
     }
-    const bool clean = bad == 0;
     for (int t0 = from + wv * kAttnTile; t0 < to; t0 += 4 * kAttnTile) {
       // (rows past the end lie in the last page or repeat its last row; what they give is masked)
       Frag kf[2][KS];
@@ -357,7 +377,7 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
       float p[8];
   #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * a.scale_log2;
-      if (!clean || t0 + kAttnTile > to) {
+      if (__any(dead != 0) || t0 + kAttnTile > to) {
   #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if ((dead >> i & 1) || t0 + 16 * (i >> 2) + 4 * g + (i & 3) >= to) {
@@ -449,8 +469,9 @@ __global__ __launch_bounds__(256) void kv_join_kernel(const AttnArgs a, const At
   const int n = items_of(length_of(a, b), chunk);
   if (n == 1) return;
   int64_t before = 0;
-  for (int x = tid; x < b; x += 256) before += items_of(length_of(a, x), chunk);
-  before = block_sum(before, sh);
+  const int apart = requests_step(a);
+  for (int x = tid & (apart - 1); x < b; x += apart) before += items_of(length_of(a, x), chunk);
+  before = requests_sum(a, before, sh);
   const int G = a.Hq / a.Hkv, units = a.Hkv * plan.tiles;
   const int64_t step = int64_t(units) * plan.heads;      // between a unit's items
   const int64_t first = (before * units + hq / G * plan.tiles + hq % G / 16) * plan.heads + hq % G % 16;

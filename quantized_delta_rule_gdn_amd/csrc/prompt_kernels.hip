@@ -66,9 +66,10 @@ __device__ __forceinline__ Piece segment_of(const PromptArgs& a, int i, int most
 // and share a CU with short ones; each wave finds it for itself, a request per lane. On one MI355X,
 // 8,191 ragged tokens x 32 heads: 16 requests by the delta rule 245 us (255-295 us in the order given,
 // by where the long ones stood), 12 of linear attention 155-158 us (151-170 us). More than 32 requests
-// are taken as they come: for 64 of 128 tokens the search cost 8% (308 us against 284 us).
-__device__ __forceinline__ int request_by_length(const PromptArgs& a, int i) {
-  if (a.B > 32 || a.B == 1) return i;
+// are taken as they come: for 64 of 128 tokens the search cost 8% (308 us against 284 us). Nor does
+// the order matter where every workgroup has a CU to itself (`per_head`: workgroups a head).
+__device__ __forceinline__ int request_by_length(const PromptArgs& a, int i, int per_head) {
+  if (a.B > 32 || a.B * a.H * per_head <= 256) return i;
   const int lane = __builtin_amdgcn_workitem_id_x() & 63;
   int own = -1;
   if (lane < a.B) {
@@ -309,7 +310,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   constexpr int slices = D / NC;
   // the slices of a head read the same K, Q, X and P: one L2 for them
   const Place at = place_of(__builtin_amdgcn_workgroup_id_x(), static_cast<unsigned>(a.B) * a.H, slices);
-  const int c0 = at.part * NC, head = at.item % a.H, b = request_by_length(a, at.item / a.H);
+  const int c0 = at.part * NC, head = at.item % a.H, b = request_by_length(a, at.item / a.H, slices);
   const int64_t slot = a.slot_idx[b];
   if (!slot_in_pool(slot, a.num_slots)) return;
   const Span sp_b = span_of(a, b);
@@ -628,7 +629,7 @@ __global__ __launch_bounds__(256, 2) void linear_chunk_kernel(const PromptArgs a
   const int head = unit % a.H, seg = unit / a.H;
   int b = seg, t_begin, t_end;
   if constexpr (MODE == LIN_WHOLE) {
-    b = request_by_length(a, seg);
+    b = request_by_length(a, seg, 1);
     const Span sp = span_of(a, b);
     t_begin = sp.begin;
     t_end = sp.end;
