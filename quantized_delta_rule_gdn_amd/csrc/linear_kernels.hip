@@ -74,40 +74,65 @@ __global__ __launch_bounds__(LinGeo<D>::NT) void linear_step_kernel(const StepAr
 }
 
 // ---- prompts, token by token -----------------------------------------------------------------
-// One wave per (request, head, 16 value columns): column j of the state only needs column j of v,
-// so the waves are independent and the state stays in registers for the whole prompt (D / 4 rows
-// of one column per lane; the 4 row groups of a wave add up by cross-row lane swaps). Every
-// operation is binary32, in token order. It serves what the chunked form is not built for: fp32
-// inputs, a decay per key channel, d below 64. It is bound by the latency of the token chain:
-// each token's instructions depend on the last's. A prompt of 4,096 tokens x 32 heads, d = 128, with a
-// decay per key channel takes 2.8 ms by the delta rule (0.69 us a token) and 1.9 ms without it.
+// One workgroup per (request, head, 16 value columns): column j of the state only needs column j of
+// v, so workgroups are independent and the state stays in registers for the whole prompt. D / 8
+// neighbouring lanes share a column, 8 rows of it each (4 lanes at d = 16), and add up by DPP; the
+// tokens' keys, queries and gates are staged in LDS for all the waves. Every operation is binary32, in
+// token order. It serves what the chunked form is not built for: fp32 inputs, a decay per key channel,
+// d below 64. It is bound by the latency of the token chain: each token's instructions depend on the
+// last's. With a decay per key channel, bf16, 32 heads, d = 128: a prompt of 4,096 tokens takes 1.17 ms
+// by the delta rule (0.29 us a token) and 0.90 ms without it, 32 prompts of 256 tokens 780 and 610 us.
+// (4 lanes a column, one wave a workgroup: 2.23 and 1.87 ms, 911 and 781 us; it is faster where a
+// prompt is a few tokens and the state's way in and out is all, 277 against 338 us for 256 prompts of
+// 4 tokens, as its lanes read 64 bytes of a row and not 16. 16 lanes a column in workgroups of one wave
+// stage the same rows four times as often: 1.77 ms for the 32 prompts.)
 constexpr int kTokBlock = 16;   // tokens staged in LDS at a time
 
+// Sum over RG neighbouring lanes, the same in each of them (DPP: quad_perm, then mirrored halves).
+template <int RG>
+__device__ __forceinline__ float sum_lanes(float x) {
+  static_assert(RG == 4 || RG == 8 || RG == 16, "4, 8 or 16 lanes");
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0xB1, 0xF, 0xF, true));
+  x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x4E, 0xF, 0xF, true));
+  if constexpr (RG >= 8) x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x141, 0xF, 0xF, true));
+  if constexpr (RG == 16) x += __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), 0x140, 0xF, 0xF, true));
+  return x;
+}
+
+template <int D>
+struct TokGeo {
+  static constexpr int RG = D >= 32 ? D / 8 : 4;   // lanes that share a column
+  static constexpr int QR = D / (4 * RG);          // quads of rows of a lane
+  static constexpr int NT = 16 * RG;               // threads: 16 columns
+};
+
 template <int D, bool DELTA, int DECAY, int BF16>
-__global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
-  constexpr int RPL = D / 4;
+__global__ __launch_bounds__(TokGeo<D>::NT) void prompt_token_kernel(const PromptArgs a) {
+  constexpr int RG = TokGeo<D>::RG, QR = TokGeo<D>::QR, NT = TokGeo<D>::NT;
   __shared__ __align__(16) float sk[kTokBlock][D], sq[kTokBlock][D];
   __shared__ __align__(16) float sa[DECAY == DECAY_KEY ? kTokBlock : 1][DECAY == DECAY_KEY ? D : 4];
   __shared__ float sg[kTokBlock], sb[kTokBlock];
   __shared__ __align__(16) float sv[kTokBlock][16];
-  const int lane = __builtin_amdgcn_workitem_id_x();
+  const int tid = __builtin_amdgcn_workitem_id_x();
   const int unit = __builtin_amdgcn_workgroup_id_x() / (D / 16), c0 = (__builtin_amdgcn_workgroup_id_x() % (D / 16)) * 16;
   const int b = unit / a.H, head = unit - b * a.H;
   const int64_t slot = a.slot_idx[b];
   if (!slot_in_pool(slot, a.num_slots)) return;
   const Span sp = span_of(a, b);
   if (sp.end <= sp.begin) return;
-  const int rg = lane >> 4, c = lane & 15;
-  float* pool = a.pool + ((slot * a.H + head) * D + rg * RPL) * int64_t(D) + c0 + c;
-  float S[RPL];
+  const int rg = tid % RG, c = tid / RG;
+  float* pool = a.pool + ((slot * a.H + head) * D + 4 * rg) * int64_t(D) + c0 + c;
+  f32x4 S[QR];   // S[j][i]: row 4 (rg + RG j) + i
   const bool resume = a.resume && a.resume[b] != 0;
 #pragma unroll
-  for (int i = 0; i < RPL; ++i) S[i] = resume ? pool[i * D] : 0.0f;
+  for (int j = 0; j < QR; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[j][i] = resume ? pool[(4 * RG * j + i) * D] : 0.0f;
 
   // A block of tokens is on its way in registers while the one before is computed: 16-byte pieces of k
   // and q (and of per-key gates), through resources that end with the request's last row.
-  constexpr int E = BF16 ? 2 : 4, PR = D * E / 16, NP = (kTokBlock * PR + 63) / 64;      // pieces per row, per lane
-  constexpr int PA = D / 4, NA = DECAY == DECAY_KEY ? (kTokBlock * PA + 63) / 64 : 0;
+  constexpr int E = BF16 ? 2 : 4, PR = D * E / 16, NP = (kTokBlock * PR + NT - 1) / NT;   // pieces per row, per thread
+  constexpr int PA = D / 4, NA = DECAY == DECAY_KEY ? (kTokBlock * PA + NT - 1) / NT : 0;
   const uint32_t ostep = static_cast<uint32_t>(a.H) * D * E;
   struct Block {
     uint4 k[NP], q[NP], al[NA ? NA : 1];
@@ -123,7 +148,7 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
     const rsrc_t kr = region(a.k, E), qr = region(a.q, E), vr = region(a.v, E);
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int x = lane + 64 * j;
+      const int x = tid + NT * j;
       const uint32_t off = x / PR * ostep + x % PR * 16;
       const auto kk = __builtin_amdgcn_raw_buffer_load_b128(kr, off, 0, 0), qq = __builtin_amdgcn_raw_buffer_load_b128(qr, off, 0, 0);
       in.k[j] = make_uint4(kk[0], kk[1], kk[2], kk[3]);
@@ -133,13 +158,13 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
       const rsrc_t ar = region(a.alpha, 4);
 #pragma unroll
       for (int j = 0; j < NA; ++j) {
-        const int x = lane + 64 * j;
+        const int x = tid + NT * j;
         const auto aa = __builtin_amdgcn_raw_buffer_load_b128(ar, x / PA * (a.H * D * 4) + x % PA * 16, 0, 0);
         in.al[j] = make_uint4(aa[0], aa[1], aa[2], aa[3]);
       }
     }
-    // 4 value columns of token lane / 4
-    const uint32_t voff = lane / 4 * ostep + (c0 + lane % 4 * 4) * E;
+    // 4 value columns of token tid / 4 (those past the block load past the rows: 0)
+    const uint32_t voff = tid / 4 * ostep + (c0 + tid % 4 * 4) * E;
     if constexpr (BF16) {
       const auto vv = __builtin_amdgcn_raw_buffer_load_b64(vr, voff, 0, 0);
       in.v[0] = vv[0] << 16; in.v[1] = vv[0] & 0xffff0000u; in.v[2] = vv[1] << 16; in.v[3] = vv[1] & 0xffff0000u;
@@ -147,7 +172,7 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
       const auto vv = __builtin_amdgcn_raw_buffer_load_b128(vr, voff, 0, 0);
       in.v[0] = vv[0]; in.v[1] = vv[1]; in.v[2] = vv[2]; in.v[3] = vv[3];
     }
-    const int64_t tok = int64_t(t0 + min(lane, rows - 1)) * a.H + head;
+    const int64_t tok = int64_t(t0 + min(tid, rows - 1)) * a.H + head;
     if constexpr (DECAY != DECAY_KEY) in.gate = a.alpha[DECAY == DECAY_HEAD ? head : tok];
     if constexpr (DELTA) in.beta = a.beta[tok];
   };
@@ -167,8 +192,8 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const int x = lane + 64 * j;
-      if (NP * 64 == kTokBlock * PR || x < kTokBlock * PR) {
+      const int x = tid + NT * j;
+      if (NP * NT == kTokBlock * PR || x < kTokBlock * PR) {
         spread(&sk[x / PR][x % PR * (16 / E)], in.k[j]);
         spread(&sq[x / PR][x % PR * (16 / E)], in.q[j]);
       }
@@ -176,39 +201,42 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
     if constexpr (NA > 0) {
 #pragma unroll
       for (int j = 0; j < NA; ++j) {
-        const int x = lane + 64 * j;
-        if (NA * 64 == kTokBlock * PA || x < kTokBlock * PA) *reinterpret_cast<uint4*>(&sa[x / PA][x % PA * 4]) = in.al[j];
+        const int x = tid + NT * j;
+        if (NA * NT == kTokBlock * PA || x < kTokBlock * PA) *reinterpret_cast<uint4*>(&sa[x / PA][x % PA * 4]) = in.al[j];
       }
     }
-    *reinterpret_cast<uint4*>(&sv[lane / 4][lane % 4 * 4]) = make_uint4(in.v[0], in.v[1], in.v[2], in.v[3]);
-    if (lane < kTokBlock) {
-      if constexpr (DECAY != DECAY_KEY) sg[lane] = in.gate;
-      if constexpr (DELTA) sb[lane] = in.beta;
+    if (tid < 4 * kTokBlock) *reinterpret_cast<uint4*>(&sv[tid / 4][tid % 4 * 4]) = make_uint4(in.v[0], in.v[1], in.v[2], in.v[3]);
+    if (tid < kTokBlock) {
+      if constexpr (DECAY != DECAY_KEY) sg[tid] = in.gate;
+      if constexpr (DELTA) sb[tid] = in.beta;
     }
     __syncthreads();
     if (sp.end - t0 > kTokBlock) load(t0 + kTokBlock);
     for (int t = 0; t < n; ++t) {
-      float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if constexpr (DECAY == DECAY_KEY) {
-#pragma unroll
-        for (int i = 0; i < RPL; ++i) S[i] *= sa[t][rg * RPL + i];
-      } else {
-        const float g = sg[t];
-#pragma unroll
-        for (int i = 0; i < RPL; ++i) S[i] *= g;
-      }
+      f32x4 u{0.0f, 0.0f, 0.0f, 0.0f}, p{0.0f, 0.0f, 0.0f, 0.0f}, k[QR];
       float e = sv[t][c];
-      if constexpr (DELTA) {
 #pragma unroll
-        for (int i = 0; i < RPL; ++i) u[i & 3] = fmaf(sk[t][rg * RPL + i], S[i], u[i & 3]);
-        e = sb[t] * (e - sum_row_slots((u[0] + u[1]) + (u[2] + u[3])));
-      }
+      for (int j = 0; j < QR; ++j) {
+        const int row = 4 * (rg + RG * j);
+        k[j] = *reinterpret_cast<const f32x4*>(&sk[t][row]);
+        if constexpr (DECAY == DECAY_KEY) S[j] *= *reinterpret_cast<const f32x4*>(&sa[t][row]);
+        else S[j] *= sg[t];
+        if constexpr (DELTA) {
 #pragma unroll
-      for (int i = 0; i < RPL; ++i) {
-        S[i] = fmaf(sk[t][rg * RPL + i], e, S[i]);
-        p[i & 3] = fmaf(sq[t][rg * RPL + i], S[i], p[i & 3]);
+          for (int i = 0; i < 4; ++i) u[i] = fmaf(k[j][i], S[j][i], u[i]);
+        }
       }
-      const float o = sum_row_slots((p[0] + p[1]) + (p[2] + p[3]));
+      if constexpr (DELTA) e = sb[t] * (e - sum_lanes<RG>((u[0] + u[1]) + (u[2] + u[3])));
+#pragma unroll
+      for (int j = 0; j < QR; ++j) {
+        const f32x4 q = *reinterpret_cast<const f32x4*>(&sq[t][4 * (rg + RG * j)]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          S[j][i] = fmaf(k[j][i], e, S[j][i]);
+          p[i] = fmaf(q[i], S[j][i], p[i]);
+        }
+      }
+      const float o = sum_lanes<RG>((p[0] + p[1]) + (p[2] + p[3]));
       if (rg == 0) {
         const int64_t at = (int64_t(t0 + t) * a.H + head) * D + c0 + c;
         if constexpr (BF16) reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(o);
@@ -217,7 +245,9 @@ __global__ __launch_bounds__(64) void prompt_token_kernel(const PromptArgs a) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < RPL; ++i) pool[i * D] = S[i];
+  for (int j = 0; j < QR; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pool[(4 * RG * j + i) * D] = S[j][i];
 }
 
 template <int D>
@@ -232,16 +262,16 @@ hipError_t linear_step_d(int decay, int bf16, const StepArgs& a, hipStream_t s) 
 
 template <int D>
 hipError_t prompt_token_d(bool delta, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H) * (D / 16));
+  const dim3 grid(static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H) * (D / 16)), block(TokGeo<D>::NT);
   with_decay(decay, [&]<int DECAY>() {
     if (delta) {
       if constexpr (DECAY != DECAY_HEAD) {   // the delta rule takes no fixed decays
-        if (bf16) hipLaunchKernelGGL((prompt_token_kernel<D, true, DECAY, 1>), grid, dim3(64), 0, s, a);
-        else hipLaunchKernelGGL((prompt_token_kernel<D, true, DECAY, 0>), grid, dim3(64), 0, s, a);
+        if (bf16) hipLaunchKernelGGL((prompt_token_kernel<D, true, DECAY, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((prompt_token_kernel<D, true, DECAY, 0>), grid, block, 0, s, a);
       }
     } else {
-      if (bf16) hipLaunchKernelGGL((prompt_token_kernel<D, false, DECAY, 1>), grid, dim3(64), 0, s, a);
-      else hipLaunchKernelGGL((prompt_token_kernel<D, false, DECAY, 0>), grid, dim3(64), 0, s, a);
+      if (bf16) hipLaunchKernelGGL((prompt_token_kernel<D, false, DECAY, 1>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((prompt_token_kernel<D, false, DECAY, 0>), grid, block, 0, s, a);
     }
   });
   return hipGetLastError();
