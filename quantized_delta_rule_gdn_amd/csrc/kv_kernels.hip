@@ -147,7 +147,7 @@ constexpr int kAttnTile = 32;
 
 // The work is shared out on the device, by the requests' actual lengths: with `per_unit` workgroups
 // for each (key-value head, 16 query heads), an item is a run of at most
-// chunk = max(128, total tokens / per_unit) tokens of one request, so there are at most per_unit + B
+// chunk = max(256, total tokens / per_unit) tokens of one request, so there are at most per_unit + B
 // items whatever the lengths, they are of much the same length, and those of full length fill the
 // chip once. (Cut by the longest length the host knows of instead, 64 requests of 128 to 8,192
 // tokens took 244-260 us against 186-197 us of as many bytes in even lengths.)
@@ -158,7 +158,14 @@ struct AttnPlan {
   int items;      // per_unit + B, or B where no request is cut
 };
 
-constexpr int kAttnLeast = 4 * kAttnTile;    // tokens: no item is shorter unless its request is
+constexpr int kAttnLeast = 8 * kAttnTile;    // tokens: no chunk is shorter
+
+// Short requests are not cut at all: the join's launch, and an item's way in and out, cost more than
+// the cutting saves. One MI355X, d = 128, 32 query heads on 8, on the device: 64 requests of up to 512
+// tokens 16 us whole, 27 us cut; of up to 1,024 23 against 30; of up to 2,048 32 against 38. One of 704
+// 9.7 against 10.6, of 1,024 12.1 against 10.1 (but 12 against 15 with the call), of 1,536 17 against
+// 11: past 1,024 only where the requests fill the chip twice over.
+bool uncut(int64_t groups, int32_t max_len) { return max_len <= 1024 || (max_len <= 2048 && groups >= 512); }
 
 AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
   AttnPlan p;
@@ -169,7 +176,7 @@ AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
   const int64_t units = int64_t(Hkv) * p.tiles, resident = 256 * 4;
   const int64_t most = (int64_t(max_len) + kAttnLeast - 1) / kAttnLeast * B;   // no more are ever cut
   p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(resident / units, 1), std::max<int64_t>(most, 1)));
-  p.items = max_len <= kAttnLeast ? B : p.per_unit + B;
+  p.items = uncut(units * B, max_len) ? B : p.per_unit + B;
   return p;
 }
 

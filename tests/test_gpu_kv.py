@@ -178,6 +178,26 @@ def test_attention_many_requests():
     _attend([int(x) for x in rng.integers(0, 400, 300)], 2, 1, 64, 16)
 
 
+@pytest.mark.parametrize("B", [40, 64, 65, 300])
+def test_attention_many_requests_in_a_wide_table(B):
+    """Many requests of which some are cut (the table allows for more than any holds)."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 60, B)]
+    lens[0], lens[B // 2], lens[-1] = 2500, 700, 3100
+    _attend(lens, 4, 2, 64, 16, blocks=200)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(40, 1), (17, 1), (64, 2)])
+def test_attention_many_heads_cut(Hq, Hkv):
+    _attend([3000, 5, 1100], Hq, Hkv, 128, 16)
+
+
+@pytest.mark.parametrize("longest", [1023, 1024, 1025, 2048, 2049])
+def test_attention_around_the_lengths_that_are_cut(longest):
+    _attend([longest, 1, 300], 4, 1, 64, 1)
+    _attend([longest] + [3] * 128, 4, 4, 64, 1)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_attention_scales_and_sharp_scores(d):
     _attend([200, 33], 4, 2, d, 16, scale=0.0)
