@@ -171,11 +171,13 @@ AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
   AttnPlan p;
   p.tiles = (Hq / Hkv + 15) / 16;
   p.heads = std::min(Hq / Hkv, 16);
-  // 4 workgroups a CU: at d = 128 that many are resident by registers and LDS; at d = 64 6 would be,
-  // and 64 requests of 8,192 tokens took 208 us shared out among 6 a CU against 197 us among 4
-  const int64_t units = int64_t(Hkv) * p.tiles, resident = 256 * 4;
+  // 4 workgroups a CU, though 3 are resident at d = 128 (by registers) and 5 at 64: the load evens out.
+  // 64 ragged requests from HBM, d = 128, 32 query heads on 8: 211 us against 217 with 2 a CU. (Where
+  // the cache's pages lie in the on-chip caches fewer, longer items win: 5 requests of 40,000 tokens,
+  // d = 64, 43 us against 37.)
+  const int64_t units = int64_t(Hkv) * p.tiles, wanted = 256 * 4;
   const int64_t most = (int64_t(max_len) + kAttnLeast - 1) / kAttnLeast * B;   // no more are ever cut
-  p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(resident / units, 1), std::max<int64_t>(most, 1)));
+  p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(wanted / units, 1), std::max<int64_t>(most, 1)));
   p.items = uncut(units * B, max_len) ? B : p.per_unit + B;
   return p;
 }
