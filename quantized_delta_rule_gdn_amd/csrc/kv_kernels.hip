@@ -172,9 +172,9 @@ AttnPlan attn_plan(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len) {
   p.tiles = (Hq / Hkv + 15) / 16;
   p.heads = std::min(Hq / Hkv, 16);
   // 4 workgroups a CU, though 3 are resident at d = 128 (by registers) and 5 at 64: the load evens out.
-  // 64 ragged requests from HBM, d = 128, 32 query heads on 8: 211 us against 217 with 2 a CU. (Where
-  // the cache's pages lie in the on-chip caches fewer, longer items win: 5 requests of 40,000 tokens,
-  // d = 64, 43 us against 37.)
+  // 64 ragged requests from HBM, d = 128, 32 query heads on 8: 232-237 us against 237-244 with 2 a CU,
+  // both after 1 GB of other traffic. (Where the pages lie in the on-chip caches fewer, longer items
+  // win: 5 requests of 40,000 tokens, d = 64, 43 us against 37.)
   const int64_t units = int64_t(Hkv) * p.tiles, wanted = 256 * 4;
   const int64_t most = (int64_t(max_len) + kAttnLeast - 1) / kAttnLeast * B;   // no more are ever cut
   p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(wanted / units, 1), std::max<int64_t>(most, 1)));

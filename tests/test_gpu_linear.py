@@ -161,6 +161,14 @@ def test_prompts_of_every_form(delta, d, form, dtype):
     _run(delta, [37, 1, 70], 3, d, dtype, form, resume=[1, 0, 1], seed=d)
 
 
+@RULES
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype,form", [("bf16", "key"), ("fp32", "key"), ("fp32", "token")])
+def test_token_by_token_lengths(delta, d, dtype, form):
+    """Lengths around the blocks of 16 tokens that are staged at a time, rows behind the last request."""
+    _run(delta, [300, 17, 16, 0, 15, 1, 33], 3, d, dtype, form, resume=[1, 0, 1, 0, 0, 1, 0], seed=d + 5, tail=2)
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 def test_prompts_with_a_fixed_decay_per_head(d):
     _run(False, [130, 5, 64], 3, d, "bf16", "head", seed=d)
