@@ -985,20 +985,27 @@ hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// bf16 inputs with one decay per head run in chunks; the rest token by token.
-bool chunked(int d, int decay, int bf16) { return bf16 && (d == 64 || d == 128) && decay != DECAY_KEY; }
+// bf16 inputs with one decay per head run in chunks; the rest token by token. So do calls of the delta
+// rule of few tokens: one launch instead of two, and no chunk's inverse. On one MI355X, d = 128, 32
+// heads, one prompt of 1 token 4.0 us against 13.1, of 16 7.6 against 13.2, of 32 11.9 against 13.3, of
+// 48 16.4 against 13.5; 64 of one token 68 against 127 us. (Only the sum of the lengths is known here:
+// the bounds hold if all tokens are one request's. Linear attention's chunks need one launch too: 3.9 us
+// against 8.5 for one token, but 67 against 43 for 64 requests of one.)
+bool chunked(bool delta, int d, int decay, int bf16, int32_t B, int32_t T) {
+  return bf16 && (d == 64 || d == 128) && decay != DECAY_KEY && !(delta && T <= std::max(32, B));
+}
 
 }  // namespace
 
 int64_t prefill_ws_bytes(bool delta, int d, int decay, int bf16, int32_t B, int32_t T, int32_t H) {
-  if (!chunked(d, decay, bf16)) return 0;
+  if (!chunked(delta, d, decay, bf16, B, T)) return 0;
   if (delta) return (int64_t(T) / kC + B) * H * kDeltaUnit;
   const int len = segment_len(B, T, H);
   return len ? (int64_t(T / len) + B) * H * (int64_t(d) * d + 1) * 4 : 0;
 }
 
 hipError_t launch_prefill(bool delta, int d, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
-  if (!chunked(d, decay, bf16)) return launch_prompt_token(d, delta, decay, bf16, a, s);
+  if (!chunked(delta, d, decay, bf16, a.B, a.T)) return launch_prompt_token(d, delta, decay, bf16, a, s);
   if (!delta) return d == 64 ? linear_d<64>(decay, a, s) : linear_d<128>(decay, a, s);
   return d == 64 ? delta_d<64>(a, s) : delta_d<128>(a, s);
 }

@@ -131,7 +131,8 @@ def _run(delta, lens, H, d, dtype, form, resume=None, slots=None, num_slots=None
             al = a[h].double().expand(n) if form == "head" else a[r, h].double()
             x = [y[r, h].double() for y in (q, k, v)]
             o, X, mag, A, top = ref.prompt(S, *x, al, b[r, h].double() if delta else None)
-            chain = n if (dtype == "fp32" or form == "key" or d < 64) else -(-n // 64)
+            by_token = dtype == "fp32" or form == "key" or d < 64 or (delta and rows <= max(32, B))   # the form the call takes
+            chain = n if by_token else -(-n // 64)
             store = 2.0 ** -8 if dtype == "bf16" else ref.EPS32
             if not delta:
                 e_state = (512 + 8 * chain) * ref.EPS32 * A
@@ -139,7 +140,7 @@ def _run(delta, lens, H, d, dtype, form, resume=None, slots=None, num_slots=None
                 used = max(used, ref.is_close(got[s, h], X, e_state + 1e-37, f"state {i} {h}"))
                 used = max(used, ref.is_close(out[r, h], o, e_out + 1e-37, f"readouts {i} {h}"))
             else:
-                kappa = ref.chunk_condition(x[1], al, b[r, h].double()) if form != "key" and dtype == "bf16" and d >= 64 else 1.0
+                kappa = ref.chunk_condition(x[1], al, b[r, h].double()) if not by_token else 1.0
                 e_col = (2 * d + 140 + 16) * chain * kappa * ref.EPS32 * top
                 err = (got[s, h].double().cpu() - X).norm(dim=0)
                 assert bool((err <= e_col).all()), f"state {i} {h}: {float((err / e_col).max()):.3g} of the bound"
@@ -187,6 +188,14 @@ def test_prompt_lengths(delta, d, lens):
 @pytest.mark.parametrize("heads", [1, 5, 33])
 def test_prompt_heads_and_resumed_parts(delta, heads):
     _run(delta, [70, 130, 3], heads, 64, "bf16", "token", resume=[1, 0, 1], seed=heads)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[31], [32], [33], [1] * 40, [0] * 45 + [44], [1] * 40 + [2], [3, 0, 29]], ids=lambda x: f"{len(x)}x{sum(x)}")
+def test_delta_calls_of_few_tokens(d, lens):
+    """Around the sizes up to which a call runs token by token."""
+    _run(True, lens, 3, d, "bf16", "token", resume=[i % 2 for i in range(len(lens))], seed=sum(lens))
+    _run(True, lens, 1, d, "bf16", "token", seed=len(lens))
 
 
 @RULES
