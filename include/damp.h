@@ -602,8 +602,8 @@ size_t kv_decode_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32
  *   k_new, v_new dev bf16 [B][num_kv_heads][d] or both NULL: the new token's key and value, stored
  *               at position seq_lens[b] - 1 before the attention reads it (NULL: already stored).
  *               That position's page must be the request's alone; other pages may be shared.
- * Scores, softmax statistics and sums are binary32; the softmax weights are rounded to bf16 for the
- * product with V. B * num_q_heads stays below 2^24. B == 0 is a no-op. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
+ * Scores, softmax statistics and sums are binary32; the softmax weights enter the product with V as two
+ * bf16 pieces, within 2^-15 + 2^-20 of their value. B * num_q_heads stays below 2^24. B == 0 is a no-op. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
 damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages,
                                 const int32_t* block_table, const int32_t* seq_lens, int32_t B,
                                 int32_t num_q_heads, int32_t num_kv_heads, int32_t d,
