@@ -688,9 +688,12 @@ def _decay(alpha, n, H, d, dev, fixed):
 
 
 def _workspace(workspace, nbytes, dev):
+    """The workspace of a call, its address and its size. The caller holds the tensor until the C call
+    is back: that call runs without the interpreter's lock, and another thread's call on the same stream
+    could be given memory that is free by then, and use it between this call's launches."""
     torch = _torch()
     if nbytes == 0:
-        return 0, 0
+        return None, 0, 0
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     elif not isinstance(workspace, torch.Tensor):
@@ -698,7 +701,7 @@ def _workspace(workspace, nbytes, dev):
     _fit(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
     if workspace.numel() < nbytes:
         raise ValueError(f"workspace has {workspace.numel()} bytes, {nbytes} needed")
-    return _ptr(workspace), workspace.numel()
+    return workspace, _ptr(workspace), workspace.numel()
 
 
 def fp32_linear_step(pool, slot_idx, q, k, v, alpha, out, stream=None) -> None:
@@ -743,7 +746,7 @@ def _prefill(delta, pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, resum
         _fit(resume, "resume", torch.int32, (B,), dev)
     L = load()
     with _On(dev, stream) as s:
-        ws, n = _workspace(workspace, L.fp32_prefill_workspace_bytes(delta, B, T, H, d, dt, decay), dev)
+        held, ws, n = _workspace(workspace, L.fp32_prefill_workspace_bytes(delta, B, T, H, d, dt, decay), dev)
         head = (_ptr(pool), S_, H, d, d, _ptr(slot_idx), _ptr(cu_seqlens),
                 _ptr(resume) if resume is not None else None, B, T, _ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), decay)
         if delta:
@@ -856,7 +859,7 @@ def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=N
     max_len = min(blocks * page if max_len is None else max_len, 1 << 30)
     L = load()
     with _On(dev, stream) as s:
-        ws, nb = _workspace(workspace, L.kv_decode_attention_workspace_bytes(B, Hq, Hkv, dc, max_len), dev)
+        held, ws, nb = _workspace(workspace, L.kv_decode_attention_workspace_bytes(B, Hq, Hkv, dc, max_len), dev)
         _check(L.kv_decode_attention(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), B,
                                      Hq, Hkv, dc, n, page, blocks, max_len, dc ** -0.5 if scale is None else scale,
                                      _ptr(k_new) if k_new is not None else None,
