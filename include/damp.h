@@ -529,8 +529,9 @@ size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t
  * of its 64-token chunk (but no other request). A request of no tokens keeps its state. B == 0 or
  * T == 0 is a no-op. At most 65,536 heads, and (T / 64 + B) * num_heads below 2^24, B * num_heads
  * below 2^21. bf16 inputs with d in {64, 128} and a decay per head (SCALAR, PER_HEAD) run chunk by
- * chunk on the matrix cores, with binary32 states, sums and decays; other forms, and calls of few
- * tokens where that is faster, token by token in binary32.
+ * chunk on the matrix cores, with binary32 states, sums and decays; other forms, and for the delta rule
+ * calls of few tokens (and short requests of calls with no more tokens than requests), token by token in
+ * binary32.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (d), SLOT_INDEX (debug), HIP. */
 damp_status fp32_linear_prefill(float* pool, int32_t num_slots, int32_t num_heads, int32_t d_k,
                                 int32_t d_v, const int32_t* slot_idx, const int32_t* cu_seqlens,

@@ -124,6 +124,7 @@ struct PromptArgs {
   const float* beta;        // [T][H] (delta rule)
   void* out;                // [T][H][d], the type of q
   uint8_t* ws;              // the chunked forms' workspace
+  int32_t few;              // 0, or: requests of at most so many tokens go token by token, the others in chunks
 };
 
 hipError_t launch_linear_step(int d, int decay, int bf16, const StepArgs& a, hipStream_t s);

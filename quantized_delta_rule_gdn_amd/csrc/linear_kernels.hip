@@ -119,7 +119,7 @@ __global__ __launch_bounds__(TokGeo<D>::NT) void prompt_token_kernel(const Promp
   const int64_t slot = a.slot_idx[b];
   if (!slot_in_pool(slot, a.num_slots)) return;
   const Span sp = span_of(a, b);
-  if (sp.end <= sp.begin) return;
+  if (sp.end <= sp.begin || (a.few && sp.end - sp.begin > a.few)) return;
   const int rg = tid % RG, c = tid / RG;
   float* pool = a.pool + ((slot * a.H + head) * D + 4 * rg) * int64_t(D) + c0 + c;
   f32x4 S[QR];   // S[j][i]: row 4 (rg + RG j) + i

@@ -34,16 +34,25 @@ struct Piece {
   int b, t0, n;   // n = 0: none
 };
 
+// Where requests of at most `few` tokens have none (PromptArgs), the others' chunks start at begin_b / few:
+// n > few tokens have at most n / few chunks of 2 few, so a request's numbers end before the next one's
+// begin, and T / few numbers are enough however many requests there are.
+constexpr int kFew = kC / 2;
+
+__device__ __forceinline__ int first_piece(const PromptArgs& a, int b, int begin, int len) {
+  return a.few ? begin / kFew : begin / len + b;
+}
+
 __device__ __forceinline__ Piece piece_of(const PromptArgs& a, int i, int len) {
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (span_of(a, mid).begin / len + mid <= i) lo = mid; else hi = mid;
+    if (first_piece(a, mid, span_of(a, mid).begin, len) <= i) lo = mid; else hi = mid;
   }
   const Span sp = span_of(a, lo);
-  const int j = i - (sp.begin / len + lo);
+  const int j = i - first_piece(a, lo, sp.begin, len);
   const int64_t t0 = sp.begin + int64_t(j) * len;
-  if (j < 0 || t0 >= sp.end) return Piece{lo, 0, 0};
+  if (j < 0 || t0 >= sp.end || (a.few && sp.end - sp.begin <= a.few)) return Piece{lo, 0, 0};
   return Piece{lo, static_cast<int>(t0), min(len, static_cast<int>(sp.end - t0))};
 }
 
@@ -298,6 +307,10 @@ __device__ __forceinline__ Place place_of(unsigned id, unsigned count, unsigned 
   return Place{static_cast<int>(id / group), static_cast<int>(id % group)};
 }
 
+// Chunk numbers of a call, and (request, head) pairs that a chain is started for.
+__host__ __device__ __forceinline__ unsigned chunks_of(const PromptArgs& a) { return a.few ? a.T / kFew : a.T / kC + a.B; }
+__host__ __device__ __forceinline__ unsigned chains_of(const PromptArgs& a) { return static_cast<unsigned>(a.few ? a.T / kFew : a.B) * a.H; }
+
 template <int D, int NT>
 __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, MD = D / 64, LS = D + 8, NC = 16 * NT;
@@ -309,8 +322,16 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   const int r = lane & 15, g = lane >> 4;
   constexpr int slices = D / NC;
   // the slices of a head read the same K, Q, X and P: one L2 for them
-  const Place at = place_of(__builtin_amdgcn_workgroup_id_x(), static_cast<unsigned>(a.B) * a.H, slices);
-  const int c0 = at.part * NC, head = at.item % a.H, b = request_by_length(a, at.item / a.H, slices);
+  const Place at = place_of(__builtin_amdgcn_workgroup_id_x(), chains_of(a), slices);
+  const int c0 = at.part * NC, head = at.item % a.H;
+  int b = at.item / a.H;
+  if (a.few) {           // a chain for each chunk number; it is the request's whose first chunk that is
+    const Piece pc = piece_of(a, b, kC);
+    if (pc.n <= 0 || pc.t0 != span_of(a, pc.b).begin) return;
+    b = pc.b;
+  } else {
+    b = request_by_length(a, b, slices);
+  }
   const int64_t slot = a.slot_idx[b];
   if (!slot_in_pool(slot, a.num_slots)) return;
   const Span sp_b = span_of(a, b);
@@ -320,7 +341,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(head) * D;
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D + c0;
   uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D + c0;
-  const uint8_t* ws = a.ws + (int64_t(sp_b.begin / kC + b) * a.H + head) * kDeltaUnit;
+  const uint8_t* ws = a.ws + (int64_t(first_piece(a, b, sp_b.begin, kC)) * a.H + head) * kDeltaUnit;
   const int64_t ws_step = int64_t(a.H) * kDeltaUnit;
   const int own = (D / 4) * w;                      // this wave's first key channel of the state
   float* pool = a.pool + ((slot * a.H + head) * D + own + 4 * g) * int64_t(D) + c0 + r;
@@ -971,9 +992,8 @@ hipError_t linear_d(int decay, const PromptArgs& a, hipStream_t s) {
 
 template <int D>
 hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
-  const unsigned chunks = static_cast<unsigned>(a.T / kC + a.B) * static_cast<unsigned>(a.H);
-  hipLaunchKernelGGL((delta_chunk_kernel<D>), dim3(chunks), dim3(256), 0, s, a);
-  const unsigned units = static_cast<unsigned>(a.B) * static_cast<unsigned>(a.H);
+  hipLaunchKernelGGL((delta_chunk_kernel<D>), dim3(chunks_of(a) * static_cast<unsigned>(a.H)), dim3(256), 0, s, a);
+  const unsigned units = chains_of(a);
   // 32 columns a workgroup read K, Q, X and P half as often, 16 give twice the workgroups. On one
   // MI355X, d = 128, 32 heads, 8,192 tokens in all, with 32 columns against 16: 64 states 264 against
   // 289 us, 128 states 229 against 288, 2,048 states 287 against 378; 32 states (one prompt) 431
@@ -988,26 +1008,45 @@ hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
 // bf16 inputs with one decay per head run in chunks; the rest token by token. So do calls of the delta
 // rule of few tokens: one launch instead of two, and no chunk's inverse. On one MI355X, d = 128, 32
 // heads, one prompt of 1 token 4.0 us against 13.1, of 16 7.6 against 13.2, of 32 11.9 against 13.3, of
-// 48 16.4 against 13.5; 64 of one token 68 against 127 us. (Only the sum of the lengths is known here:
-// the bounds hold if all tokens are one request's. Linear attention's chunks need one launch too: 3.9 us
-// against 8.5 for one token, but 67 against 43 for 64 requests of one.)
-bool chunked(bool delta, int d, int decay, int bf16, int32_t B, int32_t T) {
-  return bf16 && (d == 64 || d == 128) && decay != DECAY_KEY && !(delta && T <= std::max(32, B));
+// 48 16.4 against 13.5. Calls of no more tokens than requests (a fixed list of which few are in use, or a
+// token each) of more than 64 tokens take both forms, by the requests' lengths, which only the device knows:
+// those of up to 32 tokens one, longer ones the other. 512 requests, all 512 tokens one's: 70 us, 171 all
+// token by token, 75 all in chunks; a token each: 578, 568 and 1,061 us. At 64 tokens of 64 requests the
+// two launches more are not worth it: 21.5 and 72 us against 23.4 and 68 (19 and 128 in chunks).
+// (Linear attention's chunks need one launch too: 3.9 us against 8.5 for one token, but 67 against 43 for
+// 64 requests of one, which stay in chunks.)
+enum Form : int { TOKENS, CHUNKS, BY_LENGTH };
+
+Form form_of(bool delta, int d, int decay, int bf16, int32_t B, int32_t T) {
+  if (!bf16 || (d != 64 && d != 128) || decay == DECAY_KEY || (delta && (T <= kFew || T <= std::min(B, 2 * kFew))))
+    return TOKENS;
+  return delta && T <= B ? BY_LENGTH : CHUNKS;
 }
 
 }  // namespace
 
 int64_t prefill_ws_bytes(bool delta, int d, int decay, int bf16, int32_t B, int32_t T, int32_t H) {
-  if (!chunked(delta, d, decay, bf16, B, T)) return 0;
-  if (delta) return (int64_t(T) / kC + B) * H * kDeltaUnit;
+  PromptArgs a{};
+  a.B = B;
+  a.T = T;
+  const Form form = form_of(delta, d, decay, bf16, B, T);
+  if (form == TOKENS) return 0;
+  a.few = form == BY_LENGTH ? kFew : 0;
+  if (delta) return int64_t(chunks_of(a)) * H * kDeltaUnit;
   const int len = segment_len(B, T, H);
   return len ? (int64_t(T / len) + B) * H * (int64_t(d) * d + 1) * 4 : 0;
 }
 
 hipError_t launch_prefill(bool delta, int d, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
-  if (!chunked(delta, d, decay, bf16, a.B, a.T)) return launch_prompt_token(d, delta, decay, bf16, a, s);
-  if (!delta) return d == 64 ? linear_d<64>(decay, a, s) : linear_d<128>(decay, a, s);
-  return d == 64 ? delta_d<64>(a, s) : delta_d<128>(a, s);
+  const Form form = form_of(delta, d, decay, bf16, a.B, a.T);
+  PromptArgs c = a;
+  c.few = form == BY_LENGTH ? kFew : 0;
+  if (form != CHUNKS) {
+    const hipError_t e = launch_prompt_token(d, delta, decay, bf16, c, s);
+    if (e != hipSuccess || form == TOKENS) return e;
+  }
+  if (!delta) return d == 64 ? linear_d<64>(decay, c, s) : linear_d<128>(decay, c, s);
+  return d == 64 ? delta_d<64>(c, s) : delta_d<128>(c, s);
 }
 
 }  // namespace damp
