@@ -500,7 +500,8 @@ damp_status stq_decode_step(stq_state* state, void* dst_pool, const int32_t* slo
 
 /* One token per request of linear attention: arguments as fp32_decode_step without beta. alpha is
  * [B][num_heads] (DAMP_DECAY_SCALAR), [B][num_heads][d_k] (PER_KEY) or [num_heads] (PER_HEAD).
- * out fp32 [B][num_heads][d_v], 16-byte aligned: the readout of the updated state. */
+ * out fp32 [B][num_heads][d_v], 16-byte aligned: the readout of the updated state. B * num_heads stays
+ * below 2^24 (d_k of 64 and 128) or 2^26 (16 and 32). */
 damp_status fp32_linear_step(float* pool, int32_t num_slots, int32_t num_heads, int32_t d_k,
                              int32_t d_v, const int32_t* slot_idx, int32_t B, const void* q,
                              const void* k, const void* v, damp_dtype qkv_dtype,

@@ -1149,6 +1149,10 @@ damp_status fp32_linear_step(float* pool, int32_t num_slots, int32_t H, int32_t 
                              float* out, void* stream) {
   damp_status st = check_fp32_pool(pool, num_slots, H, d_k, d_v);
   if (st != DAMP_OK) return st;
+  // (a launch takes less than 2^32 threads)
+  if (static_cast<int64_t>(B) * H > 0xffffffffLL / damp::linear_step_threads(d_k))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B * num_heads = %lld exceeds the grid limit",
+                static_cast<long long>(B) * H);
   // (beta is not used: alpha stands in for the pointer check)
   st = check_step_args(B, H, d_k, slot_idx, q, k, v, dt, alpha,
                        decay == DAMP_DECAY_PER_HEAD ? DAMP_DECAY_SCALAR : decay, alpha, out);

@@ -127,6 +127,7 @@ struct PromptArgs {
   int32_t few;              // 0, or: requests of at most so many tokens go token by token, the others in chunks
 };
 
+int linear_step_threads(int d);   // of a state's workgroup
 hipError_t launch_linear_step(int d, int decay, int bf16, const StepArgs& a, hipStream_t s);
 // Chooses between the chunked and the token-by-token form; ws_bytes is what that choice needs.
 int64_t prefill_ws_bytes(bool delta, int d, int decay, int bf16, int32_t B, int32_t T, int32_t H);

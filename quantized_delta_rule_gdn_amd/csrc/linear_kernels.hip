@@ -14,10 +14,12 @@ namespace {
 // (64 fp32 values per lane at d = 128). The readout is taken from the updated row while it is in
 // registers; the partial column sums of the row groups meet in LDS, added in a fixed order.
 // 1,024 requests x 32 heads, d = 128: 792 us for 4.34 GB, 5.5 TB/s (a copy reaches 4.8); 3 x 32: 4.5 us.
+constexpr int lin_threads(int d) { return d >= 64 ? 256 : 64; }
+
 template <int D>
 struct LinGeo {
   static constexpr int LPR = D / 4;                         // lanes per row
-  static constexpr int NT = D >= 64 ? 256 : 64;             // threads per workgroup
+  static constexpr int NT = lin_threads(D);                 // threads per workgroup
   static constexpr int RPS = NT / LPR;                      // rows per row step
   static constexpr int RPL = D / RPS;                       // rows per lane
   static_assert(RPL >= 1 && RPL * RPS == D, "unsupported d");
@@ -278,6 +280,8 @@ hipError_t prompt_token_d(bool delta, int decay, int bf16, const PromptArgs& a, 
 }
 
 }  // namespace
+
+int linear_step_threads(int d) { return lin_threads(d); }
 
 hipError_t launch_linear_step(int d, int decay, int bf16, const StepArgs& a, hipStream_t s) {
   switch (d) {
