@@ -507,9 +507,10 @@ damp_status fp32_linear_step(float* pool, int32_t num_slots, int32_t num_heads, 
                              const void* k, const void* v, damp_dtype qkv_dtype,
                              const float* alpha, damp_decay decay, float* out, void* stream);
 
-/* Device bytes of workspace that a prefill call of these sizes needs (0: none, or invalid sizes);
- * delta: 0 for fp32_linear_prefill, 1 for fp32_delta_prefill. Its contents before the call do not
- * matter and nothing in it is kept for a later call; calls that may overlap need their own. */
+/* Device bytes of workspace that a prefill call of these sizes needs (0: none, or arguments that the
+ * call refuses); delta: 0 for fp32_linear_prefill, 1 for fp32_delta_prefill. Its contents before the
+ * call do not matter and nothing in it is kept for a later call; calls that may overlap need their
+ * own. */
 size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t num_heads, int32_t d,
                                     damp_dtype qkv_dtype, damp_decay decay);
 

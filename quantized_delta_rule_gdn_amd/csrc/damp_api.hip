@@ -424,17 +424,29 @@ damp_status debug_check_seqlens(const int32_t* cu, int32_t B, int32_t T, hipStre
   return DAMP_OK;
 }
 
+// What the prompt calls take, whatever their arrays hold; the size function of their workspaces goes by the same.
+bool takes_dtype(damp_dtype dt) { return dt == DAMP_F32 || dt == DAMP_BF16; }
+
+bool takes_decay(bool delta, damp_decay decay) {
+  return decay == DAMP_DECAY_SCALAR || decay == DAMP_DECAY_PER_KEY || (!delta && decay == DAMP_DECAY_PER_HEAD);
+}
+
+constexpr int32_t kMaxPromptHeads = 65536;
+
+// (a launch takes less than 2^32 threads: 256 a chunk, and 8 workgroups of 256 a state)
+bool fits_launch(int32_t B, int32_t T, int32_t H) {
+  return (static_cast<int64_t>(T) / 64 + B) * H <= kMaxGroups && static_cast<int64_t>(B) * H <= kMaxGroups / 8;
+}
+
 damp_status run_prefill(bool delta, float* pool, int32_t num_slots, int32_t H, int32_t d_k, int32_t d_v,
                         const int32_t* slot_idx, const int32_t* cu, const int32_t* resume, int32_t B,
                         int32_t T, const void* q, const void* k, const void* v, damp_dtype dt,
                         const float* alpha, damp_decay decay, const float* beta, void* out,
                         void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || T < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d) and T (%d) must be >= 0", B, T);
-  if (dt != DAMP_F32 && dt != DAMP_BF16)
+  if (!takes_dtype(dt))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "qkv_dtype %d is not DAMP_F32 or DAMP_BF16", int(dt));
-  const bool ok_decay = decay == DAMP_DECAY_SCALAR || decay == DAMP_DECAY_PER_KEY ||
-                        (!delta && decay == DAMP_DECAY_PER_HEAD);
-  if (!ok_decay) return fail(DAMP_ERR_INVALID_ARGUMENT, "decay %d is not one this call takes", int(decay));
+  if (!takes_decay(delta, decay)) return fail(DAMP_ERR_INVALID_ARGUMENT, "decay %d is not one this call takes", int(decay));
   damp_status st = check_fp32_pool(pool, num_slots, H, d_k, d_v);
   if (st != DAMP_OK) return st;
   if (B == 0 || T == 0) return ok();
@@ -444,9 +456,8 @@ damp_status run_prefill(bool delta, float* pool, int32_t num_slots, int32_t H, i
     return fail(DAMP_ERR_INVALID_ARGUMENT, "q, k, v and out must be 16-byte aligned");
   if (!aligned(slot_idx, 4) || !aligned(cu, 4) || !aligned(resume, 4) || !aligned(alpha, 4) || !aligned(beta, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned input pointer (need natural alignment)");
-  if (H > 65536) return fail(DAMP_ERR_UNSUPPORTED, "num_heads = %d: prompts take at most 65,536 heads", H);
-  // (a launch takes less than 2^32 threads: 256 a chunk, and 8 workgroups of 256 a state)
-  if ((static_cast<int64_t>(T) / 64 + B) * H > kMaxGroups || static_cast<int64_t>(B) * H > kMaxGroups / 8)
+  if (H > kMaxPromptHeads) return fail(DAMP_ERR_UNSUPPORTED, "num_heads = %d: prompts take at most 65,536 heads", H);
+  if (!fits_launch(B, T, H))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "T = %d tokens of %d requests with %d heads exceed the grid limit", T, B, H);
   const int64_t need = damp::prefill_ws_bytes(delta, d_k, decay, dt == DAMP_BF16, B, T, H);
   if (need > 0 && (!workspace || !aligned(workspace, kBlockAlign) || workspace_bytes < static_cast<size_t>(need)))
@@ -1178,7 +1189,9 @@ damp_status fp32_linear_step(float* pool, int32_t num_slots, int32_t H, int32_t 
 
 size_t fp32_prefill_workspace_bytes(int32_t delta, int32_t B, int32_t T, int32_t H, int32_t d,
                                     damp_dtype dt, damp_decay decay) {
-  if (B <= 0 || T <= 0 || H <= 0 || !supported_d(d)) return 0;
+  if (B <= 0 || T <= 0 || H <= 0 || H > kMaxPromptHeads || !supported_d(d) || !takes_dtype(dt) ||
+      !takes_decay(delta != 0, decay) || !fits_launch(B, T, H))
+    return 0;
   return static_cast<size_t>(damp::prefill_ws_bytes(delta != 0, d, decay, dt == DAMP_BF16, B, T, H));
 }
 
