@@ -775,6 +775,13 @@ def fp32_delta_prefill(pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, re
 # ------------------------------------------------------------------------------------------
 # paged key-value cache
 # ------------------------------------------------------------------------------------------
+def _sizes(**n):
+    """Sizes that go into the library as int32 (ctypes would cut longer ones to their lower 32 bits)."""
+    for name, x in n.items():
+        if x > 0x7FFFFFFF:
+            raise ValueError(f"{name} = {x} is more than 32 bits hold")
+
+
 def _pages(k_pages, v_pages, dev):
     torch = _torch()
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
@@ -808,9 +815,10 @@ def kv_build_tables(seq_lens, new_lens, free_pages, block_table, page_size: int,
         _fit(positions, "positions", torch.int32, (T,), dev)
     _fit(cu_new, "cu_new", torch.int32, (B + 1,), dev)
     _fit(used, "used", torch.int32, (1,), dev)
+    _sizes(max_blocks=blocks, num_free=free_pages.numel(), T=T)
     with _On(dev, stream) as s:
         _check(load().kv_build_tables(_ptr(seq_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(),
-                                      min(page_size, 1 << 30), _ptr(block_table), blocks, _ptr(slot_map),
+                                      max(-1, min(page_size, 1 << 30)), _ptr(block_table), blocks, _ptr(slot_map),
                                       _ptr(positions) if positions is not None else None, T, _ptr(cu_new),
                                       _ptr(used), s))
 
@@ -856,7 +864,8 @@ def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=N
     if k_new is not None:
         _fit(k_new, "k_new", torch.bfloat16, (B, Hkv, dc), dev)
         _fit(v_new, "v_new", torch.bfloat16, (B, Hkv, dc), dev)
-    max_len = min(blocks * page if max_len is None else max_len, 1 << 30)
+    _sizes(max_blocks=blocks)
+    max_len = max(-1, min(blocks * page if max_len is None else max_len, 1 << 30))
     L = load()
     with _On(dev, stream) as s:
         held, ws, nb = _workspace(workspace, L.kv_decode_attention_workspace_bytes(B, Hq, Hkv, dc, max_len), dev)
