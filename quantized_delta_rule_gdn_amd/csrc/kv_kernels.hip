@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const AppendArgs a) {
 // 7% above that rounding's. The second piece takes no time, 210 us for the batch below with either: the
 // matrix instructions are 3% busy.) Scores, m, the sum and the accumulators are binary32.
 // 64 requests of up to 8,192 tokens (266,000 in all), 32 query heads on 8, d = 128: 202 us for 1.09 GB,
-// 5.4 TB/s (a copy reaches 4.8); 5 of up to 65,536, 32 on 4, d = 64: 36 us for 201 MB, 5.6 TB/s.
+// 5.4 TB/s (reading alone reaches 7.1); 5 of up to 65,536, 32 on 4, d = 64: 36 us for 201 MB, 5.6 TB/s.
 constexpr int kAttnTile = 32;
 
 // The work is shared out on the device, by the requests' actual lengths: with `per_unit` workgroups

@@ -13,7 +13,7 @@ namespace {
 // flops). A row of the state is D / 4 lanes of 16 bytes; the whole unit is in flight at once
 // (64 fp32 values per lane at d = 128). The readout is taken from the updated row while it is in
 // registers; the partial column sums of the row groups meet in LDS, added in a fixed order.
-// 1,024 requests x 32 heads, d = 128: 792 us for 4.34 GB, 5.5 TB/s (a copy reaches 4.8); 3 x 32: 4.5 us.
+// 1,024 requests x 32 heads, d = 128: 792 us for 4.34 GB, 5.5 TB/s (a copy reaches 5.6); 3 x 32: 4.5 us.
 constexpr int lin_threads(int d) { return d >= 64 ? 256 : 64; }
 
 template <int D>

@@ -9,11 +9,16 @@
 // gates, so every chunk's X diag(b) and P are formed at once, in parallel over the prompt, and the
 // chain from chunk to chunk is left with products of the state.
 //
-// Numerics. All exponents are differences of the same running sums, held as two binary32 numbers
-// each (a binary64 sum, split), so every decay is good to about 2^-23 whatever the sums reach. Keys,
-// queries and values are exact bf16 operands; the state, E and X enter a product as bf16 pieces
-// (prompt_common.h): three where the result feeds the state (2^-24), two where it is a readout that
-// bf16 rounds at 2^-9. The state itself and all sums are binary32.
+// Numerics. Exponents are sums of binary32 logarithms (v_log_f32, within 2^-23 of each, near 1 too), summed
+// in binary64. Those between two tokens are differences of sums held as two binary32 numbers each, so that
+// an exponent x is off by 2^-22 |x| at most whatever the sums themselves reach; 2^G_t, 2^(G_C - G_t), 2^G_C
+// and the segments' decays start at a chunk's or segment's border and come from one binary32 exponent, to
+// the same bound. A decay 2^x is then off by 2^-22 |x| ln 2 of itself and v_exp_f32's 2^-23: by less than
+// 2^-22 of 1, while the relative error grows with |x| (2^-18 at 2^-16), as it does by the number of tokens
+// where they are multiplied one by one. Keys, queries and values are exact bf16 operands; the state, E
+// and X enter a product as bf16 pieces (prompt_common.h): three where the result feeds the state (2^-24; of
+// X R the products of pieces i and j with i + j > 2, below 2^-24 of the product, are left out), two (2^-16)
+// where it is a readout, whose rounding to bf16 is 2^-8. The state itself and all sums are binary32.
 #include <algorithm>
 
 #include "prompt_common.h"
@@ -140,7 +145,7 @@ __device__ __forceinline__ f32x4 mul16_tile(const float* A, f32x4 m, int ld, f32
 // blocks are joined two by two, [[X, 0], [Y, Z]]^-1 = [[X', 0], [-Z' Y X', Z']], with binary32
 // matrix instructions: no power of A is formed, so the result is as good as forward substitution.
 // Bound by its stream: q and k in, 40.5 KB of workspace a chunk and head out. 16,384 tokens x 32 heads,
-// d = 128: 138 us for 558 MB moved (302 read, 256 written), 4.0 TB/s of the 4.8 a copy reaches.
+// d = 128: 138 us for 558 MB moved (302 read, 256 written), 4.0 TB/s of the 5.6 a copy reaches.
 template <int D>
 __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, LK = D + 8, LF = kC + 4;
@@ -623,7 +628,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
 // segment, and the readouts of all segments run at once.
 // Bound by issue (splitting the state and the weights into pieces, their products, the LDS reads):
 // 4.1 us a chunk with one workgroup a CU. 8,191 ragged tokens of 12 prompts x 32 heads, d = 128: 160 us,
-// 71 us where 16 prompts are even, against 64 us of its 307 MB at the rate of a copy; the longest
+// 71 us where 16 prompts are even, against 55 us of its 307 MB at the rate of a copy; the longest
 // prompt's chain sets the ragged time. 8 waves a workgroup took 84 us where 4 took 72-74.
 enum LinearMode : int { LIN_WHOLE = 0, LIN_STATES = 1, LIN_SEGMENTS = 2 };
 

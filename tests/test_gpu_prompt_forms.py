@@ -74,3 +74,38 @@ def test_segments_of_more_than_256_tokens(lens, H, form):
 
 def test_segments_of_more_than_256_tokens_at_128_channels():
     _some_heads([1700, 900], 70, 128, "token", (3, 69), [1, 0], seed=5)
+
+
+@RULES
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,total", [(64, 4.0), (64, 30.0), (64, 90.0), (200, 1.0), (200, 60.0), (1500, 0.3), (1500, 90.0)])
+def test_decays_to_their_bound(delta, d, n, total):
+    """Only the first token writes (later values are 0, by the delta rule with beta 0), so the last state is the
+    product of n - 1 decays times k v^T. An exponent x is a sum of binary32 logarithms (within 2^-23 of each),
+    taken as a difference and rounded (2^-23 of it more): 2^-22 |x| in all, over all chunks together, as every
+    chunk's is relative to its own share of x. Its power adds 2^-23 and the product with the state 2^-24 a chunk,
+    the first chunk's product with three pieces of the value 3 2^-23. Relative to the value, in every element."""
+    H = 3
+    gen = torch.Generator().manual_seed(n + d)
+    q, k = (_unit(torch.randn((n, H, d), generator=gen)).bfloat16() for _ in range(2))
+    v = torch.zeros((n, H, d))
+    v[0] = torch.randn((H, d), generator=gen)
+    v = v.bfloat16()
+    w = torch.rand((n, H), generator=gen)
+    w[:, 1] = 1.0                                              # even decays, random ones, and a few strong ones
+    w[:, 2] = (torch.rand(n, generator=gen) < 0.1).float() + 1e-3
+    alpha = torch.exp2(-total * w / w.sum(0))
+    beta = torch.zeros((n, H))
+    beta[0] = 1.0
+    pool, out = torch.zeros((1, H, d, d), device="cuda"), torch.empty((n, H, d), dtype=torch.bfloat16, device="cuda")
+    args = (pool, torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda"), q.cuda(), k.cuda(), v.cuda(), alpha.cuda())
+    if delta:
+        lib.fp32_delta_prefill(*args, beta.cuda(), out)
+    else:
+        lib.fp32_linear_prefill(*args, out)
+    torch.cuda.synchronize()
+    for h in range(H):
+        x = alpha[1:, h].double().log2().sum()
+        want = torch.exp2(x) * torch.outer(k[0, h].double(), v[0, h].double())
+        bound = (2.0 ** -22 * float(-x) * 0.6931471805599453 + (-(-n // 64) * 1.5 + 4) * 2.0 ** -23) * want.abs()
+        ref.is_close(pool[0, h], want, bound, f"head {h}, decay 2^{float(x):.3g}")
