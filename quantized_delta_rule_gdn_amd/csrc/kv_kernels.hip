@@ -143,8 +143,8 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const AppendArgs a) {
 // scores all the same way: a few tokens at the maximum and all others at p = 0.50195 over a V of ones gave
 // 0.996. Nor does it average below the readout's own rounding: 8,192 random scores gave an error
 // 7% above that rounding's. The second piece takes no time, 210 us for the batch below with either: the
-// matrix instructions are 3% busy.) Scores, m, the sum and the accumulators are binary32.
-// 64 requests of up to 8,192 tokens (266,000 in all), 32 query heads on 8, d = 128: 202 us for 1.09 GB,
+// matrix instructions are 5% busy.) Scores, m, the sum and the accumulators are binary32.
+// 64 requests of up to 8,192 tokens (266,000 in all), 32 query heads on 8, d = 128: 200 us for 1.09 GB,
 // 5.4 TB/s (reading alone reaches 7.1); 5 of up to 65,536, 32 on 4, d = 64: 36 us for 201 MB, 5.6 TB/s.
 constexpr int kAttnTile = 32;
 
