@@ -722,9 +722,17 @@ def fp32_linear_step(pool, slot_idx, q, k, v, alpha, out, stream=None) -> None:
                                        _ptr(v), dt, _ptr(alpha), decay, _ptr(out), s))
 
 
+def _sizes(**n):
+    """Sizes that go into the library as int32 (ctypes would cut longer ones to their lower 32 bits)."""
+    for name, x in n.items():
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            raise ValueError(f"{name} = {x} is more than 32 bits hold")
+
+
 def prefill_workspace_bytes(delta: bool, B: int, T: int, H: int, d: int, dtype, decay: int = DAMP_DECAY_SCALAR) -> int:
     """Bytes of the workspace of fp32_linear_prefill (``delta`` false) or fp32_delta_prefill."""
     torch = _torch()
+    _sizes(B=B, T=T, H=H, d=d)
     return load().fp32_prefill_workspace_bytes(int(delta), B, T, H, d,
                                                DAMP_BF16 if dtype == torch.bfloat16 else DAMP_F32, decay)
 
@@ -775,13 +783,6 @@ def fp32_delta_prefill(pool, slot_idx, cu_seqlens, q, k, v, alpha, beta, out, re
 # ------------------------------------------------------------------------------------------
 # paged key-value cache
 # ------------------------------------------------------------------------------------------
-def _sizes(**n):
-    """Sizes that go into the library as int32 (ctypes would cut longer ones to their lower 32 bits)."""
-    for name, x in n.items():
-        if x > 0x7FFFFFFF:
-            raise ValueError(f"{name} = {x} is more than 32 bits hold")
-
-
 def _pages(k_pages, v_pages, dev):
     torch = _torch()
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
@@ -837,7 +838,9 @@ def kv_append(k, v, slot_map, k_pages, v_pages, stream=None) -> None:
 
 
 def kv_decode_attention_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int, d: int, max_len: int) -> int:
-    return load().kv_decode_attention_workspace_bytes(B, num_q_heads, num_kv_heads, d, max_len)
+    """Bytes of the workspace of kv_decode_attention with that ``max_len`` (2^30 stands for more, as there)."""
+    _sizes(B=B, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, d=d)
+    return load().kv_decode_attention_workspace_bytes(B, num_q_heads, num_kv_heads, d, max(-1, min(max_len, 1 << 30)))
 
 
 def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=None, k_new=None, v_new=None,

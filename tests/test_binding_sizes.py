@@ -73,3 +73,17 @@ def test_attention_bounds_of_more_than_32_bits(library):
     with pytest.raises(ValueError):
         _attention(blocks=2 ** 32 + 1)
     assert len(library.calls) == n
+
+
+def test_workspace_sizes_of_more_than_32_bits():
+    """The size functions see what the calls would: sizes beyond 32 bits raise, a length bound stops at 2^30."""
+    for x in (2 ** 32 + 1, 2 ** 31, -(2 ** 32) + 1):
+        for n in ((x, 5000, 2, 64), (1, x, 2, 64), (1, 5000, x, 64), (1, 5000, 2, x)):
+            with pytest.raises(ValueError):
+                lib.prefill_workspace_bytes(True, *n, torch.bfloat16)
+        for n in ((x, 4, 2, 64, 5000), (1, x, 2, 64, 5000), (1, 4, x, 64, 5000), (1, 4, 2, x, 5000)):
+            with pytest.raises(ValueError):
+                lib.kv_decode_attention_workspace_bytes(*n)
+    size = lib.kv_decode_attention_workspace_bytes
+    assert size(1, 4, 2, 64, 2 ** 32 + 5) == size(1, 4, 2, 64, 2 ** 40) == size(1, 4, 2, 64, 2 ** 30) > 0
+    assert size(1, 4, 2, 64, 5000 - 2 ** 32) == 0
