@@ -138,12 +138,13 @@ __global__ __launch_bounds__(256) void kv_append_kernel(const AppendArgs a) {
 //   lane group g holds tokens 4 g .. + 3 of both 16-token halves), so V^T's operand takes those
 //   tokens: each lane loads D / 16 neighbouring channels of 8 tokens (whole rows per 16 lanes)
 //   and transposes them with byte permutes; output channel D / 16 * row + m is tile m's row.
-// A weight p enters the second product as two bf16 pieces, what its upper 16 bits hold and the rest
-// rounded, good to 2^-15 + 2^-20 of it. (One rounded piece is off by up to 2^-8, and tokens of equal
+// A weight p enters the second product as two bf16 pieces, the upper 16 bits of p (1 - 2^-12) and the rest
+// rounded, good to 2^-15 + 2^-20 of p. (One rounded piece is off by up to 2^-8, and tokens of equal
 // scores all the same way: a few tokens at the maximum and all others at p = 0.50195 over a V of ones gave
 // 0.996. Nor does it average below the readout's own rounding: 8,192 random scores gave an error
-// 7% above that rounding's. The second piece takes no time, 210 us for the batch below with either: the
-// matrix instructions are 5% busy.) Scores, m, the sum and the accumulators are binary32.
+// 7% above that rounding's. The second piece takes no time where the stream is long, 208.5 us for the batch
+// below with either, and 0.3 of 10.7 us for one request of 700 tokens: the matrix instructions are 5% busy.)
+// Scores, m, the sum and the accumulators are binary32.
 // 64 requests of up to 8,192 tokens (266,000 in all), 32 query heads on 8, d = 128: 200 us for 1.09 GB,
 // 5.4 TB/s (reading alone reaches 7.1); 5 of up to 65,536, 32 on 4, d = 64: 36 us for 201 MB, 5.6 TB/s.
 constexpr int kAttnTile = 32;
@@ -420,21 +421,25 @@ __global__ __launch_bounds__(256, 2) void kv_attention_kernel(const AttnArgs a, 
       }
   #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        // (of a little less than x, so that the rest is never 0: times an infinite value that would be NaN)
         const float x0 = p[2 * j], x1 = p[2 * j + 1];
-        const uint32_t w0 = __float_as_uint(x0), w1 = __float_as_uint(x1);
+        const uint32_t w0 = __float_as_uint(x0 * 0x1.ffep-1f), w1 = __float_as_uint(x1 * 0x1.ffep-1f);
         pf[0].w[j] = __builtin_amdgcn_perm(w1, w0, 0x07060302u);
-        // (never 0: an infinite value times a rest of 0 would be NaN)
-        pf[1].w[j] = pack_bf16(fmaxf(x0 - __uint_as_float(w0 & 0xffff0000u), x0 * 0x1p-20f),
-                               fmaxf(x1 - __uint_as_float(w1 & 0xffff0000u), x1 * 0x1p-20f));
+        pf[1].w[j] = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
       }
   #pragma unroll
-      for (int m = 0; m < DPL; ++m) {
-        Frag vf;
+      for (int m = 0; m < DPL; m += 2) {   // (each sum's two products apart)
+        Frag vf[2];
   #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          vf.w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][m / 2], vr[2 * j][m / 2], m % 2 ? 0x07060302u : 0x05040100u);
-        o[m] = mfma(vf, pf[0], o[m]);
-        o[m] = mfma(vf, pf[1], o[m]);
+        for (int j = 0; j < 4; ++j) {
+          vf[0].w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][m / 2], vr[2 * j][m / 2], 0x05040100u);
+          vf[1].w[j] = __builtin_amdgcn_perm(vr[2 * j + 1][m / 2], vr[2 * j][m / 2], 0x07060302u);
+        }
+  #pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          o[m] = mfma(vf[0], pf[x], o[m]);
+          o[m + 1] = mfma(vf[1], pf[x], o[m + 1]);
+        }
       }
     }
   }

@@ -1,8 +1,8 @@
 """How well the softmax weights of kv_decode_attention enter the product with V.
 
-Bounds. A weight enters as two bf16 pieces: the first is cut off (below 2^-7 of the weight is left), the
-second rounded (half a step, 2^-8) and at least 2^-20 of the weight, so together they are within
-2^-15 + 2^-20 of it. Sums over n tokens add n / 32 + 64 roundings of 2^-24 (products and joins), the
+Bounds. A weight enters as two bf16 pieces: the first is the weight less 2^-12 of it, cut off (below
+2^-7 + 2^-12 of the weight is left), the second what is left, rounded (half a step, 2^-8), so together they
+are within 2^-15 + 2^-20 of it. Sums over n tokens add n / 32 + 64 roundings of 2^-24 (products and joins), the
 normaliser as many, the scores what serving_ref.score_error says on both sides of the quotient, and the
 result's own rounding to bf16 is 2^-8 of it."""
 import math
