@@ -124,7 +124,7 @@ struct PromptArgs {
   const float* beta;        // [T][H] (delta rule)
   void* out;                // [T][H][d], the type of q
   uint8_t* ws;              // the chunked forms' workspace
-  int32_t few;              // 0, or: requests of at most so many tokens go token by token, the others in chunks
+  int32_t few;              // token by token: 0, or leave requests of more tokens than these to the chunks
 };
 
 int linear_step_threads(int d);   // of a state's workgroup

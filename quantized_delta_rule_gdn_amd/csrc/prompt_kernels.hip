@@ -39,25 +39,28 @@ struct Piece {
   int b, t0, n;   // n = 0: none
 };
 
-// Where requests of at most `few` tokens have none (PromptArgs), the others' chunks start at begin_b / few:
-// n > few tokens have at most n / few chunks of 2 few, so a request's numbers end before the next one's
-// begin, and T / few numbers are enough however many requests there are.
+// Where requests of at most kFew tokens go token by token and have none (FEW), the others' chunks start at
+// begin_b / kFew: n > 32 tokens have at most n / 32 chunks of 64, so a request's numbers end before the next
+// one's begin, and T / 32 numbers are enough however many requests there are. (A build of its own: the same
+// test at run time cost ordinary calls 0.5%, 624.5 against 621.6 us for a prompt of 16,384 tokens.)
 constexpr int kFew = kC / 2;
 
-__device__ __forceinline__ int first_piece(const PromptArgs& a, int b, int begin, int len) {
-  return a.few ? begin / kFew : begin / len + b;
+template <bool FEW>
+__device__ __forceinline__ int first_piece(int b, int begin, int len) {
+  return FEW ? begin / kFew : begin / len + b;
 }
 
+template <bool FEW>
 __device__ __forceinline__ Piece piece_of(const PromptArgs& a, int i, int len) {
   int lo = 0, hi = a.B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (first_piece(a, mid, span_of(a, mid).begin, len) <= i) lo = mid; else hi = mid;
+    if (first_piece<FEW>(mid, span_of(a, mid).begin, len) <= i) lo = mid; else hi = mid;
   }
   const Span sp = span_of(a, lo);
-  const int j = i - first_piece(a, lo, sp.begin, len);
+  const int j = i - first_piece<FEW>(lo, sp.begin, len);
   const int64_t t0 = sp.begin + int64_t(j) * len;
-  if (j < 0 || t0 >= sp.end || (a.few && sp.end - sp.begin <= a.few)) return Piece{lo, 0, 0};
+  if (j < 0 || t0 >= sp.end || (FEW && sp.end - sp.begin <= kFew)) return Piece{lo, 0, 0};
   return Piece{lo, static_cast<int>(t0), min(len, static_cast<int>(sp.end - t0))};
 }
 
@@ -69,7 +72,7 @@ __device__ __forceinline__ int even_len(int tokens, int most) {
 }
 
 __device__ __forceinline__ Piece segment_of(const PromptArgs& a, int i, int most) {
-  const Piece pc = piece_of(a, i, most);
+  const Piece pc = piece_of<false>(a, i, most);
   if (pc.n <= 0) return pc;
   const Span sp = span_of(a, pc.b);
   const int len = even_len(sp.end - sp.begin, most), t0 = sp.begin + (pc.t0 - sp.begin) / most * len;
@@ -146,7 +149,7 @@ __device__ __forceinline__ f32x4 mul16_tile(const float* A, f32x4 m, int ld, f32
 // matrix instructions: no power of A is formed, so the result is as good as forward substitution.
 // Bound by its stream: q and k in, 40.5 KB of workspace a chunk and head out. 16,384 tokens x 32 heads,
 // d = 128: 138 us for 558 MB moved (302 read, 256 written), 4.0 TB/s of the 5.6 a copy reaches.
-template <int D>
+template <int D, bool FEW>
 __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, LK = D + 8, LF = kC + 4;
   __shared__ __align__(16) float pf[kC][LF];   // the keys (bf16 rows of LK), later P
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(const PromptArgs a) {
   const int r = lane & 15, g = lane >> 4;
   const int unit = __builtin_amdgcn_workgroup_id_x();
   const int head = unit % a.H;
-  const Piece pc = piece_of(a, unit / a.H, kC);
+  const Piece pc = piece_of<FEW>(a, unit / a.H, kC);
   if (pc.n <= 0) return;
   uint8_t* ws = a.ws + int64_t(unit) * kDeltaUnit;
   const int64_t row0 = (int64_t(pc.t0) * a.H + head) * D, rstep = int64_t(a.H) * D;
@@ -313,10 +316,12 @@ __device__ __forceinline__ Place place_of(unsigned id, unsigned count, unsigned 
 }
 
 // Chunk numbers of a call, and (request, head) pairs that a chain is started for.
-__host__ __device__ __forceinline__ unsigned chunks_of(const PromptArgs& a) { return a.few ? a.T / kFew : a.T / kC + a.B; }
-__host__ __device__ __forceinline__ unsigned chains_of(const PromptArgs& a) { return static_cast<unsigned>(a.few ? a.T / kFew : a.B) * a.H; }
+int64_t chunks_of(bool few, int32_t B, int32_t T) { return few ? T / kFew : int64_t(T / kC) + B; }
 
-template <int D, int NT>
+template <bool FEW>
+__host__ __device__ __forceinline__ unsigned chains_of(const PromptArgs& a) { return static_cast<unsigned>(FEW ? a.T / kFew : a.B) * a.H; }
+
+template <int D, int NT, bool FEW>
 __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a) {
   constexpr int KS = D / 32, MD = D / 64, LS = D + 8, NC = 16 * NT;
   __shared__ __align__(16) uint16_t kb[kC][LS];
@@ -327,11 +332,11 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   const int r = lane & 15, g = lane >> 4;
   constexpr int slices = D / NC;
   // the slices of a head read the same K, Q, X and P: one L2 for them
-  const Place at = place_of(__builtin_amdgcn_workgroup_id_x(), chains_of(a), slices);
+  const Place at = place_of(__builtin_amdgcn_workgroup_id_x(), chains_of<FEW>(a), slices);
   const int c0 = at.part * NC, head = at.item % a.H;
   int b = at.item / a.H;
-  if (a.few) {           // a chain for each chunk number; it is the request's whose first chunk that is
-    const Piece pc = piece_of(a, b, kC);
+  if constexpr (FEW) {   // a chain for each chunk number; it is the request's whose first chunk that is
+    const Piece pc = piece_of<true>(a, b, kC);
     if (pc.n <= 0 || pc.t0 != span_of(a, pc.b).begin) return;
     b = pc.b;
   } else {
@@ -346,7 +351,7 @@ __global__ __launch_bounds__(256, 2) void delta_chain_kernel(const PromptArgs a)
   const uint16_t* qp = static_cast<const uint16_t*>(a.q) + int64_t(head) * D;
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + int64_t(head) * D + c0;
   uint16_t* op = static_cast<uint16_t*>(a.out) + int64_t(head) * D + c0;
-  const uint8_t* ws = a.ws + (int64_t(first_piece(a, b, sp_b.begin, kC)) * a.H + head) * kDeltaUnit;
+  const uint8_t* ws = a.ws + (int64_t(first_piece<FEW>(b, sp_b.begin, kC)) * a.H + head) * kDeltaUnit;
   const int64_t ws_step = int64_t(a.H) * kDeltaUnit;
   const int own = (D / 4) * w;                      // this wave's first key channel of the state
   float* pool = a.pool + ((slot * a.H + head) * D + own + 4 * g) * int64_t(D) + c0 + r;
@@ -995,18 +1000,18 @@ hipError_t linear_d(int decay, const PromptArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D>
+template <int D, bool FEW>
 hipError_t delta_d(const PromptArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((delta_chunk_kernel<D>), dim3(chunks_of(a) * static_cast<unsigned>(a.H)), dim3(256), 0, s, a);
-  const unsigned units = chains_of(a);
+  hipLaunchKernelGGL((delta_chunk_kernel<D, FEW>), dim3(static_cast<unsigned>(chunks_of(FEW, a.B, a.T) * a.H)), dim3(256), 0, s, a);
+  const unsigned units = chains_of<FEW>(a);
   // 32 columns a workgroup read K, Q, X and P half as often, 16 give twice the workgroups. On one
   // MI355X, d = 128, 32 heads, 8,192 tokens in all, with 32 columns against 16: 64 states 264 against
   // 289 us, 128 states 229 against 288, 2,048 states 287 against 378; 32 states (one prompt) 431
   // against 321. d = 64: 128 states 138 against 143 us, 64 states 201 against 154.
   if (units * (D / 32) >= 256)
-    hipLaunchKernelGGL((delta_chain_kernel<D, 2>), dim3(units * (D / 32)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((delta_chain_kernel<D, 2, FEW>), dim3(units * (D / 32)), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((delta_chain_kernel<D, 1>), dim3(units * (D / 16)), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((delta_chain_kernel<D, 1, FEW>), dim3(units * (D / 16)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1031,27 +1036,23 @@ Form form_of(bool delta, int d, int decay, int bf16, int32_t B, int32_t T) {
 }  // namespace
 
 int64_t prefill_ws_bytes(bool delta, int d, int decay, int bf16, int32_t B, int32_t T, int32_t H) {
-  PromptArgs a{};
-  a.B = B;
-  a.T = T;
   const Form form = form_of(delta, d, decay, bf16, B, T);
   if (form == TOKENS) return 0;
-  a.few = form == BY_LENGTH ? kFew : 0;
-  if (delta) return int64_t(chunks_of(a)) * H * kDeltaUnit;
+  if (delta) return chunks_of(form == BY_LENGTH, B, T) * H * kDeltaUnit;
   const int len = segment_len(B, T, H);
   return len ? (int64_t(T / len) + B) * H * (int64_t(d) * d + 1) * 4 : 0;
 }
 
 hipError_t launch_prefill(bool delta, int d, int decay, int bf16, const PromptArgs& a, hipStream_t s) {
   const Form form = form_of(delta, d, decay, bf16, a.B, a.T);
-  PromptArgs c = a;
-  c.few = form == BY_LENGTH ? kFew : 0;
-  if (form != CHUNKS) {
-    const hipError_t e = launch_prompt_token(d, delta, decay, bf16, c, s);
-    if (e != hipSuccess || form == TOKENS) return e;
-  }
-  if (!delta) return d == 64 ? linear_d<64>(decay, c, s) : linear_d<128>(decay, c, s);
-  return d == 64 ? delta_d<64>(c, s) : delta_d<128>(c, s);
+  if (form == TOKENS) return launch_prompt_token(d, delta, decay, bf16, a, s);
+  if (!delta) return d == 64 ? linear_d<64>(decay, a, s) : linear_d<128>(decay, a, s);
+  if (form == CHUNKS) return d == 64 ? delta_d<64, false>(a, s) : delta_d<128, false>(a, s);
+  PromptArgs few = a;
+  few.few = kFew;
+  const hipError_t e = launch_prompt_token(d, delta, decay, bf16, few, s);
+  if (e != hipSuccess) return e;
+  return d == 64 ? delta_d<64, true>(a, s) : delta_d<128, true>(a, s);
 }
 
 }  // namespace damp
