@@ -614,6 +614,152 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages,
                                 int32_t max_len, float scale, const void* k_new, const void* v_new,
                                 void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The life of the cache's pages. Pages may be held by several requests: shares (dev int32
+ * [num_pages], zero at first, never negative) counts the holders of each page beyond the first;
+ * kv_build_tables takes pages whose count is 0 and leaves it so. Only a request's full pages are ever
+ * shared. The calls that move rows take pages [num_pages][num_kv_heads][page_size][d] of 2-byte
+ * channels, d a multiple of 8 up to 2,048; v_pages may be NULL (latents: num_kv_heads 1, d the row).
+ * ------------------------------------------------------------------------------------- */
+
+/* Requests forked from others (samples of one prompt, beams): request dst[i] of the table becomes a
+ * copy of request src[i], in the order of i. Its full pages are the source's, their shares go up by
+ * one; a partly filled last page is replaced by the next page of free_pages.
+ *   src, dst    dev int32 [n]: rows of the table. No dst may appear twice or as a src. A fork with an
+ *               index outside [0, B) is skipped.
+ *   seq_lens    dev int32 [B]: read at src, written at dst
+ *   block_table dev int32 [B][max_blocks]: read at src, written at dst (entries behind the request's pages
+ *               are left as they were)
+ *   copy_src, copy_dst, copy_rows dev int32 [n] (output): the partly filled page, its replacement, its
+ *               filled rows, for kv_copy_pages (once per layer); -1, -1, 0 where nothing is to be copied
+ *   used        dev int32 [1] (output): pages needed; beyond num_free of them the entries are -1
+ * At most 8,000 forks (else UNSUPPORTED). Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP. */
+damp_status kv_fork_tables(const int32_t* src, const int32_t* dst, int32_t n, int32_t* seq_lens, int32_t B,
+                           const int32_t* free_pages, int32_t num_free, int32_t* block_table,
+                           int32_t max_blocks, int32_t* shares, int32_t num_pages, int32_t page_size,
+                           int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows, int32_t* used,
+                           void* stream);
+
+/* Copies page src[i] to page dst[i] (dev int32 [n]), all heads, keys and values: the first rows[i] rows (dev
+ * int32 [n], clamped to the page), or all with rows NULL. A page outside the cache is skipped. No dst
+ * may appear twice or as a src. */
+damp_status kv_copy_pages(const int32_t* src, const int32_t* dst, const int32_t* rows, int32_t n,
+                          void* k_pages, void* v_pages, int32_t num_pages, int32_t num_kv_heads,
+                          int32_t page_size, int32_t d, void* stream);
+
+/* Kept tokens moved together, in place (accepted drafts; a cache that drops tokens). Of the last
+ * new_lens[b] of request b's seq_lens[b] tokens, the ones listed are kept, the others dropped:
+ *   kept      dev int32 [num_kept]: entries cu_kept[b] .. cu_kept[b + 1] - 1 (dev int32 [B + 1]) are
+ *             request b's, ascending, each in [0, new_lens[b]): the j-th one's key and value move to
+ *             the j-th of those positions. A list that does not ascend leaves unspecified rows
+ *             (inside the request's pages); an entry past the new tokens moves nothing.
+ *   out_lens  dev int32 [B] (output): seq_lens[b] - new_lens[b] + the number kept (keep_lens of
+ *             kv_free_pages). It must not be seq_lens or new_lens.
+ * The pages that tokens move in must be the request's alone. Called once per layer. */
+damp_status kv_compact(const int32_t* kept, const int32_t* cu_kept, int32_t num_kept,
+                       const int32_t* seq_lens, const int32_t* new_lens, int32_t B,
+                       const int32_t* block_table, int32_t max_blocks, void* k_pages, void* v_pages,
+                       int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t d,
+                       int32_t* out_lens, void* stream);
+
+/* Device bytes of workspace kv_free_pages needs (0: none); nothing in it is kept. */
+size_t kv_free_pages_workspace_bytes(int32_t num_pages);
+
+/* Gives back pages: of each request those behind its first keep_lens[b] tokens (dev int32 [B], NULL: all),
+ * up to the last that seq_lens[b] tokens fill. A page with shares left loses one; the others are listed.
+ *   shares    dev int32 [num_pages]: updated (calls on it that overlap race)
+ *   freed     dev int32 [num_pages] (output): ids of the pages that no request holds any more, ascending;
+ *             entries behind the last are left as they were
+ *   num_freed dev int32 [1] (output)
+ *   workspace dev, 16-byte aligned, kv_free_pages_workspace_bytes
+ * The table is not written. Two requests may give back the same page in one call. */
+damp_status kv_free_pages(const int32_t* keep_lens, const int32_t* seq_lens, int32_t B,
+                          const int32_t* block_table, int32_t max_blocks, int32_t* shares,
+                          int32_t num_pages, int32_t page_size, int32_t* freed, int32_t* num_freed,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Attention of several new tokens per request (drafted ones, a tree or a run in order), and latent
+ * attention.
+ * ------------------------------------------------------------------------------------- */
+
+/* Device bytes of workspace kv_tree_attention needs with these sizes (0: none, or sizes that it refuses).
+ * Its contents before the call do not matter and nothing in it is kept; calls that may overlap need
+ * their own. */
+size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t num_kv_heads,
+                                         int32_t d, int32_t max_new, int32_t max_len);
+
+/* Attention of several new tokens per request over its cached tokens, the new ones among them (stored
+ * before by kv_append): the j-th of request b's n new tokens is at position seq_lens[b] - n + j. Token i
+ * sees the positions before the new ones, and of the new ones those up to its own, or with a mask those
+ * whose bit is set.
+ *   q, out      dev bf16 [T][num_q_heads][d], 16-byte aligned; a token that sees nothing gives 0
+ *   seq_lens    dev int32 [B], the new tokens included
+ *   cu_new      dev int32 [B + 1], ascending: request b's new tokens are rows cu_new[b] .. cu_new[b + 1] - 1.
+ *               Values are kept inside [0, T]. Rows of out behind the last request are not written.
+ *   mask        dev int64 [T][mask_words] or NULL: bit j % 64 of word j / 64 of a token's row says whether
+ *               it sees its request's j-th new token (its own bit included)
+ *   max_new     no request has more new tokens than this (in [0, 2^30], at most 64 mask_words with a mask);
+ *               further ones get no readout
+ * Other arguments as kv_decode_attention; pages may be shared, nothing is stored. Scores, softmax
+ * statistics and sums are binary32; the softmax weights enter the product with V as in kv_decode_attention.
+ * A NaN or infinity of a new token's value reaches only the tokens that see it. max_new * num_q_heads
+ * stays at most 2^30 - 1, B * max_new * num_q_heads / 16 below 2^24. Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED (d, page_size), HIP. */
+damp_status kv_tree_attention(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* seq_lens,
+                              const int32_t* cu_new, const int64_t* mask, int32_t mask_words, int32_t T,
+                              int32_t B, int32_t max_new, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t d, int32_t num_pages, int32_t page_size, int32_t max_blocks,
+                              int32_t max_len, float scale, void* out, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Latent attention: a token's cache row is its latent c (d_latent channels) and the rotary part of its
+ * key (d_rope), shared by all heads: pages bf16 [num_pages][page_size][d_latent + d_rope], d_latent and
+ * d_rope 512 and 64, or 256 and 32; tables and slot maps as for the other caches.
+ *
+ * Stores c (dev bf16 [T][d_latent]) and k_rope (dev bf16 [T][d_rope]), both 16-byte aligned, of T tokens at
+ * slot_map (dev int64 [T]); a slot outside the cache (such as -1) is skipped, a repeated one races. */
+damp_status kv_latent_append(const void* c, const void* k_rope, const int64_t* slot_map, int32_t T,
+                             int32_t d_latent, int32_t d_rope, void* pages, int32_t num_pages,
+                             int32_t page_size, void* stream);
+
+size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t d_latent,
+                                           int32_t max_new, int32_t max_len);
+
+/* The absorbed form, for new tokens: with c_t | r_t the cached rows,
+ *   out = sum_t p_t c_t, p = softmax(scale q . (c_t | r_t)),
+ * q dev bf16 [T][num_heads][d_latent + d_rope] (a head's query times its key up-projection, then the rotary
+ * part), out dev bf16 [T][num_heads][d_latent] (the value up-projection follows). scale is that of the
+ * expanded form's channels. cu_new NULL: one token per request (T == B, max_new 1, no mask). Other arguments
+ * and limits as kv_tree_attention. The softmax weights enter the product rounded to bf16 (2^-9 of
+ * each), over the sum of the rounded ones. */
+damp_status kv_latent_attention(const void* q, const void* pages, const int32_t* block_table,
+                                const int32_t* seq_lens, const int32_t* cu_new, const int64_t* mask,
+                                int32_t mask_words, int32_t T, int32_t B, int32_t max_new,
+                                int32_t num_heads, int32_t d_latent, int32_t d_rope, int32_t num_pages,
+                                int32_t page_size, int32_t max_blocks, int32_t max_len, float scale,
+                                void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The expanded form, for prompts: request b's queries are rows cu_q[b] .. cu_q[b+1] - 1 of q and out, its
+ * keys and values rows cu_k[b] .. cu_k[b+1] - 1 of k, k_rope and v (its cached tokens first, then those of
+ * the queries); query i of n sees the first m - n + i + 1 of its m keys.
+ *   q           dev bf16 [Tq][num_heads][d + d / 2], its rotary part last
+ *   k, v        dev bf16: channels 0 .. d - 1 of token t and head h at t * token_stride + h * head_stride
+ *               elements (multiples of 8 up to 2^31; the up-projection may leave keys and values side by side)
+ *   k_rope      dev bf16 [Tk][d / 2]
+ *   out         dev bf16 [Tq][num_heads][d]; a query that sees no key gives 0
+ *   cu_q, cu_k  dev int32 [B + 1], ascending, kept inside [0, Tq] and [0, Tk]. Rows of out behind the last
+ *               request are not written.
+ * All 16-byte aligned but cu_q and cu_k. d is 64 or 128. Scores, statistics and sums are binary32, the
+ * weights rounded as in kv_latent_attention. A NaN or infinity of a token reaches only queries that see
+ * it. (Tq / 64 + B) * num_heads stays below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d), HIP. */
+damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride,
+                                       int64_t k_head_stride, const void* k_rope, const void* v,
+                                       int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,
+                                       const int32_t* cu_k, int32_t B, int32_t Tq, int32_t Tk,
+                                       int32_t num_heads, int32_t d, float scale, void* out, void* stream);
+
 /* Message for the last non-OK status returned on the calling thread ("" if none). The string
  * is owned by the library and valid until the thread's next call. (Library infrastructure: no
  * page defines it.) */

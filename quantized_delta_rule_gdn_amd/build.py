@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libdamp.so")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("damp_api.hip", "step_kernels.hip", "window_kernels.hip", "calib_kernels.hip",
             "stq_kernels.hip", "order_kernels.hip", "linear_kernels.hip", "prompt_kernels.hip",
-            "kv_kernels.hip")]
+            "kv_kernels.hip", "tree_kernels.hip", "page_kernels.hip", "latent_kernels.hip",
+            "latent_prompt_kernels.hip")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
@@ -45,7 +46,8 @@ FLAGS = [
 
 # The host layer validates caller data (NaN included), and the attention, linear-attention and
 # prompt kernels pass NaN and infinities of the caller's through, so these keep IEEE NaN semantics.
-IEEE_NANS = {"damp_api.hip", "linear_kernels.hip", "prompt_kernels.hip", "kv_kernels.hip"}
+IEEE_NANS = {"damp_api.hip", "linear_kernels.hip", "prompt_kernels.hip", "kv_kernels.hip",
+             "tree_kernels.hip", "page_kernels.hip", "latent_kernels.hip", "latent_prompt_kernels.hip"}
 
 
 def _compile(src: str, obj: str, extra: list[str]) -> tuple[int, str]:

@@ -1,0 +1,84 @@
+// attn_mask.h -- what the attention kernels of several tokens share: which positions a drafted token
+// sees, the softmax weights as operands, and values that are not finite.
+#pragma once
+
+#include "prompt_common.h"
+
+namespace damp {
+namespace {
+
+// A request's drafted tokens: rows first .. first + n - 1 of the queries, kept inside [0, T) whatever
+// cu holds, at the positions base .. base + n - 1.
+struct Drafts {
+  int first, n, base;
+};
+
+__device__ __forceinline__ Drafts drafts_of(const TreeArgs& a, int b) {
+  if (!a.cu) return Drafts{b, 1, max(a.seq_lens[b], 0) - 1};
+  const int lo = min(max(a.cu[b], 0), a.T), hi = min(max(a.cu[b + 1], lo), a.T);
+  return Drafts{lo, hi - lo, max(a.seq_lens[b], 0) - (hi - lo)};
+}
+
+// Bit x: drafted token `token` sees position base + rel + x (x < 32, rel > -32): every one before base,
+// from base on those in its mask, or without masks those up to its own.
+__device__ __forceinline__ uint32_t seen_window(const TreeArgs& a, const Drafts& dr, int token, int rel) {
+  const int from = max(rel, 0);
+  uint32_t bits;
+  if (a.mask) {
+    const uint64_t* words = a.mask + int64_t(dr.first + token) * a.words;
+    const int w = from >> 6, s = from & 63;
+    uint64_t x = w < a.words ? words[w] >> s : 0;
+    if (s > 32 && w + 1 < a.words) x |= words[w + 1] << (64 - s);
+    bits = static_cast<uint32_t>(x);
+  } else {
+    const int n = token + 1 - from;
+    bits = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+  }
+  return rel >= 0 ? bits : (bits << -rel) | ((1u << -rel) - 1);
+}
+
+// Softmax weights of one row as an operand of the product with V, and their sum. PIECES == 1: each
+// weight rounded to bf16 (2^-9 of it), the sum over the rounded ones, so that equal values come back
+// as they are. PIECES == 2: the upper 16 bits of the weight (less 2^-12) and the rest rounded, good
+// to 2^-15 + 2^-20 of it, the rest never 0 (an infinite value times 0 would be NaN).
+template <int PIECES, int N>
+__device__ __forceinline__ void pack_pair(float x0, float x1, int i, uint32_t (&w)[PIECES][N], float& sum) {
+  if constexpr (PIECES == 1) {
+    w[0][i] = pack_bf16(x0, x1);
+    sum += bf16_lo(w[0][i]) + bf16_hi(w[0][i]);
+  } else {
+    const uint32_t w0 = __float_as_uint(x0 * 0x1.ffep-1f), w1 = __float_as_uint(x1 * 0x1.ffep-1f);
+    w[0][i] = __builtin_amdgcn_perm(w1, w0, 0x07060302u);
+    w[1][i] = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
+    sum += x0 + x1;
+  }
+}
+
+template <int PIECES>
+__device__ __forceinline__ void pack_weights(const float (&p)[8], Frag* pf, float& sum) {
+  uint32_t w[PIECES][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pack_pair<PIECES>(p[2 * i], p[2 * i + 1], i, w, sum);
+#pragma unroll
+  for (int x = 0; x < PIECES; ++x) pf[x] = Frag{{w[x][0], w[x][1], w[x][2], w[x][3]}};
+}
+
+// 0x8000 / 0x80000000 bits of the halves that hold an infinity or a NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// Values that are not finite must not enter a product with rows that do not see their token: their
+// weight there is 0, but 0 * NaN is NaN. In tiles that hold drafted tokens they are taken out, and in
+// the end each row gets back those of the tokens that it sees (adding them up has their product's
+// result, whatever the weights).
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) { return w & ~((not_finite(w) >> 15) * 0xffffu); }
+
+__device__ __forceinline__ f32x4 add_odd(f32x4 o, uint2 v, bool seen) {   // 4 channels of one token
+  const float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+  const uint32_t odd[2] = {not_finite(v.x), not_finite(v.y)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] += seen && (odd[i >> 1] >> (16 * (i & 1)) & 0x8000u) ? x[i] : 0.0f;
+  return o;
+}
+
+}  // namespace
+}  // namespace damp

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -508,6 +509,42 @@ damp_status check_cache(int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_
 }
 
 constexpr double kLog2E = 1.4426950408889634;
+
+// Pages of any row that is whole 16-byte pieces, for the calls that only move rows.
+damp_status check_rows(int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_size) {
+  if (d < 8 || d % 8 || d > 2048)
+    return fail(DAMP_ERR_UNSUPPORTED, "d = %d: rows are moved for multiples of 8 channels up to 2,048", d);
+  return check_cache(Hkv, 64, num_pages, page_size);
+}
+
+damp_status check_latent(int32_t dc, int32_t dr, int32_t num_pages, int32_t page_size) {
+  if ((dc != 256 && dc != 512) || dr != dc / 8)
+    return fail(DAMP_ERR_UNSUPPORTED, "d_latent = %d, d_rope = %d: latents have 512 + 64 or 256 + 32 channels", dc, dr);
+  return check_cache(1, 64, num_pages, page_size);
+}
+
+// Sizes of an attention of several tokens, and its mask's.
+damp_status check_tokens(int32_t T, int32_t B, int32_t max_blocks, int32_t max_len, int32_t max_new, const void* mask, int32_t mask_words) {
+  if (T < 0 || B < 0 || max_blocks < 0 || max_len < 0 || max_len > (1 << 30))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "T (%d), B (%d) and max_blocks (%d) must be >= 0, max_len (%d) in [0, 2^30]", T, B, max_blocks, max_len);
+  if (max_new < 0 || max_new > (1 << 30)) return fail(DAMP_ERR_INVALID_ARGUMENT, "max_new (%d) outside [0, 2^30]", max_new);
+  if (mask && (mask_words < 1 || static_cast<int64_t>(mask_words) * 64 < max_new))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "mask_words (%d) must hold max_new = %d bits", mask_words, max_new);
+  return DAMP_OK;
+}
+
+damp_status check_workspace(const void* workspace, size_t have, size_t need) {
+  if (need > 0 && (!workspace || !aligned(workspace, 16) || have < need))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned and hold %zu bytes (%zu given)", need, workspace ? have : size_t(0));
+  return DAMP_OK;
+}
+
+// The attentions of several tokens take no more of them than there are rows.
+damp::TreeSizes tree_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_new, int32_t max_len) {
+  return damp::TreeSizes{B, Hq, Hkv, std::max(max_new, 1), max_len};
+}
+
+bool tree_fits(const damp::TreeSizes& z) { return static_cast<int64_t>(z.max_new) * z.Hq <= 0x3fffffff; }
 
 }  // namespace
 
@@ -1327,5 +1364,286 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages, con
   return launched(damp::launch_kv_attention(d, a, static_cast<hipStream_t>(stream)), "decode attention");
 }
 
-}  // extern "C"
+damp_status kv_fork_tables(const int32_t* src, const int32_t* dst, int32_t n, int32_t* seq_lens, int32_t B, const int32_t* free_pages,
+                           int32_t num_free, int32_t* block_table, int32_t max_blocks, int32_t* shares, int32_t num_pages, int32_t page_size,
+                           int32_t* copy_src, int32_t* copy_dst, int32_t* copy_rows, int32_t* used, void* stream) {
+  if (n < 0 || B < 0 || num_free < 0 || max_blocks < 0)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "n (%d), B (%d), num_free (%d) and max_blocks (%d) must be >= 0", n, B, num_free, max_blocks);
+  damp_status st = check_cache(1, 64, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (n > damp::kMaxForks) return fail(DAMP_ERR_UNSUPPORTED, "n = %d: at most %d forks", n, damp::kMaxForks);
+  if (!used || (n > 0 && (!src || !dst || !copy_src || !copy_dst || !copy_rows || !shares)) || (n > 0 && B > 0 && !seq_lens) ||
+      (n > 0 && B > 0 && max_blocks > 0 && !block_table) || (num_free > 0 && !free_pages))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among src/dst/seq_lens/free_pages/block_table/shares/copy_src/copy_dst/copy_rows/used");
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(seq_lens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) || !aligned(shares, 4) ||
+      !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !aligned(copy_rows, 4) || !aligned(used, 4))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned pointer (need natural alignment)");
+  damp::ForkArgs a{};
+  a.src = src;
+  a.dst = dst;
+  a.seq_lens = seq_lens;
+  a.free_pages = free_pages;
+  a.table = block_table;
+  a.shares = shares;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.copy_rows = copy_rows;
+  a.used = used;
+  a.n = n;
+  a.B = B;
+  a.num_free = num_free;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  a.page_log2 = page_log2(page_size);
+  return launched(damp::launch_kv_fork(a, static_cast<hipStream_t>(stream)), "forked tables");
+}
 
+damp_status kv_copy_pages(const int32_t* src, const int32_t* dst, const int32_t* rows, int32_t n, void* k_pages, void* v_pages, int32_t num_pages,
+                          int32_t num_kv_heads, int32_t page_size, int32_t d, void* stream) {
+  if (n < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "n (%d) must be >= 0", n);
+  damp_status st = check_rows(num_kv_heads, d, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (n == 0) return ok();
+  if (!src || !dst || !k_pages) return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among src/dst/k_pages");
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(rows, 4) || !aligned(k_pages, 16) || !aligned(v_pages, 16))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "the pages must be 16-byte, src, dst and rows 4-byte aligned");
+  damp::CopyArgs a{};
+  a.src = src;
+  a.dst = dst;
+  a.rows = rows;
+  a.k_pages = static_cast<uint8_t*>(k_pages);
+  a.v_pages = static_cast<uint8_t*>(v_pages);
+  a.n = n;
+  a.num_pages = num_pages;
+  a.Hkv = num_kv_heads;
+  a.page_log2 = page_log2(page_size);
+  a.d = d;
+  return launched(damp::launch_kv_copy(a, static_cast<hipStream_t>(stream)), "page copies");
+}
+
+damp_status kv_compact(const int32_t* kept, const int32_t* cu_kept, int32_t num_kept, const int32_t* seq_lens, const int32_t* new_lens, int32_t B,
+                       const int32_t* block_table, int32_t max_blocks, void* k_pages, void* v_pages, int32_t num_pages, int32_t num_kv_heads,
+                       int32_t page_size, int32_t d, int32_t* out_lens, void* stream) {
+  if (num_kept < 0 || B < 0 || max_blocks < 0)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_kept (%d), B (%d) and max_blocks (%d) must be >= 0", num_kept, B, max_blocks);
+  damp_status st = check_rows(num_kv_heads, d, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (B == 0) return ok();
+  if (!cu_kept || !seq_lens || !new_lens || !k_pages || !out_lens || (num_kept > 0 && !kept) || (max_blocks > 0 && !block_table))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among kept/cu_kept/seq_lens/new_lens/block_table/k_pages/out_lens");
+  if (!aligned(kept, 4) || !aligned(cu_kept, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(out_lens, 4) ||
+      !aligned(k_pages, 16) || !aligned(v_pages, 16))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "the pages must be 16-byte, the other arrays 4-byte aligned");
+  if (static_cast<int64_t>(B) * num_kv_heads > kMaxGroups / 2)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B * num_kv_heads = %lld exceeds the grid limit", static_cast<long long>(B) * num_kv_heads);
+  damp::CompactArgs a{};
+  a.kept = kept;
+  a.cu = cu_kept;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.table = block_table;
+  a.k_pages = static_cast<uint8_t*>(k_pages);
+  a.v_pages = static_cast<uint8_t*>(v_pages);
+  a.out_lens = out_lens;
+  a.K = num_kept;
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  a.Hkv = num_kv_heads;
+  a.page_log2 = page_log2(page_size);
+  a.d = d;
+  return launched(damp::launch_kv_compact(a, static_cast<hipStream_t>(stream)), "kept tokens");
+}
+
+size_t kv_free_pages_workspace_bytes(int32_t num_pages) { return num_pages <= 0 ? 0 : damp::kv_free_ws_bytes(num_pages); }
+
+damp_status kv_free_pages(const int32_t* keep_lens, const int32_t* seq_lens, int32_t B, const int32_t* block_table, int32_t max_blocks, int32_t* shares,
+                          int32_t num_pages, int32_t page_size, int32_t* freed, int32_t* num_freed, void* workspace, size_t workspace_bytes, void* stream) {
+  if (B < 0 || max_blocks < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d) and max_blocks (%d) must be >= 0", B, max_blocks);
+  damp_status st = check_cache(1, 64, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (!shares || !freed || !num_freed || (B > 0 && !seq_lens) || (B > 0 && max_blocks > 0 && !block_table))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among seq_lens/block_table/shares/freed/num_freed");
+  if (!aligned(keep_lens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(shares, 4) || !aligned(freed, 4) || !aligned(num_freed, 4))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned pointer (need natural alignment)");
+  if (B > kMaxGroups) return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d exceeds the grid limit", B);
+  st = check_workspace(workspace, workspace_bytes, damp::kv_free_ws_bytes(num_pages));
+  if (st != DAMP_OK) return st;
+  damp::FreeArgs a{};
+  a.keep_lens = keep_lens;
+  a.seq_lens = seq_lens;
+  a.table = block_table;
+  a.shares = shares;
+  a.freed = freed;
+  a.num_freed = num_freed;
+  a.ws = static_cast<int32_t*>(workspace);
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.num_pages = num_pages;
+  a.page_log2 = page_log2(page_size);
+  return launched(damp::launch_kv_free(a, static_cast<hipStream_t>(stream)), "freed pages");
+}
+
+size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t num_kv_heads, int32_t d, int32_t max_new, int32_t max_len) {
+  if (B <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads || (d != 64 && d != 128) || max_new < 0 || max_new > (1 << 30) ||
+      max_len < 0 || max_len > (1 << 30))
+    return 0;
+  const damp::TreeSizes z = tree_sizes(B, num_q_heads, num_kv_heads, max_new, max_len);
+  return tree_fits(z) && damp::kv_tree_grid(z, d) <= kMaxGroups ? damp::kv_tree_ws_bytes(z, d) : 0;
+}
+
+damp_status kv_tree_attention(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table, const int32_t* seq_lens,
+                              const int32_t* cu_new, const int64_t* mask, int32_t mask_words, int32_t T, int32_t B, int32_t max_new,
+                              int32_t num_q_heads, int32_t num_kv_heads, int32_t d, int32_t num_pages, int32_t page_size, int32_t max_blocks,
+                              int32_t max_len, float scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  damp_status st = check_tokens(T, B, max_blocks, max_len, max_new, mask, mask_words);
+  if (st != DAMP_OK) return st;
+  st = check_cache(num_kv_heads, d, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (num_q_heads <= 0 || num_q_heads % num_kv_heads)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)", num_q_heads, num_kv_heads);
+  if (B == 0 || T == 0 || max_new == 0) return ok();
+  if (!q || !k_pages || !v_pages || !seq_lens || !cu_new || !out || (max_blocks > 0 && !block_table))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among q/k_pages/v_pages/block_table/seq_lens/cu_new/out");
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_new, 4) || !aligned(mask, 8))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages and out must be 16-byte, mask 8-byte, block_table, seq_lens and cu_new 4-byte aligned");
+  const damp::TreeSizes z = tree_sizes(B, num_q_heads, num_kv_heads, max_new, max_len);
+  if (!tree_fits(z) || damp::kv_tree_grid(z, d) > kMaxGroups)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_new = %d and max_len = %d exceeds the grid limit", B, max_new, max_len);
+  st = check_workspace(workspace, workspace_bytes, damp::kv_tree_ws_bytes(z, d));
+  if (st != DAMP_OK) return st;
+  damp::TreeArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k_pages = static_cast<uint8_t*>(const_cast<void*>(k_pages));
+  a.v_pages = static_cast<uint8_t*>(const_cast<void*>(v_pages));
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = static_cast<uint8_t*>(out);
+  a.ws = static_cast<float*>(workspace);
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2E);
+  a.B = B;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.page_log2 = page_log2(page_size);
+  a.max_len = max_len;
+  a.cu = cu_new;
+  a.mask = reinterpret_cast<const uint64_t*>(mask);
+  a.words = mask_words;
+  a.T = T;
+  a.max_new = max_new;
+  return launched(damp::launch_kv_tree(d, a, static_cast<hipStream_t>(stream)), "tree attention");
+}
+
+damp_status kv_latent_append(const void* c, const void* k_rope, const int64_t* slot_map, int32_t T, int32_t d_latent, int32_t d_rope, void* pages,
+                             int32_t num_pages, int32_t page_size, void* stream) {
+  if (T < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "T (%d) must be >= 0", T);
+  damp_status st = check_latent(d_latent, d_rope, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (T == 0) return ok();
+  if (!c || !k_rope || !slot_map || !pages) return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among c/k_rope/slot_map/pages");
+  if (!aligned(c, 16) || !aligned(k_rope, 16) || !aligned(pages, 16) || !aligned(slot_map, 8))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "c, k_rope and the pages must be 16-byte, slot_map 8-byte aligned");
+  damp::LatentAppendArgs a{};
+  a.c = static_cast<const uint8_t*>(c);
+  a.k_rope = static_cast<const uint8_t*>(k_rope);
+  a.slot_map = slot_map;
+  a.pages = static_cast<uint8_t*>(pages);
+  a.num_slots = static_cast<int64_t>(num_pages) << page_log2(page_size);
+  a.T = T;
+  a.dc = d_latent;
+  a.dr = d_rope;
+  return launched(damp::launch_latent_append(a, static_cast<hipStream_t>(stream)), "latent append");
+}
+
+size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t d_latent, int32_t max_new, int32_t max_len) {
+  if (B <= 0 || num_heads <= 0 || (d_latent != 256 && d_latent != 512) || max_new < 0 || max_new > (1 << 30) || max_len < 0 || max_len > (1 << 30)) return 0;
+  const damp::TreeSizes z = tree_sizes(B, num_heads, 1, max_new, max_len);
+  return tree_fits(z) && damp::latent_grid(z, d_latent) <= kMaxGroups ? damp::latent_ws_bytes(z, d_latent) : 0;
+}
+
+damp_status kv_latent_attention(const void* q, const void* pages, const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_new,
+                                const int64_t* mask, int32_t mask_words, int32_t T, int32_t B, int32_t max_new, int32_t num_heads, int32_t d_latent,
+                                int32_t d_rope, int32_t num_pages, int32_t page_size, int32_t max_blocks, int32_t max_len, float scale, void* out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  damp_status st = check_tokens(T, B, max_blocks, max_len, max_new, mask, mask_words);
+  if (st != DAMP_OK) return st;
+  st = check_latent(d_latent, d_rope, num_pages, page_size);
+  if (st != DAMP_OK) return st;
+  if (num_heads <= 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "num_heads (%d) must be positive", num_heads);
+  if (!cu_new && (T != B || max_new > 1 || mask))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "without cu_new there is one token a request: T (%d) must be B (%d), max_new (%d) 1, and no mask", T, B, max_new);
+  if (B == 0 || T == 0 || max_new == 0) return ok();
+  if (!q || !pages || !seq_lens || !out || (max_blocks > 0 && !block_table))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among q/pages/block_table/seq_lens/out");
+  if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(mask, 8))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages and out must be 16-byte, mask 8-byte, block_table, seq_lens and cu_new 4-byte aligned");
+  const damp::TreeSizes z = tree_sizes(B, num_heads, 1, max_new, max_len);
+  if (!tree_fits(z) || damp::latent_grid(z, d_latent) > kMaxGroups)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_new = %d and max_len = %d exceeds the grid limit", B, max_new, max_len);
+  st = check_workspace(workspace, workspace_bytes, damp::latent_ws_bytes(z, d_latent));
+  if (st != DAMP_OK) return st;
+  damp::TreeArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k_pages = static_cast<uint8_t*>(const_cast<void*>(pages));
+  a.table = block_table;
+  a.seq_lens = seq_lens;
+  a.out = static_cast<uint8_t*>(out);
+  a.ws = static_cast<float*>(workspace);
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * kLog2E);
+  a.B = B;
+  a.Hq = num_heads;
+  a.Hkv = 1;
+  a.num_pages = num_pages;
+  a.max_blocks = max_blocks;
+  a.page_log2 = page_log2(page_size);
+  a.max_len = max_len;
+  a.cu = cu_new;
+  a.mask = reinterpret_cast<const uint64_t*>(mask);
+  a.words = mask_words;
+  a.T = T;
+  a.max_new = max_new;
+  return launched(damp::launch_latent(d_latent, a, static_cast<hipStream_t>(stream)), "latent attention");
+}
+
+damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* k_rope, const void* v,
+                                       int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q, const int32_t* cu_k, int32_t B, int32_t Tq,
+                                       int32_t Tk, int32_t num_heads, int32_t d, float scale, void* out, void* stream) {
+  if (B < 0 || Tq < 0 || Tk < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d), Tq (%d) and Tk (%d) must be >= 0", B, Tq, Tk);
+  if (num_heads <= 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "num_heads (%d) must be positive", num_heads);
+  if (d != 64 && d != 128) return fail(DAMP_ERR_UNSUPPORTED, "d = %d: prompts by latents support d in {64, 128}", d);
+  for (const int64_t x : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+    if (x < 0 || x % 8 || x > (int64_t(1) << 31))
+      return fail(DAMP_ERR_INVALID_ARGUMENT, "a stride (%lld) is not a multiple of 8 elements in [0, 2^31]", static_cast<long long>(x));
+  if (B == 0 || Tq == 0) return ok();
+  if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !k_rope || !v)))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among q/k/k_rope/v/cu_q/cu_k/out");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(k_rope, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "q, k, k_rope, v and out must be 16-byte, cu_q and cu_k 4-byte aligned");
+  if (damp::latent_prompt_grid(B, Tq, num_heads) > kMaxGroups)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "Tq = %d tokens of %d requests with %d heads exceed the grid limit", Tq, B, num_heads);
+  damp::LatentPromptArgs a{};
+  a.q = static_cast<const uint8_t*>(q);
+  a.k = static_cast<const uint8_t*>(k);
+  a.k_rope = static_cast<const uint8_t*>(k_rope);
+  a.v = static_cast<const uint8_t*>(v);
+  a.out = static_cast<uint8_t*>(out);
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.k_token = k_token_stride;
+  a.k_head = k_head_stride;
+  a.v_token = v_token_stride;
+  a.v_head = v_head_stride;
+  // (a scale of 0 becomes the least one: the kernel forms 0 times -infinity for keys that a query does not see)
+  a.scale_log2 = std::max(static_cast<float>(std::fabs(static_cast<double>(scale)) * kLog2E), 0x1p-126f);
+  a.flip = std::signbit(scale) ? 0x80008000u : 0;
+  a.B = B;
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.H = num_heads;
+  return launched(damp::launch_latent_prompt(d, a, static_cast<hipStream_t>(stream)), "latent prompt attention");
+}
+
+}  // extern "C"

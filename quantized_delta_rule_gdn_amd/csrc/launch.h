@@ -179,6 +179,112 @@ size_t kv_attention_ws_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int3
 int64_t kv_attention_grid(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_len);
 hipError_t launch_kv_attention(int d, const AttnArgs& a, hipStream_t s);
 
+// Attention of several new tokens of each request (tree_kernels.hip): AttnArgs with q and out
+// [T][Hq][d], request b's tokens at the rows cu[b] .. cu[b + 1] - 1 (cu nullptr: row b).
+struct TreeArgs : AttnArgs {
+  const int32_t* cu;         // [B + 1] or nullptr
+  const uint64_t* mask;      // [T][words] or nullptr: each token sees those up to itself
+  int32_t T, words;
+  int32_t max_new;           // no request has more of its tokens computed
+};
+
+struct TreeSizes {
+  int32_t B, Hq, Hkv, max_new, max_len;
+};
+
+int64_t kv_tree_grid(const TreeSizes& z, int32_t d);   // workgroups of its largest launch
+size_t kv_tree_ws_bytes(const TreeSizes& z, int32_t d);
+hipError_t launch_kv_tree(int d, const TreeArgs& a, hipStream_t s);
+
+// Latents (latent_kernels.hip): pages [num_pages][page][dc + dr] bf16, dr = dc / 8.
+struct LatentAppendArgs {
+  const uint8_t* c;          // [T][dc] bf16
+  const uint8_t* k_rope;     // [T][dr]
+  const int64_t* slot_map;   // [T]
+  uint8_t* pages;
+  int64_t num_slots;
+  int32_t T, dc, dr;
+};
+
+hipError_t launch_latent_append(const LatentAppendArgs& a, hipStream_t s);
+// Absorbed form: TreeArgs with Hkv = 1, k_pages the latents, q [T][Hq][dc + dr], out [T][Hq][dc].
+int64_t latent_grid(const TreeSizes& z, int32_t dc);
+size_t latent_ws_bytes(const TreeSizes& z, int32_t dc);
+hipError_t launch_latent(int dc, const TreeArgs& a, hipStream_t s);
+
+// Expanded form (latent_prompt_kernels.hip): dr = d / 2 rotary channels; strides in elements.
+struct LatentPromptArgs {
+  const uint8_t* q;          // [Tq][H][d + dr] bf16
+  const uint8_t* k;          // token t, head h at t * k_token + h * k_head, d channels
+  const uint8_t* k_rope;     // [Tk][dr]
+  const uint8_t* v;          // as k
+  uint8_t* out;              // [Tq][H][d]
+  const int32_t* cu_q;       // [B + 1]
+  const int32_t* cu_k;       // [B + 1]
+  int64_t k_token, k_head, v_token, v_head;
+  float scale_log2;          // |scale| log2(e)
+  uint32_t flip;             // sign bits of the queries where scale is negative
+  int32_t B, Tq, Tk, H;
+};
+
+int64_t latent_prompt_grid(int32_t B, int32_t Tq, int32_t H);
+hipError_t launch_latent_prompt(int d, const LatentPromptArgs& a, hipStream_t s);
+
+// The life of the cache's pages (page_kernels.hip). shares[p]: requests that hold page p beyond the first.
+constexpr int kMaxForks = 8000;
+
+struct ForkArgs {
+  const int32_t* src;        // [n] rows of the table
+  const int32_t* dst;        // [n]
+  int32_t* seq_lens;         // [B]
+  const int32_t* free_pages; // [num_free]
+  int32_t* table;            // [B][max_blocks]
+  int32_t* shares;           // [num_pages]
+  int32_t* copy_src;         // [n]
+  int32_t* copy_dst;
+  int32_t* copy_rows;
+  int32_t* used;             // [1]
+  int32_t n, B, num_free, max_blocks, num_pages, page_log2;
+};
+
+struct CopyArgs {
+  const int32_t* src;        // [n] pages
+  const int32_t* dst;
+  const int32_t* rows;       // [n] rows of each page that are copied, or nullptr: all
+  uint8_t* k_pages;          // [num_pages][Hkv][page][d] of 2 bytes
+  uint8_t* v_pages;          // or nullptr
+  int32_t n, num_pages, Hkv, page_log2, d;
+};
+
+struct CompactArgs {
+  const int32_t* kept;       // [K] places among a request's new tokens, ascending
+  const int32_t* cu;         // [B + 1]
+  const int32_t* seq_lens;   // [B]
+  const int32_t* new_lens;   // [B]
+  const int32_t* table;      // [B][max_blocks]
+  uint8_t* k_pages;
+  uint8_t* v_pages;          // or nullptr
+  int32_t* out_lens;         // [B]
+  int32_t K, B, max_blocks, num_pages, Hkv, page_log2, d;
+};
+
+struct FreeArgs {
+  const int32_t* keep_lens;  // [B] or nullptr: none is kept
+  const int32_t* seq_lens;   // [B]
+  const int32_t* table;      // [B][max_blocks]
+  int32_t* shares;           // [num_pages]
+  int32_t* freed;            // [num_pages]
+  int32_t* num_freed;        // [1]
+  int32_t* ws;
+  int32_t B, max_blocks, num_pages, page_log2;
+};
+
+hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s);
+hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s);
+hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t s);
+size_t kv_free_ws_bytes(int32_t num_pages);
+hipError_t launch_kv_free(const FreeArgs& a, hipStream_t s);
+
 // Calibration (calib_kernels.hip). Sizes are validated by the caller: d in {16, 32, 64, 128},
 // H * d <= alloc_max_rows(), H * (r_max / g) <= alloc_max_groups(), R % g == 0.
 hipError_t launch_risk_scores(int d, const float* S, int32_t n, int32_t H, const float* abar,

@@ -41,7 +41,10 @@ EXPORTS = (
     "damp_batch_order", "damp_decode_step_ordered", "damp_decode_step_fused_ordered",
     "damp_window_step_ordered", "damp_decode_step_sorted", "fp32_linear_step",
     "fp32_prefill_workspace_bytes", "fp32_linear_prefill", "fp32_delta_prefill", "kv_build_tables",
-    "kv_append", "kv_decode_attention_workspace_bytes", "kv_decode_attention",
+    "kv_append", "kv_decode_attention_workspace_bytes", "kv_decode_attention", "kv_fork_tables", "kv_copy_pages",
+    "kv_compact", "kv_free_pages_workspace_bytes", "kv_free_pages", "kv_tree_attention_workspace_bytes",
+    "kv_tree_attention", "kv_latent_append", "kv_latent_attention_workspace_bytes", "kv_latent_attention",
+    "kv_latent_prompt_attention",
 )
 
 
@@ -69,7 +72,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is not built: run `python -m quantized_delta_rule_gdn_amd.build`"
                           " or __graft_entry__.build()")
     L = ctypes.CDLL(LIB_PATH)
-    P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     LP = ctypes.POINTER(Layout)
     sig = {
         "damp_block_bytes": ([LP], SZ),
@@ -130,6 +133,20 @@ def load() -> ctypes.CDLL:
         "kv_decode_attention_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
         "kv_decode_attention": ([P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32,
                                  ctypes.c_float, P, P, P, P, SZ, P], ctypes.c_int),
+        "kv_fork_tables": ([P, P, I32, P, I32, P, I32, P, I32, P, I32, I32, P, P, P, P, P], ctypes.c_int),
+        "kv_copy_pages": ([P, P, P, I32, P, P, I32, I32, I32, I32, P], ctypes.c_int),
+        "kv_compact": ([P, P, I32, P, P, I32, P, I32, P, P, I32, I32, I32, I32, P, P], ctypes.c_int),
+        "kv_free_pages_workspace_bytes": ([I32], SZ),
+        "kv_free_pages": ([P, P, I32, P, I32, P, I32, I32, P, P, P, SZ, P], ctypes.c_int),
+        "kv_tree_attention_workspace_bytes": ([I32, I32, I32, I32, I32, I32], SZ),
+        "kv_tree_attention": ([P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, I32, I32,
+                               ctypes.c_float, P, P, SZ, P], ctypes.c_int),
+        "kv_latent_append": ([P, P, P, I32, I32, I32, P, I32, I32, P], ctypes.c_int),
+        "kv_latent_attention_workspace_bytes": ([I32, I32, I32, I32, I32], SZ),
+        "kv_latent_attention": ([P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I32, I32, I32, I32,
+                                 ctypes.c_float, P, P, SZ, P], ctypes.c_int),
+        "kv_latent_prompt_attention": ([P, P, I64, I64, P, P, I64, I64, P, P, I32, I32, I32, I32, I32,
+                                        ctypes.c_float, P, P], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -877,3 +894,293 @@ def kv_decode_attention(q, k_pages, v_pages, block_table, seq_lens, out, scale=N
                                      _ptr(k_new) if k_new is not None else None,
                                      _ptr(v_new) if v_new is not None else None, _ptr(out), ws, nb,
                                      s))
+
+
+# ------------------------------------------------------------------------------------------
+# the life of the cache's pages
+# ------------------------------------------------------------------------------------------
+def _table(block_table, B, dev):
+    """max_blocks of a block table int32 [B, max_blocks] (B None: whatever it has), and its B."""
+    torch = _torch()
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    rows, blocks = block_table.shape
+    if B is None:
+        B = rows
+    _fit(block_table, "block_table", torch.int32, (B, blocks), dev)
+    return B, blocks
+
+
+def _rows(k_pages, v_pages, dev):
+    """Pages [num_pages, Hkv, page_size, d], or [num_pages, page_size, d] (latents) without v_pages."""
+    torch = _torch()
+    if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 3 and v_pages is None:
+        n, page, d = k_pages.shape
+        _fit(k_pages, "k_pages", torch.bfloat16, (n, page, d), dev)
+        return n, 1, page, d
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a tensor [num_pages, Hkv, page_size, d], or [num_pages, page_size, d] without v_pages")
+    n, Hkv, page, d = k_pages.shape
+    _fit(k_pages, "k_pages", torch.bfloat16, (n, Hkv, page, d), dev)
+    if v_pages is not None:
+        _fit(v_pages, "v_pages", torch.bfloat16, (n, Hkv, page, d), dev)
+    return n, Hkv, page, d
+
+
+def _size(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a 1-dimensional tensor")
+    return t.numel()
+
+
+def kv_fork_tables(src, dst, seq_lens, free_pages, block_table, shares, page_size: int, copy_src, copy_dst, copy_rows,
+                   used, stream=None) -> None:
+    """Request dst[i] of the table becomes a copy of request src[i] (int32 [n], no dst twice or also a
+    src): its full pages are shared (shares, int32 [num_pages], counts a page's holders beyond the
+    first), a partly filled last page is replaced by the next one of free_pages, and its copy is
+    listed in copy_src, copy_dst, copy_rows (int32 [n]; -1, -1, 0 where there is none) for
+    kv_copy_pages. seq_lens int32 [B], block_table int32 [B, max_blocks] and shares are updated; used
+    int32 [1]: pages needed."""
+    torch = _torch()
+    dev = _first(src, "src", torch.int32)
+    n = src.shape[0]
+    for name, t in (("dst", dst), ("copy_src", copy_src), ("copy_dst", copy_dst), ("copy_rows", copy_rows)):
+        _fit(t, name, torch.int32, (n,), dev)
+    B, blocks = _table(block_table, None, dev)
+    _fit(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    free, pages = _size(free_pages, "free_pages"), _size(shares, "shares")
+    _fit(free_pages, "free_pages", torch.int32, (free,), dev)
+    _fit(shares, "shares", torch.int32, (pages,), dev)
+    _fit(used, "used", torch.int32, (1,), dev)
+    _sizes(n=n, B=B, max_blocks=blocks, num_free=free, num_pages=pages)
+    with _On(dev, stream) as s:
+        _check(load().kv_fork_tables(_ptr(src), _ptr(dst), n, _ptr(seq_lens), B, _ptr(free_pages), free, _ptr(block_table), blocks, _ptr(shares), pages,
+                                     max(-1, min(page_size, 1 << 30)), _ptr(copy_src), _ptr(copy_dst), _ptr(copy_rows), _ptr(used), s))
+
+
+def kv_copy_pages(src, dst, k_pages, v_pages=None, rows=None, stream=None) -> None:
+    """Copies page src[i] to page dst[i] (int32 [n]; one outside the cache: skipped; no dst twice or also
+    a src), all heads, the first rows[i] rows or all of them. Pages bf16 [num_pages, Hkv, page_size, d],
+    or [num_pages, page_size, d] (latents, without v_pages)."""
+    torch = _torch()
+    dev = _first(src, "src", torch.int32)
+    n = src.shape[0]
+    _fit(dst, "dst", torch.int32, (n,), dev)
+    if rows is not None:
+        _fit(rows, "rows", torch.int32, (n,), dev)
+    pages, Hkv, page, d = _rows(k_pages, v_pages, dev)
+    _sizes(n=n, num_pages=pages, Hkv=Hkv, page_size=page, d=d)
+    with _On(dev, stream) as s:
+        _check(load().kv_copy_pages(_ptr(src), _ptr(dst), _ptr(rows) if rows is not None else None, n, _ptr(k_pages),
+                                    _ptr(v_pages) if v_pages is not None else None, pages, Hkv, page, d, s))
+
+
+def kv_compact(kept, cu_kept, seq_lens, new_lens, block_table, k_pages, v_pages, out_lens, stream=None) -> None:
+    """Keeps some of each request's last new_lens[b] tokens and moves them together, in place: the j-th
+    kept one, token kept[cu_kept[b] + j] of them (int32, ascending), becomes token j. out_lens int32 [B]:
+    the requests' lengths after it. seq_lens, new_lens int32 [B]; cu_kept int32 [B + 1]; pages as in
+    kv_copy_pages. The pages that tokens move in must be the request's alone."""
+    torch = _torch()
+    dev = _first(seq_lens, "seq_lens", torch.int32)
+    B = seq_lens.shape[0]
+    num = _size(kept, "kept")
+    _fit(kept, "kept", torch.int32, (num,), dev)
+    _fit(cu_kept, "cu_kept", torch.int32, (B + 1,), dev)
+    _fit(new_lens, "new_lens", torch.int32, (B,), dev)
+    _fit(out_lens, "out_lens", torch.int32, (B,), dev)
+    _, blocks = _table(block_table, B, dev)
+    pages, Hkv, page, d = _rows(k_pages, v_pages, dev)
+    _sizes(num_kept=num, B=B, max_blocks=blocks, num_pages=pages, Hkv=Hkv, page_size=page, d=d)
+    with _On(dev, stream) as s:
+        _check(load().kv_compact(_ptr(kept), _ptr(cu_kept), num, _ptr(seq_lens), _ptr(new_lens), B, _ptr(block_table), blocks, _ptr(k_pages),
+                                 _ptr(v_pages) if v_pages is not None else None, pages, Hkv, page, d, _ptr(out_lens), s))
+
+
+def kv_free_pages_workspace_bytes(num_pages: int) -> int:
+    """Bytes of the workspace of kv_free_pages."""
+    _sizes(num_pages=num_pages)
+    return load().kv_free_pages_workspace_bytes(num_pages)
+
+
+def kv_free_pages(keep_lens, seq_lens, block_table, shares, page_size: int, freed, num_freed, workspace=None, stream=None) -> None:
+    """Gives back each request's pages behind its first keep_lens[b] tokens (int32 [B], or None: all its
+    pages), up to those of seq_lens[b] tokens. A page with shares (int32 [num_pages]) left loses one;
+    the others are listed in freed (int32 [num_pages]), ids ascending, their number in num_freed
+    (int32 [1]). The table keeps its entries."""
+    torch = _torch()
+    dev = _first(seq_lens, "seq_lens", torch.int32)
+    B = seq_lens.shape[0]
+    if keep_lens is not None:
+        _fit(keep_lens, "keep_lens", torch.int32, (B,), dev)
+    _, blocks = _table(block_table, B, dev)
+    pages = _size(shares, "shares")
+    _fit(shares, "shares", torch.int32, (pages,), dev)
+    _fit(freed, "freed", torch.int32, (pages,), dev)
+    _fit(num_freed, "num_freed", torch.int32, (1,), dev)
+    _sizes(B=B, max_blocks=blocks, num_pages=pages)
+    L = load()
+    with _On(dev, stream) as s:
+        held, ws, nb = _workspace(workspace, L.kv_free_pages_workspace_bytes(pages), dev)
+        _check(L.kv_free_pages(_ptr(keep_lens) if keep_lens is not None else None, _ptr(seq_lens), B, _ptr(block_table), blocks, _ptr(shares), pages,
+                               max(-1, min(page_size, 1 << 30)), _ptr(freed), _ptr(num_freed), ws, nb, s))
+
+
+# ------------------------------------------------------------------------------------------
+# attention of several new tokens, and of latents
+# ------------------------------------------------------------------------------------------
+def _mask(mask, T, max_new, dev):
+    """Words of a mask int64 [T, words] (0 without one) and max_new, which holds for none more than T."""
+    torch = _torch()
+    words = 0
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+            raise ValueError("mask must be a tensor [T, words]")
+        words = mask.shape[1]
+        _fit(mask, "mask", torch.int64, (T, words), dev)
+    max_new = T if max_new is None else min(max_new, T)
+    if mask is not None and max_new > 64 * words:
+        raise ValueError(f"mask has {words} words of 64 tokens, max_new is {max_new}")
+    _sizes(mask_words=words, T=T, max_new=max_new)
+    return words, min(max_new, 1 << 30)
+
+
+def kv_tree_attention_workspace_bytes(B: int, num_q_heads: int, num_kv_heads: int, d: int, max_new: int, max_len: int) -> int:
+    """Bytes of the workspace of kv_tree_attention with that ``max_new`` (and no more than its T) and ``max_len``."""
+    _sizes(B=B, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, d=d, max_new=max_new)
+    return load().kv_tree_attention_workspace_bytes(B, num_q_heads, num_kv_heads, d, max_new, max(-1, min(max_len, 1 << 30)))
+
+
+def kv_tree_attention(q, k_pages, v_pages, block_table, seq_lens, cu_new, out, mask=None, max_new=None, scale=None,
+                      max_len=None, workspace=None, stream=None) -> None:
+    """Attention of several new tokens per request, their keys and values already in the cache (kv_append):
+    q, out bf16 [T, Hq, d], request b's tokens the rows cu_new[b] .. cu_new[b + 1] - 1 (int32 [B + 1]) and
+    the last positions of its seq_lens[b]. Each sees all positions before them, and of them those up
+    to itself, or with ``mask`` (int64 [T, words]) those whose bit is set: bit j % 64 of word j / 64 for
+    the request's j-th new token. ``max_new``: an upper bound of a request's new tokens (T by default: give
+    it where there are several requests); later rows are left as they are. Other arguments as kv_decode_attention."""
+    torch = _torch()
+    dev = _first(q, "q", torch.bfloat16, 3)
+    T, Hq, d = q.shape
+    n, Hkv, page, dc = _pages(k_pages, v_pages, dev)
+    if d != dc:
+        raise ValueError(f"q has {d} channels, the pages {dc}")
+    _fit(out, "out", torch.bfloat16, (T, Hq, d), dev)
+    B, blocks = _table(block_table, None, dev)
+    _fit(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _fit(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    words, max_new = _mask(mask, T, max_new, dev)
+    _sizes(B=B, max_blocks=blocks)
+    max_len = max(-1, min(blocks * page if max_len is None else max_len, 1 << 30))
+    L = load()
+    with _On(dev, stream) as s:
+        held, ws, nb = _workspace(workspace, L.kv_tree_attention_workspace_bytes(B, Hq, Hkv, d, max_new, max_len), dev)
+        _check(L.kv_tree_attention(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_lens), _ptr(cu_new),
+                                   _ptr(mask) if mask is not None else None, words, T, B, max_new, Hq, Hkv, d, n, page, blocks, max_len,
+                                   d ** -0.5 if scale is None else scale, _ptr(out), ws, nb, s))
+
+
+def _latents(pages, dev):
+    torch = _torch()
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 3:
+        raise ValueError("pages must be a tensor [num_pages, page_size, d_latent + d_rope]")
+    n, page, width = pages.shape
+    _fit(pages, "pages", torch.bfloat16, (n, page, width), dev)
+    dr = width // 9                                  # d_rope = d_latent / 8
+    return n, page, width - dr, dr
+
+
+def kv_latent_append(c, k_rope, slot_map, pages, stream=None) -> None:
+    """Stores latents c bf16 [T, d_latent] and rotary keys k_rope bf16 [T, d_rope] side by side at the cache
+    slots slot_map int64 [T] (outside the cache: skipped); pages bf16 [num_pages, page_size, d_latent + d_rope]."""
+    torch = _torch()
+    dev = _first(slot_map, "slot_map", torch.int64)
+    T = slot_map.shape[0]
+    n, page, dc, dr = _latents(pages, dev)
+    _fit(c, "c", torch.bfloat16, (T, dc), dev)
+    _fit(k_rope, "k_rope", torch.bfloat16, (T, dr), dev)
+    _sizes(T=T, num_pages=n, page_size=page, d_latent=dc)
+    with _On(dev, stream) as s:
+        _check(load().kv_latent_append(_ptr(c), _ptr(k_rope), _ptr(slot_map), T, dc, dr, _ptr(pages), n, page, s))
+
+
+def kv_latent_attention_workspace_bytes(B: int, num_heads: int, d_latent: int, max_new: int, max_len: int) -> int:
+    """Bytes of the workspace of kv_latent_attention with that ``max_new`` (and no more than its T) and ``max_len``."""
+    _sizes(B=B, num_heads=num_heads, d_latent=d_latent, max_new=max_new)
+    return load().kv_latent_attention_workspace_bytes(B, num_heads, d_latent, max_new, max(-1, min(max_len, 1 << 30)))
+
+
+def kv_latent_attention(q, pages, block_table, seq_lens, out, scale: float, cu_new=None, mask=None, max_new=None, max_len=None,
+                        workspace=None, stream=None) -> None:
+    """Latent attention in its absorbed form: q bf16 [T, H, d_latent + d_rope] (each head's query times its
+    key up-projection, then its rotary part) over the cached rows c | k_rope, which all heads share; out
+    bf16 [T, H, d_latent] is in latent channels (the value up-projection follows). ``scale`` is the expanded
+    form's. Without ``cu_new`` one token per request (T == B), else as kv_tree_attention, masks included."""
+    torch = _torch()
+    dev = _first(q, "q", torch.bfloat16, 3)
+    T, H, width = q.shape
+    n, page, dc, dr = _latents(pages, dev)
+    if width != dc + dr:
+        raise ValueError(f"q has {width} channels, the pages {dc + dr}")
+    _fit(out, "out", torch.bfloat16, (T, H, dc), dev)
+    B, blocks = _table(block_table, None, dev)
+    _fit(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if cu_new is None:
+        if mask is not None:
+            raise ValueError("mask needs cu_new")
+        max_new = 1
+    else:
+        _fit(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    words, max_new = _mask(mask, T, max_new, dev)
+    _sizes(B=B, max_blocks=blocks)
+    max_len = max(-1, min(blocks * page if max_len is None else max_len, 1 << 30))
+    L = load()
+    with _On(dev, stream) as s:
+        held, ws, nb = _workspace(workspace, L.kv_latent_attention_workspace_bytes(B, H, dc, max_new, max_len), dev)
+        _check(L.kv_latent_attention(_ptr(q), _ptr(pages), _ptr(block_table), _ptr(seq_lens), _ptr(cu_new) if cu_new is not None else None,
+                                     _ptr(mask) if mask is not None else None, words, T, B, max_new, H, dc, dr, n, page, blocks, max_len, scale,
+                                     _ptr(out), ws, nb, s))
+
+
+def _strided(t, name, shape, dev):
+    """Token and head strides of a bf16 tensor [T, H, d] whose channels lie together (a view of a wider one)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev or t.dtype != torch.bfloat16 or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a bfloat16 tensor {shape} on {dev}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must lie together")
+    # (of one token or head the stride does not matter, and may be anything)
+    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0) if t.numel() else (0, 0)
+
+
+def kv_latent_prompt_attention(q, k, k_rope, v, cu_q, out, cu_k=None, scale=None, stream=None) -> None:
+    """Latent attention over prompts, in its expanded form: q bf16 [Tq, H, d + d / 2], k and v bf16 [Tk, H, d]
+    (the up-projected latents; views of a wider tensor will do, with strides of multiples of 8 elements),
+    k_rope bf16 [Tk, d / 2] for all heads, out bf16 [Tq, H, d]. Request b's queries are the rows
+    cu_q[b] .. cu_q[b + 1] - 1 (int32 [B + 1]), its keys the rows of cu_k (by default cu_q); the queries
+    are its last tokens and each sees the keys up to its own. ``scale`` defaults to (d + d / 2)^-0.5."""
+    torch = _torch()
+    dev = _first(q, "q", torch.bfloat16, 3)
+    Tq, H, width = q.shape
+    d = width // 3 * 2
+    if width != d + d // 2:
+        raise ValueError(f"q has {width} channels, not d + d / 2")
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [Tk, H, d]")
+    Tk = k.shape[0]
+    ks, vs = _strided(k, "k", (Tk, H, d), dev), _strided(v, "v", (Tk, H, d), dev)
+    _fit(k_rope, "k_rope", torch.bfloat16, (Tk, d // 2), dev)
+    _fit(out, "out", torch.bfloat16, (Tq, H, d), dev)
+    B = _size(cu_q, "cu_q") - 1
+    _fit(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    if B < 0:
+        raise ValueError("cu_q must have B + 1 entries")
+    if cu_k is None:
+        cu_k = cu_q
+    _fit(cu_k, "cu_k", torch.int32, (B + 1,), dev)
+    _sizes(B=B, Tq=Tq, Tk=Tk, H=H)
+    with _On(dev, stream) as s:
+        _check(load().kv_latent_prompt_attention(_ptr(q), _ptr(k), *ks, _ptr(k_rope), _ptr(v), *vs, _ptr(cu_q), _ptr(cu_k), B, Tq, Tk, H, d,
+                                                 width ** -0.5 if scale is None else scale, _ptr(out), s))
