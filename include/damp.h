@@ -642,14 +642,15 @@ damp_status kv_fork_tables(const int32_t* src, const int32_t* dst, int32_t n, in
 
 /* Copies page src[i] to page dst[i] (dev int32 [n]), all heads, keys and values: the first rows[i] rows (dev
  * int32 [n], clamped to the page), or all with rows NULL. A page outside the cache is skipped. No dst
- * may appear twice or as a src. */
+ * may appear twice or as a src. n * num_kv_heads, twice that with v_pages, stays below 2^31 for pages of
+ * up to 64 KB a head (and as many times less for larger ones). */
 damp_status kv_copy_pages(const int32_t* src, const int32_t* dst, const int32_t* rows, int32_t n,
                           void* k_pages, void* v_pages, int32_t num_pages, int32_t num_kv_heads,
                           int32_t page_size, int32_t d, void* stream);
 
 /* Kept tokens moved together, in place (accepted drafts; a cache that drops tokens). Of the last
  * new_lens[b] of request b's seq_lens[b] tokens, the ones listed are kept, the others dropped:
- *   kept      dev int32 [num_kept]: entries cu_kept[b] .. cu_kept[b + 1] - 1 (dev int32 [B + 1]) are
+ *   kept      dev int32 [num_kept] (up to 2^30): entries cu_kept[b] .. cu_kept[b + 1] - 1 (dev int32 [B + 1]) are
  *             request b's, ascending, each in [0, new_lens[b]): the j-th one's key and value move to
  *             the j-th of those positions. A list that does not ascend leaves unspecified rows
  *             (inside the request's pages); an entry past the new tokens moves nothing.
@@ -746,7 +747,7 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
  * the queries); query i of n sees the first m - n + i + 1 of its m keys.
  *   q           dev bf16 [Tq][num_heads][d + d / 2], its rotary part last
  *   k, v        dev bf16: channels 0 .. d - 1 of token t and head h at t * token_stride + h * head_stride
- *               elements (multiples of 8 up to 2^31; the up-projection may leave keys and values side by side)
+ *               elements (multiples of 8, up to 2^24 for tokens; the up-projection may leave keys and values side by side)
  *   k_rope      dev bf16 [Tk][d / 2]
  *   out         dev bf16 [Tq][num_heads][d]; a query that sees no key gives 0
  *   cu_q, cu_k  dev int32 [B + 1], ascending, kept inside [0, Tq] and [0, Tk]. Rows of out behind the last

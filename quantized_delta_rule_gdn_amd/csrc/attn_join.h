@@ -1,5 +1,5 @@
-// attn_join.h -- the second launch of the attention kernels of several tokens: requests that were cut
-// into items are joined.
+// attn_join.h -- how the attention kernels of several tokens share out their work, and their second
+// launch, which joins the parts of requests that were cut.
 #pragma once
 
 #include <algorithm>
@@ -10,61 +10,199 @@
 namespace damp {
 namespace {
 
-// The items of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels a
-// thread, 1,024 / D rows a workgroup. Bound by the stream of the items.
-template <int D, int GRAIN>
-__global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const AttnPlan plan, int groups) {
-  constexpr int LPR = D / 4, RPG = 256 / LPR;      // threads a row, rows a workgroup
-  __shared__ int64_t sh[8];
+// ---- how the work is shared out --------------------------------------------------------------------
+// A request's query rows (its new tokens' heads of one key-value head) are taken in tiles of `rows`, and
+// its cached tokens in runs; a workgroup takes one (run, key-value head, tile). The runs are cut on the
+// device, where the lengths are: by the least chunk with which the workgroups are no more than the chip
+// holds at once, as often over as 1.5 workgroups for each (request, head, tile) need, so that a launch
+// is whole rounds of much the same length.
+struct TokenPlan {
+  int rows;       // query rows of a tile
+  int heads;      // rows of the largest tile there is
+  int tiles;      // row tiles of a request with the most new tokens
+  int slots;      // workgroups that the chip holds at once
+  int groups;     // of the launch
+  int whole;      // no request is cut
+};
+
+// One workgroup's part. b < 0: none.
+struct Spot {
+  int b, kvh, tile;
+  int split, splits;     // its part of the request's tokens
+  int at;                // its place in the workspace
+};
+
+struct Share {           // of a request: row tiles, tokens
+  int tiles, len;
+};
+
+__device__ __forceinline__ Share share_of(const TreeArgs& a, const TokenPlan& plan, int b) {
+  const int64_t rows = int64_t(min(drafts_of(a, b).n, a.max_new)) * (a.Hq / a.Hkv);
+  return Share{static_cast<int>((rows + plan.rows - 1) / plan.rows), length_of(a, b)};
+}
+
+// What the workgroups leave in the workspace: a tile's partial readouts, {maximum, sum} of its rows, and
+// each request's {first place, runs}.
+template <int D>
+struct Parts {
+  float* o;
+  float2* ml;
+  int2* info;
+  __device__ Parts(const TreeArgs& a, const TokenPlan& plan) {
+    const int64_t n = int64_t(plan.groups) * plan.heads;
+    o = a.ws;
+    ml = reinterpret_cast<float2*>(a.ws + n * D);
+    info = reinterpret_cast<int2*>(ml + n);
+  }
+};
+
+inline size_t parts_bytes(const TokenPlan& p, const TreeSizes& z, int32_t d) {
+  return p.whole ? 0 : static_cast<size_t>(p.groups) * p.heads * (static_cast<size_t>(d) + 2) * 4 + static_cast<size_t>(z.B) * 8;
+}
+
+// Every wave finds its workgroup's part for itself, its lanes taking a request each. Workgroups go round the 8
+// dies, which have an L2 each: a die takes neighbouring parts of the list (request, run, head, tile), so
+// that row tiles that read the same keys meet in one L2.
+template <int GRAIN, int D>
+__device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan) {
+  const unsigned id = __builtin_amdgcn_workgroup_id_x();
+  if (plan.whole) {
+    const int per = plan.tiles * a.Hkv;
+    const int at = per == 1 ? static_cast<int>(id) : static_cast<int>(id % 8 * (plan.groups / 8) + id / 8);   // (rounded up to 8)
+    const int b = at / per, unit = at % per;
+    return Spot{b < a.B ? b : -1, unit / plan.tiles, unit % plan.tiles, 0, 1, 0};
+  }
+  const int lane = __builtin_amdgcn_workitem_id_x() & 63;
+  const Share own = lane < a.B ? share_of(a, plan, lane) : Share{0, 0};
+  const auto over_requests = [&](auto&& f) {
+    int64_t x = f(own);
+    for (int b = lane + 64; b < a.B; b += 64) x += f(share_of(a, plan, b));
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
+    return x * a.Hkv;
+  };
+  const int64_t least = over_requests([](const Share& s) { return int64_t(s.tiles); });
+  const int64_t work = over_requests([](const Share& s) { return int64_t(s.tiles) * s.len; });
+  const int64_t budget = max((3 * least / 2 + plan.slots - 1) / plan.slots, int64_t(1)) * plan.slots;   // at most plan.groups
+  int64_t chunk = max((work + budget - 1) / budget, int64_t(1)), n;
+  for (int round = 0;; ++round) {
+    chunk = min((chunk + GRAIN - 1) / GRAIN * GRAIN, int64_t(1) << 30);
+    n = over_requests([&](const Share& s) { return int64_t(s.tiles) * items_of(s.len, static_cast<int>(chunk)); });
+    if (n <= budget || chunk == int64_t(1) << 30) break;
+    // as much longer as there are too many (twice, where that has not done for a while)
+    chunk = max(round < 6 ? chunk * n / budget : 2 * chunk, chunk + GRAIN);
+  }
+  const int per_die = static_cast<int>((n + 7) / 8), at = static_cast<int>(id % 8) * per_die + static_cast<int>(id / 8);
+  if (static_cast<int>(id / 8) >= per_die || at >= n) return Spot{-1, 0, 0, 0, 1, 0};
+  for (int b0 = 0, before = 0; b0 < a.B; b0 += 64) {
+    const Share s = b0 == 0 ? own : b0 + lane < a.B ? share_of(a, plan, b0 + lane) : Share{0, 0};
+    const int runs = items_of(s.len, static_cast<int>(chunk)), mine = s.tiles * runs * a.Hkv;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int first = before + incl - mine;
+    if (const uint64_t here = __ballot(at >= first && at < first + mine); here != 0) {
+      const int l = __builtin_ctzll(here), tiles = __builtin_amdgcn_readlane(s.tiles, l), first_l = __builtin_amdgcn_readlane(first, l);
+      const int local = at - first_l, splits = __builtin_amdgcn_readlane(runs, l), unit = local / tiles;
+      if (local == 0 && __builtin_amdgcn_workitem_id_x() == 0) Parts<D>(a, plan).info[b0 + l] = make_int2(first_l, splits);
+      return Spot{b0 + l, unit % a.Hkv, local % tiles, unit / a.Hkv, splits, at};
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return Spot{-1, 0, 0, 0, 1, 0};
+}
+
+// The runs of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels a
+// thread, 1,024 / D rows a workgroup, eight runs at a time. Bound by the stream of the parts.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const TokenPlan plan, int groups) {
+  constexpr int LPR = D / 4, RPG = 256 / LPR, U = 8;   // threads a row, rows a workgroup
   const int tid = __builtin_amdgcn_workitem_id_x();
-  const int64_t id = __builtin_amdgcn_workgroup_id_x();
+  const unsigned id = __builtin_amdgcn_workgroup_id_x();
   const int units = a.Hkv * plan.tiles;
   const int group = static_cast<int>(id % groups), unit = static_cast<int>(id / groups % units), b = static_cast<int>(id / groups / units);
   const int tile = unit % plan.tiles, kvh = unit / plan.tiles, G = a.Hq / a.Hkv;
+  const Parts<D> parts(a, plan);
+  const int2 info = parts.info[b];                 // (not written where a request has no rows: not used either)
   const Drafts dr = drafts_of(a, b);
-  const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, tile0 = int64_t(tile) * plan.rows;
-  if (tile0 + group * RPG >= rows) return;
-  const int chunk = chunk_of<GRAIN>(a, plan, sh), n = items_of(length_of(a, b), chunk);
-  if (n == 1) return;                              // it has its readout already
-  int64_t before = 0;
-  const int apart = requests_step(a);
-  for (int x = tid & (apart - 1); x < b; x += apart) before += items_of(length_of(a, x), chunk);
-  before = requests_sum(a, before, sh);
-  const int in_tile = group * RPG + tid / LPR;
-  const int64_t row = tile0 + in_tile;
+  const int rows = min(dr.n, a.max_new) * G, tile0 = tile * plan.rows;
+  if (tile0 + group * RPG >= rows || info.y == 1) return;   // (one run: it has its readout already)
+  const int in_tile = group * RPG + tid / LPR, row = tile0 + in_tile;
   if (in_tile >= plan.heads || row >= rows) return;
-  const int64_t step = int64_t(units) * plan.heads;      // between a unit's items
-  const int64_t first = (before * units + unit) * plan.heads + in_tile;
-  const float4* po = reinterpret_cast<const float4*>(a.ws + first * D) + tid % LPR;
-  const float2* ml = reinterpret_cast<const float2*>(a.ws + int64_t(plan.items) * step * D) + first;
-  float m = -INFINITY;
-  for (int s = 0; s < n; ++s) m = fmaxf(m, ml[s * step].x);
-  const float base = m == -INFINITY ? 0.0f : m;
+  const int tiles = (rows + plan.rows - 1) / plan.rows;
+  const int64_t step = int64_t(a.Hkv) * tiles * plan.heads;      // between a tile's runs
+  const int64_t first = (int64_t(info.x) + kvh * tiles + tile) * plan.heads + in_tile;
+  const float4* po = reinterpret_cast<const float4*>(parts.o + first * D) + tid % LPR;
+  const float2* ml = parts.ml + first;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const float2 x = ml[s * step];
-    const float4 v = po[s * step * LPR];
-    const float f = pow2(x.x - base);
-    l = fmaf(f, x.y, l);
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
+  float m = -INFINITY, l = 0.0f;
+  for (int s0 = 0; s0 < info.y; s0 += U) {
+    float2 x[U];
+    float4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int s = min(s0 + i, info.y - 1);
+      x[i] = ml[s * step];
+      v[i] = po[s * step * LPR];
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (s0 + i >= info.y) x[i] = make_float2(-INFINITY, 0.0f);
+      top = fmaxf(top, x[i].x);
+    }
+    const float base = top == -INFINITY ? 0.0f : top, shrink = pow2(m - base);
+    m = top;
+    l *= shrink;
+    acc.x *= shrink; acc.y *= shrink; acc.z *= shrink; acc.w *= shrink;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (s0 + i >= info.y) break;                 // (its values stand in for none)
+      const float f = pow2(x[i].x - base);
+      l = fmaf(f, x[i].y, l);
+      acc.x = fmaf(f, v[i].x, acc.x);
+      acc.y = fmaf(f, v[i].y, acc.y);
+      acc.z = fmaf(f, v[i].z, acc.z);
+      acc.w = fmaf(f, v[i].w, acc.w);
+    }
   }
   const float back = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (int64_t(dr.first + static_cast<int>(row / G)) * a.Hq + kvh * G + row % G) * LPR + tid % LPR;
+  const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * LPR + tid % LPR;
   reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack_bf16(acc.x * back, acc.y * back), pack_bf16(acc.z * back, acc.w * back));
 }
 
-// Workgroups that a (request, row tile) takes.
-inline int64_t join_groups(const AttnPlan& p, int d) { return (p.heads + 1024 / d - 1) / (1024 / d); }
+// Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where they alone
+// fill the chip four times over.
+inline TokenPlan token_plan(const TreeSizes& z, int rows, int slots, int whole) {
+  const int64_t all = int64_t(z.max_new) * (z.Hq / z.Hkv);
+  TokenPlan p;
+  p.rows = rows;
+  p.tiles = static_cast<int>((all + rows - 1) / rows);
+  p.heads = static_cast<int>(std::min<int64_t>(all, rows));
+  p.slots = slots;
+  const int64_t most = int64_t(z.B) * z.Hkv * p.tiles;
+  p.whole = z.max_len <= whole || most >= 4 * slots;
+  const int64_t groups = !p.whole ? (3 * most / 2 + slots - 1) / slots * slots : p.tiles * z.Hkv == 1 ? most : (most + 7) / 8 * 8;
+  p.groups = static_cast<int>(std::min<int64_t>(groups, 0x7fffffff));
+  return p;
+}
 
-template <int D, int GRAIN>
-void launch_join(const TreeArgs& a, const AttnPlan& p, hipStream_t s) {
+// Workgroups that a (request, head, row tile) takes to join.
+inline int64_t join_groups(const TokenPlan& p, int d) { return (p.heads + 1024 / d - 1) / (1024 / d); }
+
+// Workgroups of the larger launch.
+inline int64_t token_groups(const TokenPlan& p, const TreeSizes& z, int d) {
+  return p.whole ? p.groups : std::max<int64_t>(p.groups, int64_t(z.B) * z.Hkv * p.tiles * join_groups(p, d));
+}
+
+template <int D>
+void launch_join(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
+  if (p.whole) return;
   const int64_t groups = join_groups(p, D);
-  hipLaunchKernelGGL((attn_join_kernel<D, GRAIN>), dim3(static_cast<unsigned>(int64_t(a.B) * a.Hkv * p.tiles * groups)), dim3(256), 0, s, a, p,
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(static_cast<unsigned>(int64_t(a.B) * a.Hkv * p.tiles * groups)), dim3(256), 0, s, a, p,
                      static_cast<int>(groups));
 }
 

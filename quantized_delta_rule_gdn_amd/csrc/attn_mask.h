@@ -7,6 +7,8 @@
 namespace damp {
 namespace {
 
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
+
 // A request's drafted tokens: rows first .. first + n - 1 of the queries, kept inside [0, T) whatever
 // cu holds, at the positions base .. base + n - 1.
 struct Drafts {
@@ -37,6 +39,17 @@ __device__ __forceinline__ uint32_t seen_window(const TreeArgs& a, const Drafts&
   return rel >= 0 ? bits : (bits << -rel) | ((1u << -rel) - 1);
 }
 
+// x, in a branch that few tiles take: what goes by it is not worked out before the branch (for all tiles, to be
+// selected from).
+template <typename T>
+__device__ __forceinline__ T rarely(T x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// An operand of ones: its product with the weights is their sum, in every row of the C tile.
+__device__ __forceinline__ Frag ones() { return Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}; }
+
 // Softmax weights of one row as an operand of the product with V, and their sum. PIECES == 1: each
 // weight rounded to bf16 (2^-9 of it), the sum over the rounded ones, so that equal values come back
 // as they are. PIECES == 2: the upper 16 bits of the weight (less 2^-12) and the rest rounded, good
@@ -52,6 +65,11 @@ __device__ __forceinline__ void pack_pair(float x0, float x1, int i, uint32_t (&
     w[1][i] = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
     sum += x0 + x1;
   }
+}
+
+// (one piece, the sum left to a product with ones)
+__device__ __forceinline__ Frag round_weights(const float (&p)[8]) {
+  return Frag{{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])}};
 }
 
 template <int PIECES>

@@ -16,14 +16,13 @@ constexpr int kAttnTile = 32;
 // chip once. (Cut by the longest length the host knows of instead, 64 requests of 128 to 8,192
 // tokens took 244-260 us against 186-197 us of as many bytes in even lengths.)
 struct AttnPlan {
-  int tiles;      // groups of 16 query heads per key-value head (of `rows` query rows, for several tokens)
-  int heads;      // query heads of a full group (query rows)
+  int tiles;      // groups of 16 query heads per key-value head
+  int heads;      // query heads of a full group
   int per_unit;
   int items;      // per_unit + B, or B where no request is cut
-  int rows;       // several tokens: query rows a workgroup takes
 };
 
-constexpr int kAttnLeast = 8 * kAttnTile;    // tokens: no chunk is shorter (of one token's attention)
+constexpr int kAttnLeast = 8 * kAttnTile;    // tokens: no chunk is shorter
 
 // Tokens of request b that are read.
 __device__ __forceinline__ int length_of(const AttnArgs& a, int b) {
@@ -48,7 +47,6 @@ __device__ __forceinline__ int64_t requests_sum(const AttnArgs& a, int64_t x, in
   return (sh[0] + sh[1]) + (sh[2] + sh[3]);
 }
 
-template <int GRAIN = kAttnLeast>
 __device__ __forceinline__ int chunk_of(const AttnArgs& a, const AttnPlan& plan, int64_t* sh) {
   const int step = requests_step(a);
   int64_t total = 0;
@@ -56,18 +54,17 @@ __device__ __forceinline__ int chunk_of(const AttnArgs& a, const AttnPlan& plan,
   total = requests_sum(a, total, sh);
   const int64_t chunk = (total + plan.per_unit - 1) / plan.per_unit;
   // (no request is longer than 2^30: a longer chunk would be the same)
-  return static_cast<int>(min(max((chunk + GRAIN - 1) / GRAIN * GRAIN, int64_t(GRAIN)), int64_t(1) << 30));
+  return static_cast<int>(min(max((chunk + kAttnLeast - 1) / kAttnLeast * kAttnLeast, int64_t(kAttnLeast)), int64_t(1) << 30));
 }
 
 struct Item {   // part `split` of `splits` of request b; b < 0: none
   int b, split, splits;
 };
 
-template <int GRAIN = kAttnLeast>
 __device__ __forceinline__ Item item_of(const AttnArgs& a, const AttnPlan& plan, int item, int64_t* sh) {
   if (plan.items == a.B) return Item{item, 0, 1};   // none is cut (4,000 requests of 60 tokens: 30 us, 95 with the search)
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63, wv = tid >> 6;
-  const int chunk = chunk_of<GRAIN>(a, plan, sh), step = requests_step(a);
+  const int chunk = chunk_of(a, plan, sh), step = requests_step(a);
   int* wave_items = reinterpret_cast<int*>(sh + 4);
   int* found = wave_items + 4;
   if (step > 64 && tid == 0) found[0] = -1;

@@ -1418,14 +1418,17 @@ damp_status kv_copy_pages(const int32_t* src, const int32_t* dst, const int32_t*
   a.Hkv = num_kv_heads;
   a.page_log2 = page_log2(page_size);
   a.d = d;
+  // (a page has at most 2,048 runs: no overflow)
+  if (static_cast<int64_t>(n) * num_kv_heads > 0x7fffffff || damp::kv_copy_items(a) > 0x7fffffff)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "n = %d copies of %d heads exceed the launch limit", n, num_kv_heads);
   return launched(damp::launch_kv_copy(a, static_cast<hipStream_t>(stream)), "page copies");
 }
 
 damp_status kv_compact(const int32_t* kept, const int32_t* cu_kept, int32_t num_kept, const int32_t* seq_lens, const int32_t* new_lens, int32_t B,
                        const int32_t* block_table, int32_t max_blocks, void* k_pages, void* v_pages, int32_t num_pages, int32_t num_kv_heads,
                        int32_t page_size, int32_t d, int32_t* out_lens, void* stream) {
-  if (num_kept < 0 || B < 0 || max_blocks < 0)
-    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_kept (%d), B (%d) and max_blocks (%d) must be >= 0", num_kept, B, max_blocks);
+  if (num_kept < 0 || num_kept > (1 << 30) || B < 0 || max_blocks < 0)
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "num_kept (%d) outside [0, 2^30], or B (%d) or max_blocks (%d) below 0", num_kept, B, max_blocks);
   damp_status st = check_rows(num_kv_heads, d, num_pages, page_size);
   if (st != DAMP_OK) return st;
   if (B == 0) return ok();
@@ -1614,9 +1617,12 @@ damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_t
   if (B < 0 || Tq < 0 || Tk < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d), Tq (%d) and Tk (%d) must be >= 0", B, Tq, Tk);
   if (num_heads <= 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "num_heads (%d) must be positive", num_heads);
   if (d != 64 && d != 128) return fail(DAMP_ERR_UNSUPPORTED, "d = %d: prompts by latents support d in {64, 128}", d);
-  for (const int64_t x : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
-    if (x < 0 || x % 8 || x > (int64_t(1) << 31))
-      return fail(DAMP_ERR_INVALID_ARGUMENT, "a stride (%lld) is not a multiple of 8 elements in [0, 2^31]", static_cast<long long>(x));
+  for (const int64_t x : {k_token_stride, v_token_stride})
+    if (x < 0 || x % 8 || x > (1 << 24))
+      return fail(DAMP_ERR_INVALID_ARGUMENT, "a token stride (%lld) is not a multiple of 8 elements in [0, 2^24]", static_cast<long long>(x));
+  for (const int64_t x : {k_head_stride, v_head_stride})
+    if (x < 0 || x % 8 || x > (int64_t(1) << 40))
+      return fail(DAMP_ERR_INVALID_ARGUMENT, "a head stride (%lld) is not a multiple of 8 elements in [0, 2^40]", static_cast<long long>(x));
   if (B == 0 || Tq == 0) return ok();
   if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !k_rope || !v)))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among q/k/k_rope/v/cu_q/cu_k/out");

@@ -10,11 +10,10 @@ namespace {
 
 // ---- the store of new latents --------------------------------------------------------------------
 // A copy by slot map, 16 bytes a thread.
-__global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppendArgs a) {
+__global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppendArgs a, int64_t step) {
   const int pc = a.dc / 8, per_row = pc + a.dr / 8;
   const int64_t n = int64_t(a.T) * per_row;
   const int64_t first = int64_t(__builtin_amdgcn_workgroup_id_x()) * 256 + __builtin_amdgcn_workitem_id_x();
-  const int64_t step = __builtin_amdgcn_grid_size_x();
   for (int64_t x = first; x < n; x += step) {
     const int64_t t = x / per_row;
     const int c = static_cast<int>(x - t * per_row);
@@ -35,59 +34,53 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppendAr
 // Few heads are bound by the stream of the cache, many by the products.
 constexpr int kLatTile = 64;
 
-template <int DC>
+template <int DC, int NW>
 struct LatGeo {
   static constexpr int DR = DC / 8, W = DC + DR;     // channels of a row
   static constexpr int CH = W / 8;                   // 16-byte pieces of a row
-  static constexpr int ST = 16 * CH / 64;            // pieces that a lane carries: 16 rows a wave,
-  static constexpr int PW = CH % 8 == 0 ? 8 : 4;     // of which a load takes PW neighbouring ones
-  static constexpr int RL = 64 / PW, NR = 16 / RL;   // of RL rows; NR loads for all rows
+  static constexpr int ROWS = kLatTile / NW;         // rows of a tile that a wave carries
+  static constexpr int NR = ROWS / 8, PK = (CH + 7) / 8;   // by loads of 8 neighbouring pieces of 8 rows
   static constexpr int LD = W * 2 + 32;              // bytes between rows in LDS: an odd number of 32-byte units
 };
 
-template <int DC, int R, bool P16, int PIECES>
-__global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const TreeArgs a, const AttnPlan plan) {
-  using Geo = LatGeo<DC>;
-  constexpr int W = Geo::W, KS = W / 32, CB = DC / 64;   // k steps; 16-channel blocks of a wave's share
-  constexpr int RW = R == 4 ? 2 : R, TB = R == 4 ? 2 : 1, TG = 4 / TB;   // row groups and token blocks a wave scores; token groups
+template <int DC, int R, int NW, bool P16, int PIECES>
+__global__ __launch_bounds__(64 * NW, 2) void latent_kernel(const TreeArgs a, const TokenPlan plan) {
+  using Geo = LatGeo<DC, NW>;
+  constexpr int W = Geo::W, KS = W / 32, CB = DC / (16 * NW);   // k steps; 16-channel blocks of a wave's share
+  constexpr int TG = NW / R, TB = 4 / TG;            // the waves that share 16 rows' scores; blocks of 16 tokens each takes
   constexpr int LDP = kLatTile * 2 + 16;
   __shared__ __align__(16) uint8_t tile_k[kLatTile * Geo::LD];
   __shared__ __align__(16) uint8_t tile_p[PIECES][16 * R][LDP];
   __shared__ float part[TG][16 * R];
-  __shared__ uint32_t tile_live[4], tile_odd[4];
-  __shared__ int64_t sh[8];
+  __shared__ uint32_t tile_live[NW], tile_odd[NW];
 
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const unsigned id = __builtin_amdgcn_workgroup_id_x();
-  const int item = id / plan.tiles, tile = id % plan.tiles, H = a.Hq;
-
-  const Item it = item_of<kLatTile>(a, plan, item, sh);
-  const int b = it.b, split = it.split, splits = it.splits;
+  const Spot spot = spot_of<kLatTile, DC>(a, plan);
+  const int b = spot.b, split = spot.split, splits = spot.splits, H = a.Hq;
   if (b < 0) return;
   const Drafts dr = drafts_of(a, b);
-  const int64_t rows = int64_t(min(dr.n, a.max_new)) * H, row0 = int64_t(tile) * (16 * R);
+  const int64_t rows = int64_t(min(dr.n, a.max_new)) * H, row0 = int64_t(spot.tile) * (16 * R);
   if (row0 >= rows) return;
+  const Parts<DC> parts(a, plan);
   const int len = length_of(a, b);
   const int share = ((len + splits - 1) / splits + kLatTile - 1) / kLatTile * kLatTile;
   const int begin = min(split * share, len), end = min(begin + share, len);
   const int in_page = (1 << a.page_log2) - 1;
   const int live_rows = static_cast<int>(min(rows - row0, int64_t(16 * R)));
-  const int wr = R == 4 ? wv >> 1 : 0, wt = R == 4 ? wv & 1 : wv;   // this wave's row groups and token blocks
+  const int wr = wv / TG, wt = wv % TG;              // this wave's rows and tokens
 
-  int token[RW];
-  Frag qf[RW][KS];
+  const unsigned my_row = static_cast<unsigned>(row0) + min(16 * wr + r, live_rows - 1);
+  const int token = my_row / H;
+  Frag qf[KS];
+  {
+    const int64_t at = int64_t(dr.first + token) * H + my_row % H;
 #pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    const unsigned row = static_cast<unsigned>(row0) + min(16 * (wr * RW + j) + r, live_rows - 1);
-    token[j] = row / H;
-    const int64_t at = int64_t(dr.first + token[j]) * H + row % H;
-#pragma unroll
-    for (int x = 0; x < KS; ++x) qf[j][x] = load_frag(a.q + (at * W + g * 8 + x * 32) * 2);
+    for (int x = 0; x < KS; ++x) qf[x] = load_frag(a.q + (at * W + g * 8 + x * 32) * 2);
   }
   f32x4 o[R][CB];
-  float mx[R], sum[RW];
+  float mx[R], sum = 0.0f;
   bool taken_out = false;            // values that are not finite (the same for all waves)
 #pragma unroll
   for (int j = 0; j < R; ++j) {
@@ -95,42 +88,39 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
 #pragma unroll
     for (int m = 0; m < CB; ++m) o[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-#pragma unroll
-  for (int j = 0; j < RW; ++j) sum[j] = 0.0f;
 
-  // Each wave carries 16 rows of a tile. Their pages are looked up one tile ahead of their loads.
-  uint4 st[Geo::ST];
+  // Each wave carries its rows of a tile. Their pages are looked up one tile ahead of their loads.
+  constexpr uint32_t kAll = (1u << Geo::ROWS) - 1;
+  u32x4 st[Geo::NR][Geo::PK];
   uint32_t carried = 0;              // which of the rows in st exist
-  const int row_l = lane / Geo::PW, piece_l = lane % Geo::PW;
+  const int row_l = lane / 8, piece_l = lane % 8;
   const auto page_of = [&](int t0) -> int {
-    const int pos = min(t0 + 16 * wv + (P16 ? 0 : r), end - 1);
+    const int pos = min(t0 + Geo::ROWS * wv + (P16 ? 0 : lane % Geo::ROWS), end - 1);
     return a.table[int64_t(b) * a.max_blocks + (pos >> a.page_log2)];
   };
   const auto issue = [&](int t0, int pid) {
-    const int left = min(max(end - (t0 + 16 * wv), 0), 16);
-    const uint4* pages = reinterpret_cast<const uint4*>(a.k_pages) + piece_l;
+    const int first = t0 + Geo::ROWS * wv, left = min(max(end - first, 0), Geo::ROWS);
+    int64_t row[Geo::NR];
     if constexpr (P16) {
       const int id0 = __builtin_amdgcn_readfirstlane(pid);
       const bool fine = id0 >= 0 && id0 < a.num_pages && left > 0;
       carried = fine ? (1u << left) - 1 : 0;
       // (rows past the end lie in the same page; where there is no page, the first one's rows stand in)
-      const int64_t row = fine ? (int64_t(id0) << a.page_log2) + ((t0 + 16 * wv) & in_page) : 0;
+      const int64_t at = fine ? (int64_t(id0) << a.page_log2) + (first & in_page) : 0;
 #pragma unroll
-      for (int n = 0; n < Geo::NR; ++n) {
-        const uint4* src = pages + (row + n * Geo::RL + row_l) * Geo::CH;
-#pragma unroll
-        for (int k = 0; k < Geo::ST / Geo::NR; ++k) st[n * (Geo::ST / Geo::NR) + k] = src[k * Geo::PW];
-      }
+      for (int n = 0; n < Geo::NR; ++n) row[n] = at + 8 * n + row_l;
     } else {
-      const bool fine = pid >= 0 && pid < a.num_pages && r < left;
-      carried = static_cast<uint32_t>(__ballot(fine)) & 0xffffu;
-      const uint32_t row = fine ? (static_cast<uint32_t>(pid) << a.page_log2) + ((t0 + 16 * wv + r) & in_page) : 0;
+      const bool fine = pid >= 0 && pid < a.num_pages && lane % Geo::ROWS < left;
+      carried = static_cast<uint32_t>(__ballot(fine)) & kAll;
+      const uint32_t mine = fine ? (static_cast<uint32_t>(pid) << a.page_log2) + ((first + lane % Geo::ROWS) & in_page) : 0;
 #pragma unroll
-      for (int n = 0; n < Geo::NR; ++n) {
-        const uint4* src = pages + int64_t(static_cast<uint32_t>(__shfl(static_cast<int>(row), n * Geo::RL + row_l))) * Geo::CH;
+      for (int n = 0; n < Geo::NR; ++n) row[n] = static_cast<uint32_t>(__shfl(static_cast<int>(mine), 8 * n + row_l));
+    }
 #pragma unroll
-        for (int k = 0; k < Geo::ST / Geo::NR; ++k) st[n * (Geo::ST / Geo::NR) + k] = src[k * Geo::PW];
-      }
+    for (int n = 0; n < Geo::NR; ++n) {
+      const u32x4* src = reinterpret_cast<const u32x4*>(a.k_pages) + row[n] * Geo::CH;
+#pragma unroll
+      for (int k = 0; k < Geo::PK; ++k) st[n][k] = src[8 * k + (8 * k + 7 < Geo::CH ? piece_l : min(piece_l, Geo::CH - 1 - 8 * k))];
     }
   };
   int pid = 0;
@@ -145,14 +135,18 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
       uint32_t odd = 0;
 #pragma unroll
       for (int n = 0; n < Geo::NR; ++n) {
-        const int row = n * Geo::RL + row_l;
+        const int row = 8 * n + row_l;
         const uint32_t keep = carried >> row & 1 ? ~0u : 0u;
 #pragma unroll
-        for (int k = 0; k < Geo::ST / Geo::NR; ++k) {
-          uint4 w = st[n * (Geo::ST / Geo::NR) + k];
-          if (carried != 0xffffu) w = make_uint4(w.x & keep, w.y & keep, w.z & keep, w.w & keep);
-          if (t0 + kLatTile > dr.base) odd |= not_finite(w.x) | not_finite(w.y) | not_finite(w.z) | not_finite(w.w);
-          *reinterpret_cast<uint4*>(tile_k + (16 * wv + row) * Geo::LD + (k * Geo::PW + piece_l) * 16) = w;
+        for (int k = 0; k < Geo::PK; ++k) {
+          u32x4 w = st[n][k];
+          if (carried != kAll) w &= rarely(keep);
+          if (t0 + kLatTile > dr.base) {
+            w = rarely(w);
+            odd |= not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
+          }
+          if (8 * k + 7 < Geo::CH || 8 * k + piece_l < Geo::CH)
+            *reinterpret_cast<u32x4*>(tile_k + (Geo::ROWS * wv + row) * Geo::LD + (8 * k + piece_l) * 16) = w;
         }
       }
       odd = __any(odd != 0);
@@ -166,58 +160,58 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
       issue(t0 + kLatTile, pid);
       if (t0 + 2 * kLatTile < end) pid = page_of(t0 + 2 * kLatTile);
     }
-    const bool odd_tile = (tile_odd[0] | tile_odd[1] | tile_odd[2] | tile_odd[3]) != 0;
+    uint32_t odd_tile = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) odd_tile |= tile_odd[w];
     // scores^T [token][row]: lane column = row, tokens 4 g .. + 3 of each block
-    float p[RW][TB][4];
+    float p[TB][4];
 #pragma unroll
     for (int tb = 0; tb < TB; ++tb) {
       const int block = wt * TB + tb;
-      f32x4 s[RW];
-#pragma unroll
-      for (int j = 0; j < RW; ++j) s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 s[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};   // (two sums: each product waits for the one before it)
 #pragma unroll
       for (int x = 0; x < KS; ++x) {
         const Frag kf = load_frag(tile_k + (16 * block + r) * Geo::LD + g * 16 + x * 64);
-#pragma unroll
-        for (int j = 0; j < RW; ++j) s[j] = mfma(kf, qf[j][x], s[j]);
+        s[x & 1] = mfma(kf, qf[x], s[x & 1]);
         if (x % 6 == 5) __builtin_amdgcn_sched_barrier(0);   // (all operands loaded ahead would not fit the registers)
       }
-      const uint32_t live = __builtin_amdgcn_readfirstlane(tile_live[block]);
+      uint32_t live = NW == 8 ? tile_live[2 * block % NW] | tile_live[(2 * block + 1) % NW] << 8 : tile_live[block % NW];
+      live = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(live)));
       const int first = t0 + 16 * block;
 #pragma unroll
-      for (int j = 0; j < RW; ++j) {
+      for (int i = 0; i < 4; ++i) p[tb][i] = (s[0][i] + s[1][i]) * a.scale_log2;
+      if (live != 0xffffu || first + 16 > dr.base) {
+        uint32_t seen = live;
+        if (first + 16 > dr.base) seen &= seen_window(a, dr, token, first - dr.base);
+        seen = rarely(seen);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[j][tb][i] = s[j][i] * a.scale_log2;
-        if (live != 0xffffu || first + 16 > dr.base) {
-          uint32_t seen = live;
-          if (first + 16 > dr.base) seen &= seen_window(a, dr, token[j], first - dr.base);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!(seen >> (4 * g + i) & 1)) p[j][tb][i] = -INFINITY;
-        }
+        for (int i = 0; i < 4; ++i)
+          if (!(seen >> (4 * g + i) & 1)) p[tb][i] = -INFINITY;
       }
     }
-#pragma unroll
-    for (int j = 0; j < RW; ++j) {
+    {
       float top = -INFINITY;
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, p[j][tb][i]);
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, p[tb][i]);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      if (g == 0) part[wt][16 * (wr * RW + j) + r] = top;
+      if (g == 0) part[wt][16 * wr + r] = top;
     }
     __syncthreads();
     if (odd_tile) {                  // (the scores have been taken)
       taken_out = true;
 #pragma unroll 1
-      for (int x = lane; x < 16 * Geo::CH; x += 64) {
-        uint4* at = reinterpret_cast<uint4*>(tile_k + (16 * wv + x / Geo::CH) * Geo::LD + x % Geo::CH * 16);
-        const uint4 w = *at;
-        *at = make_uint4(finite_only(w.x), finite_only(w.y), finite_only(w.z), finite_only(w.w));
+      for (int x = lane; x < Geo::ROWS * Geo::CH; x += 64) {
+        u32x4* at = reinterpret_cast<u32x4*>(tile_k + (Geo::ROWS * wv + x / Geo::CH) * Geo::LD + x % Geo::CH * 16);
+        u32x4 w = *at;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = finite_only(w[i]);
+        *at = w;
       }
     }
+    float base = 0.0f;               // of this wave's rows
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       float top = mx[j];
@@ -226,34 +220,21 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
       if (__any(top > mx[j])) {
         const float shrink = top == -INFINITY ? 1.0f : pow2(mx[j] - top);
         mx[j] = top;
-        if (j / RW == wr) {
-          // (the same for the whole wave; RW == R but for 64 rows)
-#pragma unroll
-          for (int x = 0; x < RW; ++x)
-            if (x == j % RW) sum[x] *= shrink;
-        }
+        if (j == wr) sum *= shrink;
 #pragma unroll
         for (int m = 0; m < CB; ++m) o[j][m] *= shrink;
       }
+      if (j == wr) base = mx[j] == -INFINITY ? 0.0f : mx[j];
     }
 #pragma unroll
-    for (int j = 0; j < RW; ++j) {
-      float m0 = mx[0];
+    for (int tb = 0; tb < TB; ++tb) {
 #pragma unroll
-      for (int x = 1; x < R; ++x)
-        if (x == wr * RW + j) m0 = mx[x];
-      const float base = m0 == -INFINITY ? 0.0f : m0;
+      for (int i = 0; i < 4; ++i) p[tb][i] = pow2(p[tb][i] - base);
+      uint32_t w[PIECES][2];
 #pragma unroll
-      for (int tb = 0; tb < TB; ++tb) {
+      for (int i = 0; i < 2; ++i) pack_pair<PIECES>(p[tb][2 * i], p[tb][2 * i + 1], i, w, sum);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[j][tb][i] = pow2(p[j][tb][i] - base);
-        uint32_t w[PIECES][2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) pack_pair<PIECES>(p[j][tb][2 * i], p[j][tb][2 * i + 1], i, w, sum[j]);
-        const int row = 16 * (wr * RW + j) + r, at = (16 * (wt * TB + tb) + 4 * g) * 2;
-#pragma unroll
-        for (int x = 0; x < PIECES; ++x) *reinterpret_cast<uint2*>(&tile_p[x][row][at]) = make_uint2(w[x][0], w[x][1]);
-      }
+      for (int x = 0; x < PIECES; ++x) *reinterpret_cast<uint2*>(&tile_p[x][16 * wr + r][(16 * (wt * TB + tb) + 4 * g) * 2]) = make_uint2(w[x][0], w[x][1]);
     }
     __syncthreads();
     // readout^T [channel][row] += V^T P^T, this wave's channels
@@ -264,7 +245,7 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
       for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int x = 0; x < PIECES; ++x) pf[j][x] = load_frag(&tile_p[x][16 * j + r][(32 * step + 8 * g) * 2]);
-      const uint8_t* v = tile_k + (32 * step + 8 * g + (r >> 2)) * Geo::LD + (wv * (DC / 4) + 4 * (r & 3)) * 2;
+      const uint8_t* v = tile_k + (32 * step + 8 * g + (r >> 2)) * Geo::LD + (wv * (DC / NW) + 4 * (r & 3)) * 2;
 #pragma unroll
       for (int m = 0; m < CB; ++m) {
         const Frag vf = load_frag_t(reinterpret_cast<const uint16_t*>(v + 32 * m), reinterpret_cast<const uint16_t*>(v + 32 * m + 4 * Geo::LD));
@@ -281,7 +262,7 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
     for (int t = max(dr.base - kLatTile, begin); t < end; ++t) {
       const int page = a.table[int64_t(b) * a.max_blocks + (t >> a.page_log2)];
       if (page < 0 || page >= a.num_pages) continue;
-      const uint8_t* v = a.k_pages + ((int64_t(page) << a.page_log2) + (t & in_page)) * (W * 2) + (wv * (DC / 4) + 4 * g) * 2;
+      const uint8_t* v = a.k_pages + ((int64_t(page) << a.page_log2) + (t & in_page)) * (W * 2) + (wv * (DC / NW) + 4 * g) * 2;
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const unsigned row = static_cast<unsigned>(row0) + min(16 * j + r, live_rows - 1);
@@ -294,12 +275,9 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
 
   // the rows' sums over all tokens
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < RW; ++j) {
-    sum[j] += __shfl_xor(sum[j], 16);
-    sum[j] += __shfl_xor(sum[j], 32);
-    if (g == 0) part[wt][16 * (wr * RW + j) + r] = sum[j];
-  }
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  if (g == 0) part[wt][16 * wr + r] = sum;
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < R; ++j) {
@@ -307,7 +285,7 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
 #pragma unroll
     for (int t = 0; t < TG; ++t) l += part[t][16 * j + r];
     if (16 * j + r >= live_rows) continue;
-    const int ch = wv * (DC / 4) + 4 * g;
+    const int ch = wv * (DC / NW) + 4 * g;
     if (splits == 1) {
       const unsigned row = static_cast<unsigned>(row0) + 16 * j + r;
       const int64_t at = (int64_t(dr.first + row / H) * H + row % H) * DC + ch;
@@ -317,45 +295,35 @@ __global__ __launch_bounds__(256, R * DC > 512 ? 1 : 2) void latent_kernel(const
         *reinterpret_cast<uint2*>(a.out + (at + 16 * m) * 2) =
             make_uint2(pack_bf16(o[j][m][0] * back, o[j][m][1] * back), pack_bf16(o[j][m][2] * back, o[j][m][3] * back));
     } else {
-      const int64_t at = int64_t(id) * plan.heads + 16 * j + r;
+      const int64_t at = int64_t(spot.at) * plan.heads + 16 * j + r;
 #pragma unroll
-      for (int m = 0; m < CB; ++m) *reinterpret_cast<f32x4*>(a.ws + at * DC + ch + 16 * m) = o[j][m];
-      if (wv == 0 && g == 0)
-        reinterpret_cast<float2*>(a.ws + int64_t(plan.items) * plan.tiles * plan.heads * DC)[at] = make_float2(mx[j], l);
+      for (int m = 0; m < CB; ++m) *reinterpret_cast<f32x4*>(parts.o + at * DC + ch + 16 * m) = o[j][m];
+      if (wv == 0 && g == 0) parts.ml[at] = make_float2(mx[j], l);
     }
   }
 }
 
-AttnPlan latent_plan(const TreeSizes& z) {
+TokenPlan latent_plan(const TreeSizes& z) {
   const int64_t rows = int64_t(z.max_new) * z.Hq;
-  AttnPlan p;
-  p.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  p.tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
-  p.heads = static_cast<int>(std::min<int64_t>(rows, p.rows));
-  const int64_t slots = p.rows == 64 ? 256 : 512;      // workgroups that are resident at once
-  // items of full length fill the chip once, the requests' last ones included
-  const int64_t each = std::max<int64_t>(slots / p.tiles, 1), wanted = each > 2 * int64_t(z.B) ? each - z.B : each;
-  const int64_t most = (int64_t(z.max_len) + kLatTile - 1) / kLatTile * z.B;
-  p.per_unit = static_cast<int>(std::min<int64_t>(wanted, std::max<int64_t>(most, 1)));
-  const bool whole = z.max_len <= 256 || int64_t(p.tiles) * z.B >= 4 * slots;
-  p.items = whole ? z.B : p.per_unit + z.B;
-  return p;
+  const int take = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  // workgroups that LDS leaves room for on the 256 CUs: two of four waves each, or one of eight
+  return token_plan(z, take, take == 16 ? 512 : 256, 256);
 }
 
-template <int DC, int R>
-void latent_dr(const TreeArgs& a, const AttnPlan& p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.items) * p.tiles);
-  if (a.page_log2 >= 4) hipLaunchKernelGGL((latent_kernel<DC, R, true, 1>), grid, dim3(256), 0, s, a, p);
-  else hipLaunchKernelGGL((latent_kernel<DC, R, false, 1>), grid, dim3(256), 0, s, a, p);
+template <int DC, int R, int NW>
+void latent_dr(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
+  const dim3 grid(p.groups);
+  if (a.page_log2 >= 4) hipLaunchKernelGGL((latent_kernel<DC, R, NW, true, 1>), grid, dim3(64 * NW), 0, s, a, p);
+  else hipLaunchKernelGGL((latent_kernel<DC, R, NW, false, 1>), grid, dim3(64 * NW), 0, s, a, p);
 }
 
 template <int DC>
 hipError_t latent_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
-  const AttnPlan p = latent_plan(z);
-  if (p.rows == 16) latent_dr<DC, 1>(a, p, s);
-  else if (p.rows == 32) latent_dr<DC, 2>(a, p, s);
-  else latent_dr<DC, 4>(a, p, s);
-  if (p.items > a.B) launch_join<DC, kLatTile>(a, p, s);
+  const TokenPlan p = latent_plan(z);
+  if (p.rows == 16) latent_dr<DC, 1, 4>(a, p, s);
+  else if (p.rows == 32) latent_dr<DC, 2, 8>(a, p, s);
+  else latent_dr<DC, 4, 8>(a, p, s);
+  launch_join<DC>(a, p, s);
   return hipGetLastError();
 }
 
@@ -364,20 +332,13 @@ hipError_t latent_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
 hipError_t launch_latent_append(const LatentAppendArgs& a, hipStream_t s) {
   const int64_t n = int64_t(a.T) * ((a.dc + a.dr) / 8);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 16384));
-  hipLaunchKernelGGL(latent_append_kernel, dim3(grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(latent_append_kernel, dim3(grid), dim3(256), 0, s, a, int64_t(grid) * 256);
   return hipGetLastError();
 }
 
-int64_t latent_grid(const TreeSizes& z, int32_t dc) {
-  const AttnPlan p = latent_plan(z);
-  return std::max((int64_t(p.per_unit) + z.B) * p.tiles, join_groups(p, dc) * z.B * p.tiles);
-}
+int64_t latent_grid(const TreeSizes& z, int32_t dc) { return token_groups(latent_plan(z), z, dc); }
 
-size_t latent_ws_bytes(const TreeSizes& z, int32_t dc) {
-  const AttnPlan p = latent_plan(z);
-  if (p.items == z.B) return 0;
-  return static_cast<size_t>(p.items) * p.tiles * p.heads * (static_cast<size_t>(dc) + 2) * 4;
-}
+size_t latent_ws_bytes(const TreeSizes& z, int32_t dc) { return parts_bytes(latent_plan(z), z, dc); }
 
 hipError_t launch_latent(int dc, const TreeArgs& a, hipStream_t s) {
   const TreeSizes z{a.B, a.Hq, 1, a.max_new, a.max_len};

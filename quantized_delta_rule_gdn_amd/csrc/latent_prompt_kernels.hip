@@ -15,7 +15,6 @@ namespace {
 // stand (lane group g holds keys 4 g .. + 3 of both halves of 32; V^T is read transposed from LDS in the
 // same order). Bound by the products and by the exponentials between them.
 constexpr int kKeyTile = 64;
-using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 
 template <int D, int R>
 __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromptArgs a, int items) {
@@ -80,29 +79,47 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
     }
   }
   f32x4 o[R][MB];
-  float mx[R], sum[R];
+  float mx[R];
+  f32x4 sum[R];                // the same in all four
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     mx[j] = -INFINITY;
-    sum[j] = 0.0f;
+    sum[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int m = 0; m < MB; ++m) o[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   uint32_t odd = 0;            // values that are not finite have been taken out
 
   u32x4 sn[NN], sr[NR], sv[NN];
-  const uint8_t* kb = a.k + (int64_t(k_lo) * a.k_token + int64_t(h) * a.k_head) * 2 + tid % PN * 16;
-  const uint8_t* vb = a.v + (int64_t(k_lo) * a.v_token + int64_t(h) * a.v_head) * 2 + tid % PN * 16;
-  const uint8_t* rb = a.k_rope + int64_t(k_lo) * DR * 2 + tid % PR * 16;
-  const auto issue = [&](int t0) {
+  // (offsets inside a tile fit 32 bits: a token stride is at most 2^24 elements)
+  const uint32_t k_step = static_cast<uint32_t>(a.k_token) * 2, v_step = static_cast<uint32_t>(a.v_token) * 2;
+  uint32_t k_off[NN], v_off[NN], r_off[NR];
+  const auto offsets = [&](int last) {      // rows past the end repeat the last; masked
 #pragma unroll
     for (int i = 0; i < NN; ++i) {
-      const int64_t t = min(t0 + tid / PN + 256 / PN * i, nk - 1);   // (rows past the end repeat the last; masked)
-      sn[i] = *reinterpret_cast<const u32x4*>(kb + t * a.k_token * 2);
-      sv[i] = *reinterpret_cast<const u32x4*>(vb + t * a.v_token * 2);
+      const uint32_t t = min(tid / PN + 256 / PN * i, last);
+      k_off[i] = t * k_step + tid % PN * 16;
+      v_off[i] = t * v_step + tid % PN * 16;
     }
 #pragma unroll
-    for (int i = 0; i < NR; ++i) sr[i] = *reinterpret_cast<const u32x4*>(rb + int64_t(min(t0 + tid / PR + 256 / PR * i, nk - 1)) * (DR * 2));
+    for (int i = 0; i < NR; ++i) r_off[i] = min(tid / PR + 256 / PR * i, last) * (DR * 2) + tid % PR * 16;
+  };
+  offsets(kKeyTile);
+  const auto issue = [&](int t0) {
+    if (t0 + kKeyTile > nk) {
+      offsets(rarely(nk - 1 - t0));
+    }
+    const int64_t t = int64_t(k_lo) + t0;
+    const uint8_t* kb = a.k + (t * a.k_token + h * a.k_head) * 2;
+    const uint8_t* vb = a.v + (t * a.v_token + h * a.v_head) * 2;
+    const uint8_t* rb = a.k_rope + t * (DR * 2);
+#pragma unroll
+    for (int i = 0; i < NN; ++i) {
+      sn[i] = *reinterpret_cast<const u32x4*>(kb + k_off[i]);
+      sv[i] = *reinterpret_cast<const u32x4*>(vb + v_off[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) sr[i] = *reinterpret_cast<const u32x4*>(rb + r_off[i]);
   };
   if (tid == 0) any_odd = 0;
   if (stop > 0) issue(0);
@@ -116,6 +133,7 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
       *reinterpret_cast<u32x4*>(tile_k + t * LK + tid % PN * 16) = sn[i];
       u32x4 w = sv[i];
       if (masked) {
+        w = rarely(w);
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           odd |= not_finite(w[x]);
@@ -145,7 +163,7 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
     if (t0 + kKeyTile > min(before + wave0 + 1, nk)) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        const int last = min(before + wave0 + 16 * j + r, nk - 1) - t0 - 4 * g;   // the last key that this query sees
+        const int last = rarely(min(before + wave0 + 16 * j + r, nk - 1) - t0 - 4 * g);   // the last key that this query sees
 #pragma unroll
         for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
@@ -176,7 +194,8 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
         float p[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = pow2(fmaf(s[j][2 * st + (i >> 2)][i & 3], a.scale_log2, base));
-        pack_weights<1>(p, &pf[j][st], sum[j]);
+        pf[j][st] = round_weights(p);
+        sum[j] = mfma(ones(), pf[j][st], sum[j]);
       }
     }
 #pragma unroll
@@ -205,11 +224,9 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
   }
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    sum[j] += __shfl_xor(sum[j], 16);
-    sum[j] += __shfl_xor(sum[j], 32);
     const int row = wave0 + 16 * j + r;
     if (row >= nq) continue;
-    const float back = sum[j] == 0.0f ? 0.0f : 1.0f / sum[j];
+    const float back = sum[j][0] == 0.0f ? 0.0f : 1.0f / sum[j][0];
     uint8_t* to = a.out + ((int64_t(q_lo) + row) * a.H + h) * (D * 2) + g * 8;
 #pragma unroll
     for (int m = 0; m < MB; ++m)

@@ -280,6 +280,7 @@ struct FreeArgs {
 };
 
 hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s);
+int64_t kv_copy_items(const CopyArgs& a);   // runs that are copied: below 2^31
 hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s);
 hipError_t launch_kv_compact(const CompactArgs& a, hipStream_t s);
 size_t kv_free_ws_bytes(int32_t num_pages);

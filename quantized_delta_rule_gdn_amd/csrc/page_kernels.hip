@@ -65,85 +65,116 @@ __global__ __launch_bounds__(kForkThreads) void kv_fork_kernel(const ForkArgs a)
 
 // ---- copies of pages ---------------------------------------------------------------------------
 // A workgroup takes one run of up to kCopyRun bytes of one (copy, head, keys or values), 16 bytes a
-// thread and load, four of them on their way at once. Bound by the stream.
-constexpr int kCopyRun = 16384;
+// thread and load, eight of them on their way at once. Bound by the stream.
+constexpr int kCopyRun = 65536, kCopyUnroll = 8;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 
-__global__ __launch_bounds__(256) void kv_copy_kernel(const CopyArgs a, int runs, int arrays) {
+__global__ __launch_bounds__(256) void kv_copy_kernel(const CopyArgs a, unsigned runs, unsigned arrays, unsigned groups) {
   const int tid = __builtin_amdgcn_workitem_id_x();
-  const int64_t items = int64_t(a.n) * a.Hkv * arrays * runs;
-  for (int64_t x = __builtin_amdgcn_workgroup_id_x(); x < items; x += __builtin_amdgcn_grid_size_x() / 256) {
-    const int run = static_cast<int>(x % runs);
-    const int64_t y = x / runs;
-    const int which = static_cast<int>(y % arrays), h = static_cast<int>(y / arrays % a.Hkv), i = static_cast<int>(y / arrays / a.Hkv);
+  const unsigned items = a.n * static_cast<unsigned>(a.Hkv) * arrays * runs;
+  for (unsigned x = __builtin_amdgcn_workgroup_id_x(); x < items; x += groups) {
+    const unsigned run = x % runs, y = x / runs, which = y % arrays, z = y / arrays, h = z % a.Hkv, i = z / a.Hkv;
     const int src = a.src[i], dst = a.dst[i];
     if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages || src == dst) continue;
     const int page = 1 << a.page_log2, rows = a.rows ? min(max(a.rows[i], 0), page) : page;
-    const int64_t pieces = int64_t(rows) * (a.d / 8);
-    const int64_t first = int64_t(run) * (kCopyRun / 16), stop = min(first + kCopyRun / 16, pieces);
-    uint4* base = reinterpret_cast<uint4*>(which ? a.v_pages : a.k_pages);
-    const int64_t whole = int64_t(page) * (a.d / 8);
-    const uint4* from = base + (int64_t(src) * a.Hkv + h) * whole;
-    uint4* to = base + (int64_t(dst) * a.Hkv + h) * whole;
-    int64_t p = first + tid;
-    for (; p + 768 < stop; p += 1024) {
-      uint4 w[4];
+    const int per_row = a.d / 8, first = run * (kCopyRun / 16), stop = min(first + kCopyRun / 16, rows * per_row);
+    u32x4* base = reinterpret_cast<u32x4*>(which ? a.v_pages : a.k_pages);
+    const int64_t whole = int64_t(page) * per_row;
+    const u32x4* from = base + (int64_t(src) * a.Hkv + h) * whole;
+    u32x4* to = base + (int64_t(dst) * a.Hkv + h) * whole;
+    for (int p = first + tid; p < stop; p += 256 * kCopyUnroll) {
+      u32x4 w[kCopyUnroll];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = from[p + 256 * k];
+      for (int k = 0; k < kCopyUnroll; ++k) w[k] = __builtin_nontemporal_load(from + min(p + 256 * k, stop - 1));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) to[p + 256 * k] = w[k];
+      for (int k = 0; k < kCopyUnroll; ++k)
+        if (p + 256 * k < stop) __builtin_nontemporal_store(w[k], to + p + 256 * k);
     }
-    for (; p < stop; p += 256) to[p] = from[p];
   }
 }
 
 // ---- kept tokens moved together ------------------------------------------------------------------
 // One workgroup per (request, head, keys or values) takes the kept tokens in order, as many at a time
 // as its threads hold in registers. A token never moves up (its place in the list is at most its
-// number), so a batch's stores cannot reach a later batch's tokens; within a batch every load has
-// returned before the first store. Bound by the stream for long lists, by latency for short ones.
-constexpr int kKeepUnroll = 4;
+// number), so a batch's stores cannot reach a later batch's tokens: the next batch is loaded before
+// this one is stored, its pages looked up a batch ahead, and the list read one more ahead. Within a
+// batch every load has returned before the first store. Bound by the stream for long lists, by latency
+// for short ones.
+constexpr int kKeepUnroll = 8;
 
 __global__ __launch_bounds__(256) void kv_compact_kernel(const CompactArgs a, int arrays) {
+  constexpr int U = kKeepUnroll;
   const int tid = __builtin_amdgcn_workitem_id_x();
-  const int64_t x = __builtin_amdgcn_workgroup_id_x();
+  const unsigned x = __builtin_amdgcn_workgroup_id_x();
   const int which = static_cast<int>(x % arrays), h = static_cast<int>(x / arrays % a.Hkv), b = static_cast<int>(x / arrays / a.Hkv);
   const int lo = min(max(a.cu[b], 0), a.K), hi = min(max(a.cu[b + 1], lo), a.K);
   const int len = max(a.seq_lens[b], 0), fresh = min(max(a.new_lens[b], 0), len), base = len - fresh;
   const int n = min(hi - lo, fresh);
   if (which == 0 && h == 0 && tid == 0) a.out_lens[b] = base + n;
-  const int per_row = a.d / 8, page = 1 << a.page_log2;             // (at most 256 pieces a row)
+  if (n == 0 || a.max_blocks == 0) return;
+  const int per_row = a.d / 8, in_page = (1 << a.page_log2) - 1;             // (at most 256 pieces a row)
   const int rows = 256 / per_row, row = tid / per_row, piece = tid % per_row;   // rows a pass
-  uint4* pages = reinterpret_cast<uint4*>(which ? a.v_pages : a.k_pages);
-  const auto at = [&](int pos) -> int64_t {   // of a position's row, in pieces; -1 where there is none
-    const int j = pos >> a.page_log2;
-    if (j >= a.max_blocks) return -1;
-    const int id = a.table[int64_t(b) * a.max_blocks + j];
-    if (id < 0 || id >= a.num_pages) return -1;
-    return ((((int64_t(id) * a.Hkv + h) << a.page_log2) + (pos & (page - 1))) * per_row);
+  u32x4* pages = reinterpret_cast<u32x4*>(which ? a.v_pages : a.k_pages);
+  const int* table = a.table + int64_t(b) * a.max_blocks;
+  struct Batch {                // a batch on its way: places in the list, then their pages, then their values
+    int idx[U], po[U], pt[U];
   };
-  for (int j0 = 0; j0 < n; j0 += rows * kKeepUnroll) {
-    int64_t from[kKeepUnroll], to[kKeepUnroll];
+  // (every load is unconditional and waits are for older ones than a batch's values: the loads come back in
+  // order, and the values are the last of an iteration)
+  const auto list = [&](int j0, Batch& m) {
 #pragma unroll
-    for (int u = 0; u < kKeepUnroll; ++u) {
-      const int j = j0 + u * rows + row;
-      from[u] = to[u] = -1;
-      if (row < rows && j < n) {
-        const int idx = a.kept[lo + j];
-        if (idx > j && idx < fresh) {
-          from[u] = at(base + idx);
-          to[u] = from[u] < 0 ? -1 : at(base + j);
-        }
-      }
+    for (int u = 0; u < U; ++u) m.idx[u] = a.kept[lo + min(j0 + u * rows + row, n - 1)];
+  };
+  const auto look_up = [&](int j0, Batch& m) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = min(j0 + u * rows + row, n - 1);
+      m.po[u] = table[min((base + min(max(m.idx[u], 0), fresh - 1)) >> a.page_log2, a.max_blocks - 1)];
+      m.pt[u] = table[min((base + j) >> a.page_log2, a.max_blocks - 1)];
     }
-    uint4 w[kKeepUnroll] = {};
+  };
+  const auto moves = [&](int j0, const Batch& m, int u) -> bool {
+    const int j = j0 + u * rows + row;
+    return row < rows && j < n && m.idx[u] > j && m.idx[u] < fresh && (base + m.idx[u]) >> a.page_log2 < a.max_blocks && m.po[u] >= 0 &&
+           m.po[u] < a.num_pages && m.pt[u] >= 0 && m.pt[u] < a.num_pages;
+  };
+  const auto load = [&](int j0, const Batch& m, u32x4 (&w)[U]) {
 #pragma unroll
-    for (int u = 0; u < kKeepUnroll; ++u)
-      if (to[u] >= 0) w[u] = pages[from[u] + piece];
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    for (int u = 0; u < U; ++u) {
+      const uint32_t from = moves(j0, m, u) ? ((static_cast<uint32_t>(m.po[u]) * a.Hkv + h) << a.page_log2) + ((base + m.idx[u]) & in_page) : 0;
+      w[u] = pages[int64_t(from) * per_row + piece];
+    }
+  };
+  const int batch = rows * U;
+  Batch now, next, after;
+  u32x4 w[U];
+  list(0, now);
+  list(batch, next);
+  list(2 * batch, after);
+  look_up(0, now);
+  look_up(batch, next);
+  load(0, now, w);
+  for (int j0 = 0; j0 < n; j0 += batch) {
+    u32x4 ahead[U];
+    Batch last;
+    look_up(j0 + 2 * batch, after);
+    list(j0 + 3 * batch, last);
+    load(j0 + batch, next, ahead);
+#pragma unroll
+    for (int u = 0; u < U; ++u) asm volatile("" ::"v"(w[u]) : "memory");   // (has returned)
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < kKeepUnroll; ++u)
-      if (to[u] >= 0) pages[to[u] + piece] = w[u];
+    for (int u = 0; u < U; ++u) {
+      if (moves(j0, now, u)) {
+        const uint32_t to = ((static_cast<uint32_t>(now.pt[u]) * a.Hkv + h) << a.page_log2) + ((base + j0 + u * rows + row) & in_page);
+        pages[int64_t(to) * per_row + piece] = w[u];
+      }
+      w[u] = ahead[u];
+    }
+    now = next;
+    next = after;
+#pragma unroll
+    for (int u = 0; u < U; ++u) after.idx[u] = last.idx[u];
   }
 }
 
@@ -197,7 +228,7 @@ __global__ __launch_bounds__(kListThreads) void kv_count_kernel(const FreeArgs a
 }
 
 // per_group: runs of kListPages that each workgroup lists (all of them where there is one workgroup).
-__global__ __launch_bounds__(kListThreads) void kv_list_kernel(const FreeArgs a, int per_group) {
+__global__ __launch_bounds__(kListThreads) void kv_list_kernel(const FreeArgs a, int per_group, int groups) {
   __shared__ int wave_sum[kListThreads / 64];
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63, wv = tid >> 6;
   const int g = __builtin_amdgcn_workgroup_id_x();
@@ -238,7 +269,7 @@ __global__ __launch_bounds__(kListThreads) void kv_list_kernel(const FreeArgs a,
         a.shares[p + k] = 0;
       }
   }
-  if (g == static_cast<int>(__builtin_amdgcn_grid_size_x() / kListThreads) - 1 && tid == 0) a.num_freed[0] = before;
+  if (g == groups - 1 && tid == 0) a.num_freed[0] = before;
 }
 
 // Up to this many pages one workgroup lists alone, without the launch that counts.
@@ -253,11 +284,16 @@ hipError_t launch_kv_fork(const ForkArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s) {
+int64_t kv_copy_items(const CopyArgs& a) {
   const int64_t bytes = (int64_t(a.d) * 2) << a.page_log2;
-  const int runs = static_cast<int>((bytes + kCopyRun - 1) / kCopyRun), arrays = a.v_pages ? 2 : 1;
-  const int64_t items = int64_t(a.n) * a.Hkv * arrays * runs;
-  hipLaunchKernelGGL(kv_copy_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 65536))), dim3(256), 0, s, a, runs, arrays);
+  return int64_t(a.n) * a.Hkv * (a.v_pages ? 2 : 1) * ((bytes + kCopyRun - 1) / kCopyRun);
+}
+
+hipError_t launch_kv_copy(const CopyArgs& a, hipStream_t s) {
+  const int64_t items = kv_copy_items(a);
+  const unsigned arrays = a.v_pages ? 2 : 1, runs = static_cast<unsigned>(items / (int64_t(a.n) * a.Hkv * arrays));
+  const unsigned groups = static_cast<unsigned>(std::min<int64_t>(items, 65536));
+  hipLaunchKernelGGL(kv_copy_kernel, dim3(groups), dim3(256), 0, s, a, runs, arrays, groups);
   return hipGetLastError();
 }
 
@@ -277,7 +313,7 @@ hipError_t launch_kv_free(const FreeArgs& a, hipStream_t s) {
   if (a.B > 0) hipLaunchKernelGGL(kv_drop_kernel, dim3(a.B), dim3(256), 0, s, a);
   if (groups > 1) hipLaunchKernelGGL(kv_count_kernel, dim3(groups), dim3(kListThreads), 0, s, a);
   const int per_group = groups > 1 ? 1 : static_cast<int>((a.num_pages + kListPages - 1) / kListPages);
-  hipLaunchKernelGGL(kv_list_kernel, dim3(groups), dim3(kListThreads), 0, s, a, per_group);
+  hipLaunchKernelGGL(kv_list_kernel, dim3(groups), dim3(kListThreads), 0, s, a, per_group, static_cast<int>(groups));
   return hipGetLastError();
 }
 

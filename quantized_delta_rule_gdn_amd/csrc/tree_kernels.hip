@@ -15,14 +15,13 @@ namespace {
 // at the end. The rows of a product are the (drafted token, query head) pairs of one key-value head,
 // 16 R a workgroup: a tile's keys and values serve R operand groups once they are in registers.
 template <int D, int R, bool P16, int PIECES>
-__global__ __launch_bounds__(256, R == 4 ? 1 : 2) void kv_tree_kernel(const TreeArgs a, const AttnPlan plan) {
+__global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(const TreeArgs a, const TokenPlan plan) {
   constexpr int KS = D / 32;       // k steps of the score product
   constexpr int DPL = D / 16;      // value channels per lane
   constexpr int VW = DPL / 2;      // dwords of them
   constexpr uint32_t kNone = 0xffffffffu;
   constexpr int kAttnPages = 1024;                    // page addresses held in LDS at a time
   __shared__ uint32_t first_row[kAttnPages];          // of a page, in rows of this key-value head
-  __shared__ int64_t sh[8];
   __shared__ int any_odd;                             // values that are not finite have been taken out
   __shared__ float part_m[4][16], part_l[4][16];
   __shared__ __align__(16) float part_o[4][16][D + 4];
@@ -30,18 +29,14 @@ __global__ __launch_bounds__(256, R == 4 ? 1 : 2) void kv_tree_kernel(const Tree
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const unsigned id = __builtin_amdgcn_workgroup_id_x();
-  const int units = a.Hkv * plan.tiles;
-  const int item = id / units, unit = id % units, tile = unit % plan.tiles, kvh = unit / plan.tiles;
-  const int G = a.Hq / a.Hkv;
-
-  // the request this item belongs to, and its drafted tokens
-  const Item it = item_of(a, plan, item, sh);
-  const int b = it.b, split = it.split, splits = it.splits;
+  const Spot spot = spot_of<4 * kAttnTile, D>(a, plan);
+  const int b = spot.b, kvh = spot.kvh, split = spot.split, splits = spot.splits;
   if (b < 0) return;
+  const int G = a.Hq / a.Hkv;
   const Drafts dr = drafts_of(a, b);
-  const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(tile) * (16 * R);
+  const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(spot.tile) * (16 * R);
   if (row0 >= rows) return;
+  const Parts<D> parts(a, plan);
   const int len = length_of(a, b);
   // its tokens: an even share of the request's, in whole tiles
   const int share = ((len + splits - 1) / splits + kAttnTile - 1) / kAttnTile * kAttnTile;
@@ -278,61 +273,285 @@ __global__ __launch_bounds__(256, R == 4 ? 1 : 2) void kv_tree_kernel(const Tree
         const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * D + c;
         reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc / l);
       } else {
-        const int64_t at = int64_t(id) * plan.heads + 16 * j + h;
-        a.ws[at * D + c] = acc;
-        if (c == 0) reinterpret_cast<float2*>(a.ws + int64_t(plan.items) * units * plan.heads * D)[at] = make_float2(m0, l);
+        const int64_t at = int64_t(spot.at) * plan.heads + 16 * j + h;
+        parts.o[at * D + c] = acc;
+        if (c == 0) parts.ml[at] = make_float2(m0, l);
       }
     }
   }
 }
 
-// Rows a workgroup: as many as there are, up to 64.
-int tree_groups(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Many rows: the 16 R rows of each wave are its own, and a tile of 64 tokens goes through LDS for all
+// four, the next one on its way in registers (read by every wave for itself, 64 rows would draw 64 KB a
+// tile from the L1, as long as their products take).
+constexpr int kWideTile = 64;
 
-AttnPlan tree_plan(const TreeSizes& z) {
+template <int D, int R, bool P16>
+__global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel(const TreeArgs a, const TokenPlan plan) {
+  constexpr int KS = D / 32, MB = D / 16, TB = kWideTile / 16;
+  constexpr int LD = D * 2 + 32;                        // bytes between rows in LDS: an odd number of 32-byte units
+  constexpr int PW = D / 8, RL = 64 / PW, NL = 16 / RL; // 16-byte pieces of a row, rows of a load, loads for a wave's 16 rows
+  __shared__ __align__(16) uint8_t tile_k[kWideTile * LD];
+  __shared__ __align__(16) uint8_t tile_v[kWideTile * LD];
+  __shared__ uint32_t tile_live[4];
+  __shared__ int any_odd;                               // values that are not finite have been taken out
+
+  const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const Spot spot = spot_of<kWideTile, D>(a, plan);
+  const int b = spot.b, kvh = spot.kvh, split = spot.split, splits = spot.splits;
+  if (b < 0) return;
+  const int G = a.Hq / a.Hkv;
+  const Drafts dr = drafts_of(a, b);
+  const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(spot.tile) * (64 * R);
+  if (row0 >= rows) return;
+  const Parts<D> parts(a, plan);
+  const int len = length_of(a, b);
+  const int share = ((len + splits - 1) / splits + kWideTile - 1) / kWideTile * kWideTile;
+  const int begin = min(split * share, len), end = min(begin + share, len);
+  const int in_page = (1 << a.page_log2) - 1;
+  const int live_rows = static_cast<int>(min(rows - row0, int64_t(64 * R)));
+  const bool idle = wv * 16 * R >= live_rows;           // none of the rows is this wave's
+  // (a negative scale goes into the queries' signs; one of 0 becomes the least one, as 0 times -infinity is NaN)
+  const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
+  const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0;
+
+  int token[R];
+  Frag qf[R][KS];
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const unsigned row = static_cast<unsigned>(row0) + min(16 * (wv * R + j) + r, live_rows - 1);
+    token[j] = row / G;
+    const int64_t at = int64_t(dr.first + token[j]) * a.Hq + kvh * G + row % G;
+#pragma unroll
+    for (int x = 0; x < KS; ++x) {
+      qf[j][x] = load_frag(a.q + (at * D + g * 8 + x * 32) * 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[j][x].w[i] ^= flip;
+    }
+  }
+  f32x4 o[R][MB];
+  float mx[R];
+  f32x4 sum[R];                      // the same in all four
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    mx[j] = -INFINITY;
+    sum[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int m = 0; m < MB; ++m) o[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  uint32_t odd = 0;
+
+  // Each wave carries 16 rows of a tile's keys and values. Their pages are looked up one tile ahead.
+  u32x4 sk[NL], sv[NL];
+  uint32_t carried = 0;              // which of the rows exist
+  const int row_l = lane / PW, piece_l = lane % PW;
+  const auto page_of = [&](int t0) -> int {
+    const int pos = min(t0 + 16 * wv + (P16 ? 0 : r), end - 1);
+    return a.table[int64_t(b) * a.max_blocks + (pos >> a.page_log2)];
+  };
+  const auto issue = [&](int t0, int pid) {
+    const int left = min(max(end - (t0 + 16 * wv), 0), 16);
+    if constexpr (P16) {
+      const int id0 = __builtin_amdgcn_readfirstlane(pid);
+      const bool fine = id0 >= 0 && id0 < a.num_pages && left > 0;
+      carried = fine ? (1u << left) - 1 : 0;
+      // (rows past the end lie in the same page; where there is no page, the first one's rows stand in)
+      const int64_t first = (fine ? ((int64_t(id0) * a.Hkv + kvh) << a.page_log2) + ((t0 + 16 * wv) & in_page) : 0) * (D * 2);
+      const uint8_t *kb = a.k_pages + first, *vb = a.v_pages + first;
+      const uint32_t off = row_l * (D * 2) + piece_l * 16;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        sk[n] = *reinterpret_cast<const u32x4*>(kb + off + n * RL * (D * 2));
+        sv[n] = *reinterpret_cast<const u32x4*>(vb + off + n * RL * (D * 2));
+      }
+    } else {
+      const bool fine = pid >= 0 && pid < a.num_pages && r < left;
+      carried = static_cast<uint32_t>(__ballot(fine)) & 0xffffu;
+      const uint32_t mine = fine ? ((static_cast<uint32_t>(pid) * a.Hkv + kvh) << a.page_log2) + ((t0 + 16 * wv + r) & in_page) : 0;
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        const int64_t at = (int64_t(static_cast<uint32_t>(__shfl(static_cast<int>(mine), n * RL + row_l))) * PW + piece_l) * 16;
+        sk[n] = *reinterpret_cast<const u32x4*>(a.k_pages + at);
+        sv[n] = *reinterpret_cast<const u32x4*>(a.v_pages + at);
+      }
+    }
+  };
+  int pid = 0;
+  if (tid == 0) any_odd = 0;
+  if (begin < end) {
+    pid = page_of(begin);
+    issue(begin, pid);
+    if (begin + kWideTile < end) pid = page_of(begin + kWideTile);
+  } else {
+    __syncthreads();
+  }
+  for (int t0 = begin; t0 < end; t0 += kWideTile) {
+    __syncthreads();                 // the tile before is no longer read
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+      const int row = n * RL + row_l, at = (16 * wv + row) * LD + piece_l * 16;
+      const uint32_t keep = carried >> row & 1 ? ~0u : 0u;
+      u32x4 w = sv[n];
+      if (carried != 0xffffu) w &= rarely(keep);
+      if (t0 + kWideTile > dr.base) {
+        w = rarely(w);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          odd |= not_finite(w[x]);
+          w[x] = finite_only(w[x]);
+        }
+      }
+      *reinterpret_cast<u32x4*>(tile_k + at) = sk[n];
+      *reinterpret_cast<u32x4*>(tile_v + at) = w;
+    }
+    if (lane == 0) tile_live[wv] = carried;
+    __syncthreads();
+    if (t0 + kWideTile < end) {
+      issue(t0 + kWideTile, pid);
+      if (t0 + 2 * kWideTile < end) pid = page_of(t0 + 2 * kWideTile);
+    }
+    if (idle) continue;
+
+    f32x4 s[R][TB];
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) s[j][tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        const Frag kf = load_frag(tile_k + (16 * tb + r) * LD + g * 16 + x * 64);
+#pragma unroll
+        for (int j = 0; j < R; ++j) s[j][tb] = mfma(kf, qf[j][x], s[j][tb]);
+      }
+    }
+    uint32_t live[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) live[h] = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(tile_live[2 * h] | tile_live[2 * h + 1] << 16));
+    if ((live[0] & live[1]) != ~0u || t0 + kWideTile > dr.base) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+          const int rel = t0 + 32 * h - dr.base;
+          const uint32_t seen = rarely((rel > -32 ? live[h] & seen_window(a, dr, token[j], rel) : live[h]) >> (4 * g));
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(seen >> (16 * (i >> 2) + (i & 3)) & 1)) s[j][2 * h + (i >> 2)][i & 3] = -INFINITY;
+        }
+    }
+    Frag pf[R][TB / 2];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      float top = mx[j];
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][tb][i]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__any(top > mx[j])) {               // (the maximum settles after a few tiles)
+        const float shrink = top == -INFINITY ? 1.0f : pow2((mx[j] - top) * scale);
+        mx[j] = top;
+        sum[j] *= shrink;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) o[j][m] *= shrink;
+      }
+      const float base = mx[j] == -INFINITY ? 0.0f : -mx[j] * scale;
+#pragma unroll
+      for (int st = 0; st < TB / 2; ++st) {
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = pow2(fmaf(s[j][2 * st + (i >> 2)][i & 3], scale, base));
+        pf[j][st] = round_weights(p);
+        sum[j] = mfma(ones(), pf[j][st], sum[j]);
+      }
+    }
+#pragma unroll
+    for (int st = 0; st < TB / 2; ++st) {
+      const uint8_t* v = tile_v + (32 * st + 4 * g + (r >> 2)) * LD + 8 * (r & 3);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const Frag vf = load_frag_t(reinterpret_cast<const uint16_t*>(v + 32 * m), reinterpret_cast<const uint16_t*>(v + 32 * m + 16 * LD));
+#pragma unroll
+        for (int j = 0; j < R; ++j) o[j][m] = mfma(vf, pf[j][st], o[j][m]);
+      }
+    }
+  }
+
+  if (__any(odd != 0)) any_odd = 1;
+  __syncthreads();
+  if (any_odd) {
+    // (from the first tile with a drafted token on; what an earlier tile has already is added again, to no effect)
+#pragma unroll 1
+    for (int t = max(dr.base - kWideTile, begin); t < end; ++t) {
+      const int page = a.table[int64_t(b) * a.max_blocks + (t >> a.page_log2)];
+      if (page < 0 || page >= a.num_pages) continue;
+      const uint8_t* v = a.v_pages + (((int64_t(page) * a.Hkv + kvh) << a.page_log2) + (t & in_page)) * (D * 2) + g * 8;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const bool seen = t < dr.base || (seen_window(a, dr, token[j], t - dr.base) & 1);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) o[j][m] = add_odd(o[j][m], *reinterpret_cast<const uint2*>(v + 32 * m), seen);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const int in_tile = 16 * (wv * R + j) + r;
+    if (in_tile >= live_rows) continue;
+    if (splits == 1) {
+      const unsigned row = static_cast<unsigned>(row0) + in_tile;
+      const float back = sum[j][0] == 0.0f ? 0.0f : 1.0f / sum[j][0];
+      uint8_t* to = a.out + ((int64_t(dr.first + token[j]) * a.Hq + kvh * G + row % G) * D + 4 * g) * 2;
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+        *reinterpret_cast<uint2*>(to + 32 * m) = make_uint2(pack_bf16(o[j][m][0] * back, o[j][m][1] * back), pack_bf16(o[j][m][2] * back, o[j][m][3] * back));
+    } else {
+      const int64_t at = int64_t(spot.at) * plan.heads + in_tile;
+#pragma unroll
+      for (int m = 0; m < MB; ++m) *reinterpret_cast<f32x4*>(parts.o + at * D + 16 * m + 4 * g) = o[j][m];
+      if (g == 0) parts.ml[at] = make_float2(mx[j] * scale, sum[j][0]);
+    }
+  }
+}
+
+// How a call's rows are taken. Up to 32 rows a key-value head: by every wave for itself (the R = 1 and 2 of
+// kv_tree_kernel); more: through LDS, 64 or 128 rows a workgroup.
+TokenPlan tree_plan(const TreeSizes& z, int d) {
   const int64_t rows = int64_t(z.max_new) * (z.Hq / z.Hkv);
-  AttnPlan p;
-  p.rows = 16 * tree_groups(rows);
-  p.tiles = static_cast<int>((rows + p.rows - 1) / p.rows);
-  p.heads = static_cast<int>(std::min<int64_t>(rows, p.rows));
-  const int64_t units = int64_t(z.Hkv) * p.tiles, wanted = p.rows == 64 ? 512 : 1024;
-  const int64_t most = (int64_t(z.max_len) + kAttnLeast - 1) / kAttnLeast * z.B;   // no more are ever cut
-  p.per_unit = static_cast<int>(std::min<int64_t>(std::max<int64_t>(wanted / units, 1), std::max<int64_t>(most, 1)));
-  const bool whole = z.max_len <= 1024 || (z.max_len <= 2048 && units * z.B >= 512);
-  p.items = whole ? z.B : p.per_unit + z.B;
-  return p;
+  const int take = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  // workgroups that registers leave room for on the 256 CUs: 3 each, 2 with 32 or 128 rows of d = 128
+  return token_plan(z, take, d == 128 && (take == 32 || take == 128) ? 512 : 768, take <= 32 ? 1024 : 384);
+}
+
+template <int D, int R, bool P16>
+void tree_drp(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
+  if (p.rows <= 32) hipLaunchKernelGGL((kv_tree_kernel<D, R, P16, 2>), dim3(p.groups), dim3(256), 0, s, a, p);
+  else hipLaunchKernelGGL((kv_tree_wide_kernel<D, R, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
 }
 
 template <int D, int R>
-void tree_dr(const TreeArgs& a, const AttnPlan& p, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.items) * a.Hkv * p.tiles);
-  if (a.page_log2 >= 4) hipLaunchKernelGGL((kv_tree_kernel<D, R, true, 2>), grid, dim3(256), 0, s, a, p);
-  else hipLaunchKernelGGL((kv_tree_kernel<D, R, false, 2>), grid, dim3(256), 0, s, a, p);
+void tree_dr(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
+  if (a.page_log2 >= 4) tree_drp<D, R, true>(a, p, s);
+  else tree_drp<D, R, false>(a, p, s);
 }
 
 template <int D>
 hipError_t tree_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
-  const AttnPlan p = tree_plan(z);
-  if (p.rows == 16) tree_dr<D, 1>(a, p, s);
-  else if (p.rows == 32) tree_dr<D, 2>(a, p, s);
-  else tree_dr<D, 4>(a, p, s);
-  if (p.items > a.B) launch_join<D, kAttnLeast>(a, p, s);
+  const TokenPlan p = tree_plan(z, D);
+  if (p.rows == 16 || p.rows == 64) tree_dr<D, 1>(a, p, s);
+  else tree_dr<D, 2>(a, p, s);
+  launch_join<D>(a, p, s);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t kv_tree_grid(const TreeSizes& z, int32_t d) {
-  const AttnPlan p = tree_plan(z);
-  const int64_t units = int64_t(z.Hkv) * p.tiles;
-  return std::max((int64_t(p.per_unit) + z.B) * units, z.B * units * join_groups(p, d));
-}
+int64_t kv_tree_grid(const TreeSizes& z, int32_t d) { return token_groups(tree_plan(z, d), z, d); }
 
-size_t kv_tree_ws_bytes(const TreeSizes& z, int32_t d) {
-  const AttnPlan p = tree_plan(z);
-  if (p.items == z.B) return 0;
-  return static_cast<size_t>(p.items) * z.Hkv * p.tiles * p.heads * (static_cast<size_t>(d) + 2) * 4;
-}
+size_t kv_tree_ws_bytes(const TreeSizes& z, int32_t d) { return parts_bytes(tree_plan(z, d), z, d); }
 
 hipError_t launch_kv_tree(int d, const TreeArgs& a, hipStream_t s) {
   const TreeSizes z{a.B, a.Hq, a.Hkv, a.max_new, a.max_len};
