@@ -17,7 +17,7 @@ namespace {
 // holds at once, as often over as 1.5 workgroups for each (request, head, tile) need, so that a launch
 // is whole rounds of much the same length.
 struct TokenPlan {
-  int rows;       // query rows of a tile
+  int rows_log2;  // query rows of a tile
   int heads;      // rows of the largest tile there is
   int tiles;      // row tiles of a request with the most new tokens
   int slots;      // workgroups that the chip holds at once
@@ -30,16 +30,41 @@ struct Spot {
   int b, kvh, tile;
   int split, splits;     // its part of the request's tokens
   int at;                // its place in the workspace
+  Drafts dr;
+  int len;               // tokens of the request
 };
 
-struct Share {           // of a request: row tiles, tokens
-  int tiles, len;
+struct Share {           // of a request
+  Drafts dr;
+  int len, tiles;        // tokens, row tiles
 };
 
 __device__ __forceinline__ Share share_of(const TreeArgs& a, const TokenPlan& plan, int b) {
-  const int64_t rows = int64_t(min(drafts_of(a, b).n, a.max_new)) * (a.Hq / a.Hkv);
-  return Share{static_cast<int>((rows + plan.rows - 1) / plan.rows), length_of(a, b)};
+  Share s;
+  s.dr = drafts_of(a, b);
+  s.len = length_of(a, b);
+  s.tiles = (min(s.dr.n, a.max_new) * (a.Hq / a.Hkv) + (1 << plan.rows_log2) - 1) >> plan.rows_log2;      // (rows stay below 2^30)
+  return s;
 }
+
+// Running sums over the 64 lanes, by moves inside the vector unit (a sixth of the time that moves through LDS
+// take; this is on the way of every workgroup's first load).
+template <typename T>
+__device__ __forceinline__ T scan64(T x) {
+  static_assert(sizeof(T) == 4);
+#define DAMP_SCAN_STEP(ctrl, rows) x += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, rows, 0xf, false))
+  DAMP_SCAN_STEP(0x111, 0xf);   // from 1, 2, 4, 8 lanes below, within 16 lanes
+  DAMP_SCAN_STEP(0x112, 0xf);
+  DAMP_SCAN_STEP(0x114, 0xf);
+  DAMP_SCAN_STEP(0x118, 0xf);
+  DAMP_SCAN_STEP(0x142, 0xa);   // the sum of the 16 lanes below to the odd 16s, of the lower 32 to the upper
+  DAMP_SCAN_STEP(0x143, 0xc);
+#undef DAMP_SCAN_STEP
+  return x;
+}
+
+template <typename T>
+__device__ __forceinline__ T last_lane(T x) { return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63)); }
 
 // What the workgroups leave in the workspace: a tile's partial readouts, {maximum, sum} of its rows, and
 // each request's {first place, runs}.
@@ -70,49 +95,45 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
     const int per = plan.tiles * a.Hkv;
     const int at = per == 1 ? static_cast<int>(id) : static_cast<int>(id % 8 * (plan.groups / 8) + id / 8);   // (rounded up to 8)
     const int b = at / per, unit = at % per;
-    return Spot{b < a.B ? b : -1, unit / plan.tiles, unit % plan.tiles, 0, 1, 0};
+    if (b >= a.B) return Spot{-1};
+    return Spot{b, unit / plan.tiles, unit % plan.tiles, 0, 1, 0, drafts_of(a, b), length_of(a, b)};
   }
   const int lane = __builtin_amdgcn_workitem_id_x() & 63;
-  const Share own = lane < a.B ? share_of(a, plan, lane) : Share{0, 0};
+  const Share own = lane < a.B ? share_of(a, plan, lane) : Share{};
   const auto over_requests = [&](auto&& f) {
-    int64_t x = f(own);
+    auto x = f(own);
     for (int b = lane + 64; b < a.B; b += 64) x += f(share_of(a, plan, b));
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x * a.Hkv;
+    return last_lane(scan64(x));
   };
-  const int64_t least = over_requests([](const Share& s) { return int64_t(s.tiles); });
-  const int64_t work = over_requests([](const Share& s) { return int64_t(s.tiles) * s.len; });
-  const int64_t budget = max((3 * least / 2 + plan.slots - 1) / plan.slots, int64_t(1)) * plan.slots;   // at most plan.groups
-  int64_t chunk = max((work + budget - 1) / budget, int64_t(1)), n;
+  const int least = over_requests([](const Share& s) { return s.tiles; }) * a.Hkv;
+  const int budget = max((3 * least / 2 + plan.slots - 1) / plan.slots, 1) * plan.slots;   // at most plan.groups
+  // (a first guess in binary32, the same in every wave; the count that it is held to is exact)
+  const float work = over_requests([](const Share& s) { return static_cast<float>(s.tiles) * static_cast<float>(s.len); }) * a.Hkv;
+  constexpr float kMost = 0x1p30f;
+  float guess = work / budget;
+  int chunk, n;
   for (int round = 0;; ++round) {
-    chunk = min((chunk + GRAIN - 1) / GRAIN * GRAIN, int64_t(1) << 30);
-    n = over_requests([&](const Share& s) { return int64_t(s.tiles) * items_of(s.len, static_cast<int>(chunk)); });
-    if (n <= budget || chunk == int64_t(1) << 30) break;
+    chunk = (static_cast<int>(fminf(guess, kMost - GRAIN)) / GRAIN + 1) * GRAIN;
+    n = over_requests([&](const Share& s) { return s.tiles * items_of(s.len, chunk); }) * a.Hkv;
+    if (n <= budget || guess >= kMost) break;
     // as much longer as there are too many (twice, where that has not done for a while)
-    chunk = max(round < 6 ? chunk * n / budget : 2 * chunk, chunk + GRAIN);
+    guess = fmaxf(round < 6 ? chunk * (static_cast<float>(n) / budget) : 2.0f * chunk, chunk + GRAIN * 0.5f);
   }
-  const int per_die = static_cast<int>((n + 7) / 8), at = static_cast<int>(id % 8) * per_die + static_cast<int>(id / 8);
-  if (static_cast<int>(id / 8) >= per_die || at >= n) return Spot{-1, 0, 0, 0, 1, 0};
+  const int per_die = (n + 7) / 8, at = static_cast<int>(id % 8) * per_die + static_cast<int>(id / 8);
+  if (static_cast<int>(id / 8) >= per_die || at >= n) return Spot{-1};
   for (int b0 = 0, before = 0; b0 < a.B; b0 += 64) {
-    const Share s = b0 == 0 ? own : b0 + lane < a.B ? share_of(a, plan, b0 + lane) : Share{0, 0};
-    const int runs = items_of(s.len, static_cast<int>(chunk)), mine = s.tiles * runs * a.Hkv;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(incl, o);
-      if (lane >= o) incl += y;
-    }
-    const int first = before + incl - mine;
+    const Share s = b0 == 0 ? own : b0 + lane < a.B ? share_of(a, plan, b0 + lane) : Share{};
+    const int runs = items_of(s.len, chunk), mine = s.tiles * runs * a.Hkv, incl = scan64(mine), first = before + incl - mine;
     if (const uint64_t here = __ballot(at >= first && at < first + mine); here != 0) {
-      const int l = __builtin_ctzll(here), tiles = __builtin_amdgcn_readlane(s.tiles, l), first_l = __builtin_amdgcn_readlane(first, l);
-      const int local = at - first_l, splits = __builtin_amdgcn_readlane(runs, l), unit = local / tiles;
+      const int l = __builtin_ctzll(here);
+      const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+      const int tiles = of(s.tiles), first_l = of(first), local = at - first_l, splits = of(runs), unit = local / tiles;
       if (local == 0 && __builtin_amdgcn_workitem_id_x() == 0) Parts<D>(a, plan).info[b0 + l] = make_int2(first_l, splits);
-      return Spot{b0 + l, unit % a.Hkv, local % tiles, unit / a.Hkv, splits, at};
+      return Spot{b0 + l, unit % a.Hkv, local % tiles, unit / a.Hkv, splits, at, Drafts{of(s.dr.first), of(s.dr.n), of(s.dr.base)}, of(s.len)};
     }
-    before += __builtin_amdgcn_readlane(incl, 63);
+    before += last_lane(incl);
   }
-  return Spot{-1, 0, 0, 0, 1, 0};
+  return Spot{-1};
 }
 
 // The runs of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels a
@@ -128,11 +149,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
   const Parts<D> parts(a, plan);
   const int2 info = parts.info[b];                 // (not written where a request has no rows: not used either)
   const Drafts dr = drafts_of(a, b);
-  const int rows = min(dr.n, a.max_new) * G, tile0 = tile * plan.rows;
+  const int rows = min(dr.n, a.max_new) * G, tile0 = tile << plan.rows_log2;
   if (tile0 + group * RPG >= rows || info.y == 1) return;   // (one run: it has its readout already)
   const int in_tile = group * RPG + tid / LPR, row = tile0 + in_tile;
   if (in_tile >= plan.heads || row >= rows) return;
-  const int tiles = (rows + plan.rows - 1) / plan.rows;
+  const int tiles = (rows + (1 << plan.rows_log2) - 1) >> plan.rows_log2;
   const int64_t step = int64_t(a.Hkv) * tiles * plan.heads;      // between a tile's runs
   const int64_t first = (int64_t(info.x) + kvh * tiles + tile) * plan.heads + in_tile;
   const float4* po = reinterpret_cast<const float4*>(parts.o + first * D) + tid % LPR;
@@ -176,10 +197,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
 
 // Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where they alone
 // fill the chip four times over.
-inline TokenPlan token_plan(const TreeSizes& z, int rows, int slots, int whole) {
-  const int64_t all = int64_t(z.max_new) * (z.Hq / z.Hkv);
+inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int whole) {
+  const int64_t all = int64_t(z.max_new) * (z.Hq / z.Hkv), rows = int64_t(1) << rows_log2;
   TokenPlan p;
-  p.rows = rows;
+  p.rows_log2 = rows_log2;
   p.tiles = static_cast<int>((all + rows - 1) / rows);
   p.heads = static_cast<int>(std::min<int64_t>(all, rows));
   p.slots = slots;

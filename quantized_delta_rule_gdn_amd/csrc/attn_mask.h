@@ -39,6 +39,21 @@ __device__ __forceinline__ uint32_t seen_window(const TreeArgs& a, const Drafts&
   return rel >= 0 ? bits : (bits << -rel) | ((1u << -rel) - 1);
 }
 
+// Maximum over the lanes l, l ^ 16, l ^ 32 and l ^ 48 (as sum_row_slots adds).
+__device__ __forceinline__ float max_row_slots(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const uint32_t u2 = __float_as_uint(x);
+  const auto b = __builtin_amdgcn_permlane32_swap(u2, u2, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// A row's running maximum stays as it is until a score passes it by more than this factor 2^kSlack: weights of
+// up to 2^8 lose nothing in binary32 or bf16, and most tiles then need neither the other lanes' maxima nor
+// sums scaled down.
+constexpr float kSlack = 8.0f;
+
 // x, in a branch that few tiles take: what goes by it is not worked out before the branch (for all tiles, to be
 // selected from).
 template <typename T>

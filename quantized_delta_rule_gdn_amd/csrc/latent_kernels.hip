@@ -60,11 +60,11 @@ __global__ __launch_bounds__(64 * NW, 2) void latent_kernel(const TreeArgs a, co
   const Spot spot = spot_of<kLatTile, DC>(a, plan);
   const int b = spot.b, split = spot.split, splits = spot.splits, H = a.Hq;
   if (b < 0) return;
-  const Drafts dr = drafts_of(a, b);
+  const Drafts dr = spot.dr;
   const int64_t rows = int64_t(min(dr.n, a.max_new)) * H, row0 = int64_t(spot.tile) * (16 * R);
   if (row0 >= rows) return;
   const Parts<DC> parts(a, plan);
-  const int len = length_of(a, b);
+  const int len = spot.len;
   const int share = ((len + splits - 1) / splits + kLatTile - 1) / kLatTile * kLatTile;
   const int begin = min(split * share, len), end = min(begin + share, len);
   const int in_page = (1 << a.page_log2) - 1;
@@ -195,8 +195,7 @@ __global__ __launch_bounds__(64 * NW, 2) void latent_kernel(const TreeArgs a, co
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, p[tb][i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
+      top = max_row_slots(top);
       if (g == 0) part[wt][16 * wr + r] = top;
     }
     __syncthreads();
@@ -303,26 +302,320 @@ __global__ __launch_bounds__(64 * NW, 2) void latent_kernel(const TreeArgs a, co
   }
 }
 
-TokenPlan latent_plan(const TreeSizes& z) {
-  const int64_t rows = int64_t(z.max_new) * z.Hq;
-  const int take = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  // workgroups that LDS leaves room for on the 256 CUs: two of four waves each, or one of eight
-  return token_plan(z, take, take == 16 ? 512 : 256, 256);
+// More than 16 rows: the products take longer than the stream, so the two are given to different waves and
+// run at the same time. Four waves score a tile, 16 rows each and all 64 tokens (so a row's maximum is its
+// wave's own), while the other four weigh the tile before it, a quarter of the channels each and all rows:
+// every SIMD holds one of either kind, and two barriers a tile are left. Two tiles lie in LDS, the third
+// is on its way in the registers of all eight.
+template <int DC, int R, bool P16>
+__global__ __launch_bounds__(512, 2) void latent_wide_kernel(const TreeArgs a, const TokenPlan plan) {
+  using Geo = LatGeo<DC, 8>;
+  constexpr int W = Geo::W, KS = W / 32, CB = DC / 64, TB = kLatTile / 16;
+  constexpr int LD = W * 2 + 16, LDP = kLatTile * 2 + 16;
+  __shared__ __align__(16) uint8_t tile_k[2][kLatTile * LD];
+  __shared__ __align__(16) uint8_t tile_p[16 * R][LDP];
+  __shared__ float row_m[16 * R], row_l[16 * R];     // by what the sums shrink; in the end maximum and sum
+  __shared__ uint32_t tile_live[2][8], tile_odd[2][8];
+
+  const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const Spot spot = spot_of<kLatTile, DC>(a, plan);
+  const int b = spot.b, split = spot.split, splits = spot.splits, H = a.Hq;
+  if (b < 0) return;
+  const Drafts dr = spot.dr;
+  const int64_t rows = int64_t(min(dr.n, a.max_new)) * H, row0 = int64_t(spot.tile) * (16 * R);
+  if (row0 >= rows) return;
+  const int len = spot.len;
+  const int share = ((len + splits - 1) / splits + kLatTile - 1) / kLatTile * kLatTile;
+  const int begin = min(split * share, len), end = min(begin + share, len);
+  const int in_page = (1 << a.page_log2) - 1;
+  const int live_rows = static_cast<int>(min(rows - row0, int64_t(16 * R)));
+
+  // Each wave carries 8 rows of a tile. Their pages are looked up one tile ahead of their loads.
+  u32x4 st[Geo::PK];
+  uint32_t carried = 0;              // which of the rows in st exist
+  const int row_l8 = lane / 8, piece_l = lane % 8;
+  const auto page_of = [&](int t0) -> int {
+    const int pos = min(t0 + 8 * wv + (P16 ? 0 : row_l8), end - 1);
+    return a.table[int64_t(b) * a.max_blocks + (pos >> a.page_log2)];
+  };
+  const auto issue = [&](int t0, int pid) {
+    const int first = t0 + 8 * wv, left = min(max(end - first, 0), 8);
+    int64_t row;
+    if constexpr (P16) {
+      const int id0 = __builtin_amdgcn_readfirstlane(pid);
+      const bool fine = id0 >= 0 && id0 < a.num_pages && left > 0;
+      carried = fine ? (1u << left) - 1 : 0;
+      // (rows past the end lie in the same page; where there is no page, the first one's rows stand in)
+      row = (fine ? (int64_t(id0) << a.page_log2) + (first & in_page) : 0) + row_l8;
+    } else {
+      const bool fine = pid >= 0 && pid < a.num_pages && row_l8 < left;
+      const uint64_t all = __ballot(fine);           // (8 lanes a row)
+      carried = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) carried |= static_cast<uint32_t>(all >> (8 * i) & 1) << i;
+      row = fine ? (int64_t(pid) << a.page_log2) + ((first + row_l8) & in_page) : 0;
+    }
+    const u32x4* src = reinterpret_cast<const u32x4*>(a.k_pages) + row * Geo::CH;
+#pragma unroll
+    for (int k = 0; k < Geo::PK; ++k) st[k] = src[8 * k + (8 * k + 7 < Geo::CH ? piece_l : min(piece_l, Geo::CH - 1 - 8 * k))];
+  };
+  const auto store = [&](int t0, int buf) {
+    uint32_t odd = 0;
+    const uint32_t keep = carried >> row_l8 & 1 ? ~0u : 0u;
+#pragma unroll
+    for (int k = 0; k < Geo::PK; ++k) {
+      u32x4 w = st[k];
+      if (carried != 0xffu) w &= rarely(keep);
+      if (t0 + kLatTile > dr.base) {
+        w = rarely(w);
+        odd |= not_finite(w[0]) | not_finite(w[1]) | not_finite(w[2]) | not_finite(w[3]);
+      }
+      if (8 * k + 7 < Geo::CH || 8 * k + piece_l < Geo::CH)
+        *reinterpret_cast<u32x4*>(tile_k[buf] + (8 * wv + row_l8) * LD + (8 * k + piece_l) * 16) = w;
+    }
+    odd = __any(odd != 0);
+    if (lane == 0) {
+      tile_live[buf][wv] = carried;
+      tile_odd[buf][wv] = odd;
+    }
+  };
+  int pid = 0;
+  // The tile after t0 into LDS, and values of t0's that are not finite out of it (its scores have been taken).
+  // True where there were any.
+  const auto advance = [&](int t0, int buf) -> bool {
+    if (t0 + kLatTile < end) store(t0 + kLatTile, buf ^ 1);
+    if (t0 + kLatTile <= dr.base) return false;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) odd |= tile_odd[buf][w];
+    if (odd == 0) return false;
+#pragma unroll 1
+    for (int x = lane; x < 8 * Geo::CH; x += 64) {
+      u32x4* at = reinterpret_cast<u32x4*>(tile_k[buf] + (8 * wv + x / Geo::CH) * LD + x % Geo::CH * 16);
+      u32x4 w = *at;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = finite_only(w[i]);
+      *at = w;
+    }
+    return true;
+  };
+  // The loads of the tile two after t0 (past the end they repeat rows that exist), with a page looked up before.
+  const auto fetch = [&](int t0) {
+    issue(t0 + 2 * kLatTile, pid);
+    pid = page_of(t0 + 3 * kLatTile);
+  };
+  if (begin < end) {
+    issue(begin, page_of(begin));
+    pid = page_of(begin + kLatTile);
+  }
+
+  if (wv < 4) {
+    const bool mine = 16 * wv < live_rows;           // (with R == 2, and in the last row tile, some waves only carry rows)
+    const unsigned my_row = static_cast<unsigned>(row0) + min(16 * wv + r, live_rows - 1);
+    const int token = my_row / H;
+    Frag qf[KS];
+    const int64_t at = int64_t(dr.first + token) * H + my_row % H;
+#pragma unroll
+    for (int x = 0; x < KS; ++x) qf[x] = load_frag(a.q + (at * W + g * 8 + x * 32) * 2);
+    if (begin < end) store(begin, 0);
+    __syncthreads();
+    float mx = -INFINITY, shrink = 1.0f, sum = 0.0f;
+    uint32_t w[TB][1][2];                            // the weights: tokens 16 tb + 4 g .. + 3
+    const auto score = [&](int t0, int buf) {
+      f32x4 s[TB];
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb) s[tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int x = 0; x < KS; ++x)
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) s[tb] = mfma(load_frag(tile_k[buf] + (16 * tb + r) * LD + g * 16 + x * 64), qf[x], s[tb]);
+      // operands two steps ahead, and a load of the next tile every other step
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * TB, 0);
+#pragma unroll
+      for (int x = 0; x < KS; ++x) {
+        __builtin_amdgcn_sched_group_barrier(0x008, TB, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, TB, 0);
+        if (x % 2 == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+      float p[TB][4];
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[tb][i] = s[tb][i] * a.scale_log2;
+      uint32_t live = 0xffu;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) live &= tile_live[buf][x];
+      if (live != 0xffu || t0 + kLatTile > dr.base) {
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) {
+          uint32_t seen = tile_live[buf][2 * tb] | tile_live[buf][2 * tb + 1] << 8;
+          const int rel = t0 + 16 * tb - dr.base;
+          if (rel > -16) seen &= seen_window(a, dr, token, rel);
+          seen = rarely(seen >> (4 * g));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(seen >> i & 1)) p[tb][i] = -INFINITY;
+        }
+      }
+      float top = mx;
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, p[tb][i]);
+      top = max_row_slots(top);
+      shrink = top == -INFINITY ? 1.0f : pow2(mx - top);
+      mx = top;
+      sum *= shrink;
+      const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) pack_pair<1>(pow2(p[tb][2 * i] - base), pow2(p[tb][2 * i + 1] - base), i, w[tb], sum);
+    };
+    if (begin < end) {
+      fetch(begin - kLatTile);
+      if (mine) score(begin, 0);
+    }
+    if (!mine && wv < R && g == 0) row_m[16 * wv + r] = 1.0f;
+    __syncthreads();
+    int buf = 0;
+    for (int t0 = begin; t0 < end; t0 += kLatTile, buf ^= 1) {
+      if (mine) {
+#pragma unroll
+        for (int tb = 0; tb < TB; ++tb) *reinterpret_cast<uint2*>(&tile_p[16 * wv + r][(16 * tb + 4 * g) * 2]) = make_uint2(w[tb][0][0], w[tb][0][1]);
+        if (g == 0) row_m[16 * wv + r] = shrink;
+      }
+      advance(t0, buf);
+      __syncthreads();
+      fetch(t0);
+      if (mine && t0 + kLatTile < end) score(t0 + kLatTile, buf ^ 1);
+      __syncthreads();
+    }
+    if (wv < R) {
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (g == 0) {
+        row_m[16 * wv + r] = mx;
+        row_l[16 * wv + r] = sum;
+      }
+    }
+    __syncthreads();
+    return;
+  }
+
+  const int first_ch = (wv - 4) * (DC / 4);
+  f32x4 o[R][CB];
+  bool taken_out = false;            // values that are not finite
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int m = 0; m < CB; ++m) o[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (begin < end) store(begin, 0);
+  __syncthreads();
+  if (begin < end) fetch(begin - kLatTile);
+  __syncthreads();                   // the first tile's scores
+  int buf = 0;
+  for (int t0 = begin; t0 < end; t0 += kLatTile, buf ^= 1) {
+    taken_out |= advance(t0, buf);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const float shrink = row_m[16 * j + r];
+      if (__any(shrink != 1.0f)) {     // (the maximum settles after a few tiles)
+#pragma unroll
+        for (int m = 0; m < CB; ++m) o[j][m] *= shrink;
+      }
+    }
+    fetch(t0);
+#pragma unroll
+    for (int step = 0; step < kLatTile / 32; ++step) {
+      Frag pf[R];
+#pragma unroll
+      for (int j = 0; j < R; ++j) pf[j] = load_frag(&tile_p[16 * j + r][(32 * step + 8 * g) * 2]);
+      const uint8_t* v = tile_k[buf] + (32 * step + 8 * g + (r >> 2)) * LD + (first_ch + 4 * (r & 3)) * 2;
+#pragma unroll
+      for (int m = 0; m < CB; ++m) {
+        const Frag vf = load_frag_t(reinterpret_cast<const uint16_t*>(v + 32 * m), reinterpret_cast<const uint16_t*>(v + 32 * m + 4 * LD));
+#pragma unroll
+        for (int j = 0; j < R; ++j) o[j][m] = mfma(vf, pf[j], o[j][m]);
+      }
+    }
+    // operands three blocks ahead, and a load of the next tile every other block
+    __builtin_amdgcn_sched_group_barrier(0x100, R + 6, 0);
+#pragma unroll
+    for (int step = 0; step < kLatTile / 32; ++step) {
+#pragma unroll
+      for (int m = 0; m < CB; ++m) {
+        __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        if (m % 2 == 1) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+    __syncthreads();
+  }
+  __syncthreads();                   // maxima and sums
+  if (taken_out) {
+    // (from the first tile with a drafted token on; what an earlier tile has already is added again, to no effect)
+#pragma unroll 1
+    for (int t = max(dr.base - kLatTile, begin); t < end; ++t) {
+      const int page = a.table[int64_t(b) * a.max_blocks + (t >> a.page_log2)];
+      if (page < 0 || page >= a.num_pages) continue;
+      const uint8_t* v = a.k_pages + ((int64_t(page) << a.page_log2) + (t & in_page)) * (W * 2) + (first_ch + 4 * g) * 2;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const unsigned row = static_cast<unsigned>(row0) + min(16 * j + r, live_rows - 1);
+        const bool seen = t < dr.base || (seen_window(a, dr, row / H, t - dr.base) & 1);
+#pragma unroll
+        for (int m = 0; m < CB; ++m) o[j][m] = add_odd(o[j][m], *reinterpret_cast<const uint2*>(v + 32 * m), seen);
+      }
+    }
+  }
+  const Parts<DC> parts(a, plan);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    if (16 * j + r >= live_rows) continue;
+    const float l = row_l[16 * j + r];
+    const int ch = first_ch + 4 * g;
+    if (splits == 1) {
+      const unsigned row = static_cast<unsigned>(row0) + 16 * j + r;
+      const int64_t at = (int64_t(dr.first + row / H) * H + row % H) * DC + ch;
+      const float back = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int m = 0; m < CB; ++m)
+        *reinterpret_cast<uint2*>(a.out + (at + 16 * m) * 2) =
+            make_uint2(pack_bf16(o[j][m][0] * back, o[j][m][1] * back), pack_bf16(o[j][m][2] * back, o[j][m][3] * back));
+    } else {
+      const int64_t at = int64_t(spot.at) * plan.heads + 16 * j + r;
+#pragma unroll
+      for (int m = 0; m < CB; ++m) *reinterpret_cast<f32x4*>(parts.o + at * DC + ch + 16 * m) = o[j][m];
+      if (wv == 4 && g == 0) parts.ml[at] = make_float2(row_m[16 * j + r], l);
+    }
+  }
 }
 
-template <int DC, int R, int NW>
-void latent_dr(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
+TokenPlan latent_plan(const TreeSizes& z) {
+  const int64_t rows = int64_t(z.max_new) * z.Hq;
+  const int log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : 6;
+  // workgroups that LDS leaves room for on the 256 CUs: two of four waves each, or one of eight
+  return token_plan(z, log2, log2 == 4 ? 512 : 256, 256);
+}
+
+template <int DC, bool P16>
+void latent_dp(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
   const dim3 grid(p.groups);
-  if (a.page_log2 >= 4) hipLaunchKernelGGL((latent_kernel<DC, R, NW, true, 1>), grid, dim3(64 * NW), 0, s, a, p);
-  else hipLaunchKernelGGL((latent_kernel<DC, R, NW, false, 1>), grid, dim3(64 * NW), 0, s, a, p);
+  if (p.rows_log2 == 4) hipLaunchKernelGGL((latent_kernel<DC, 1, 4, P16, 1>), grid, dim3(256), 0, s, a, p);
+  else if (p.rows_log2 == 5) hipLaunchKernelGGL((latent_wide_kernel<DC, 2, P16>), grid, dim3(512), 0, s, a, p);
+  else hipLaunchKernelGGL((latent_wide_kernel<DC, 4, P16>), grid, dim3(512), 0, s, a, p);
 }
 
 template <int DC>
 hipError_t latent_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
   const TokenPlan p = latent_plan(z);
-  if (p.rows == 16) latent_dr<DC, 1, 4>(a, p, s);
-  else if (p.rows == 32) latent_dr<DC, 2, 8>(a, p, s);
-  else latent_dr<DC, 4, 8>(a, p, s);
+  if (a.page_log2 >= 4) latent_dp<DC, true>(a, p, s);
+  else latent_dp<DC, false>(a, p, s);
   launch_join<DC>(a, p, s);
   return hipGetLastError();
 }

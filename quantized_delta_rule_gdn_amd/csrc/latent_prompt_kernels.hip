@@ -88,6 +88,7 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
 #pragma unroll
     for (int m = 0; m < MB; ++m) o[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  const float slack = fminf(kSlack / a.scale_log2, 0x1p100f);
   uint32_t odd = 0;            // values that are not finite have been taken out
 
   u32x4 sn[NN], sr[NR], sv[NN];
@@ -160,6 +161,13 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
         for (int j = 0; j < R; ++j) s[j][tb] = mfma(kf, qf[j][x], s[j][tb]);
       }
     }
+    // (operands four steps ahead: a read from LDS takes as long as some ten products)
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int x = 0; x < TB * KS; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
     if (t0 + kKeyTile > min(before + wave0 + 1, nk)) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
@@ -174,14 +182,13 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
     Frag pf[R][TB / 2];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      float top = mx[j];
+      float top = -INFINITY;
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][tb][i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > mx[j])) {               // (the maximum settles after a few tiles)
+      if (__any(top > mx[j] + slack)) {
+        top = fmaxf(max_row_slots(top), mx[j]);
         const float shrink = top == -INFINITY ? 1.0f : pow2((mx[j] - top) * a.scale_log2);
         mx[j] = top;
         sum[j] *= shrink;
@@ -207,6 +214,12 @@ __global__ __launch_bounds__(256, 2) void latent_prompt_kernel(const LatentPromp
 #pragma unroll
         for (int j = 0; j < R; ++j) o[j][m] = mfma(vf, pf[j][st], o[j][m]);
       }
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+    for (int x = 0; x < MB * TB / 2; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
   }
 

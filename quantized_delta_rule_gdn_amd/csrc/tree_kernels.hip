@@ -33,11 +33,11 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
   const int b = spot.b, kvh = spot.kvh, split = spot.split, splits = spot.splits;
   if (b < 0) return;
   const int G = a.Hq / a.Hkv;
-  const Drafts dr = drafts_of(a, b);
+  const Drafts dr = spot.dr;
   const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(spot.tile) * (16 * R);
   if (row0 >= rows) return;
   const Parts<D> parts(a, plan);
-  const int len = length_of(a, b);
+  const int len = spot.len;
   // its tokens: an even share of the request's, in whole tiles
   const int share = ((len + splits - 1) / splits + kAttnTile - 1) / kAttnTile * kAttnTile;
   const int begin = min(split * share, len), end = min(begin + share, len);
@@ -177,12 +177,11 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
       Frag pf[R][PIECES];
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        float top = mx[j];
+        float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, p[j][i]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (__any(top > mx[j])) {               // (the maximum settles after a few tiles)
+        if (__any(top > mx[j] + kSlack)) {
+          top = fmaxf(max_row_slots(top), mx[j]);
           const float shrink = top == -INFINITY ? 1.0f : pow2(mx[j] - top);
           mx[j] = top;
           sum[j] *= shrink;
@@ -303,11 +302,11 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
   const int b = spot.b, kvh = spot.kvh, split = spot.split, splits = spot.splits;
   if (b < 0) return;
   const int G = a.Hq / a.Hkv;
-  const Drafts dr = drafts_of(a, b);
+  const Drafts dr = spot.dr;
   const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(spot.tile) * (64 * R);
   if (row0 >= rows) return;
   const Parts<D> parts(a, plan);
-  const int len = length_of(a, b);
+  const int len = spot.len;
   const int share = ((len + splits - 1) / splits + kWideTile - 1) / kWideTile * kWideTile;
   const int begin = min(split * share, len), end = min(begin + share, len);
   const int in_page = (1 << a.page_log2) - 1;
@@ -316,6 +315,7 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
   // (a negative scale goes into the queries' signs; one of 0 becomes the least one, as 0 times -infinity is NaN)
   const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0;
+  const float slack = fminf(kSlack / scale, 0x1p100f);
 
   int token[R];
   Frag qf[R][KS];
@@ -426,6 +426,13 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
         for (int j = 0; j < R; ++j) s[j][tb] = mfma(kf, qf[j][x], s[j][tb]);
       }
     }
+    // (operands four steps ahead: a read from LDS takes as long as some ten products)
+    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+    for (int x = 0; x < TB * KS; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
     uint32_t live[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) live[h] = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(tile_live[2 * h] | tile_live[2 * h + 1] << 16));
@@ -444,14 +451,13 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
     Frag pf[R][TB / 2];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      float top = mx[j];
+      float top = -INFINITY;
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][tb][i]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (__any(top > mx[j])) {               // (the maximum settles after a few tiles)
+      if (__any(top > mx[j] + slack)) {
+        top = fmaxf(max_row_slots(top), mx[j]);
         const float shrink = top == -INFINITY ? 1.0f : pow2((mx[j] - top) * scale);
         mx[j] = top;
         sum[j] *= shrink;
@@ -477,6 +483,12 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
 #pragma unroll
         for (int j = 0; j < R; ++j) o[j][m] = mfma(vf, pf[j][st], o[j][m]);
       }
+    }
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+    for (int x = 0; x < MB * TB / 2; ++x) {
+      __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
   }
 
@@ -521,14 +533,14 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
 // kv_tree_kernel); more: through LDS, 64 or 128 rows a workgroup.
 TokenPlan tree_plan(const TreeSizes& z, int d) {
   const int64_t rows = int64_t(z.max_new) * (z.Hq / z.Hkv);
-  const int take = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : rows <= 64 ? 6 : 7;
   // workgroups that registers leave room for on the 256 CUs: 3 each, 2 with 32 or 128 rows of d = 128
-  return token_plan(z, take, d == 128 && (take == 32 || take == 128) ? 512 : 768, take <= 32 ? 1024 : 384);
+  return token_plan(z, log2, d == 128 && log2 % 2 == 1 ? 512 : 768, log2 <= 5 ? 1024 : 384);
 }
 
 template <int D, int R, bool P16>
 void tree_drp(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
-  if (p.rows <= 32) hipLaunchKernelGGL((kv_tree_kernel<D, R, P16, 2>), dim3(p.groups), dim3(256), 0, s, a, p);
+  if (p.rows_log2 <= 5) hipLaunchKernelGGL((kv_tree_kernel<D, R, P16, 2>), dim3(p.groups), dim3(256), 0, s, a, p);
   else hipLaunchKernelGGL((kv_tree_wide_kernel<D, R, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
 }
 
@@ -541,7 +553,7 @@ void tree_dr(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
 template <int D>
 hipError_t tree_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
   const TokenPlan p = tree_plan(z, D);
-  if (p.rows == 16 || p.rows == 64) tree_dr<D, 1>(a, p, s);
+  if (p.rows_log2 % 2 == 0) tree_dr<D, 1>(a, p, s);
   else tree_dr<D, 2>(a, p, s);
   launch_join<D>(a, p, s);
   return hipGetLastError();
