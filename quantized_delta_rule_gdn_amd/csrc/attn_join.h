@@ -47,25 +47,6 @@ __device__ __forceinline__ Share share_of(const TreeArgs& a, const TokenPlan& pl
   return s;
 }
 
-// Running sums over the 64 lanes, by moves inside the vector unit (a sixth of the time that moves through LDS
-// take; this is on the way of every workgroup's first load).
-template <typename T>
-__device__ __forceinline__ T scan64(T x) {
-  static_assert(sizeof(T) == 4);
-#define DAMP_SCAN_STEP(ctrl, rows) x += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, rows, 0xf, false))
-  DAMP_SCAN_STEP(0x111, 0xf);   // from 1, 2, 4, 8 lanes below, within 16 lanes
-  DAMP_SCAN_STEP(0x112, 0xf);
-  DAMP_SCAN_STEP(0x114, 0xf);
-  DAMP_SCAN_STEP(0x118, 0xf);
-  DAMP_SCAN_STEP(0x142, 0xa);   // the sum of the 16 lanes below to the odd 16s, of the lower 32 to the upper
-  DAMP_SCAN_STEP(0x143, 0xc);
-#undef DAMP_SCAN_STEP
-  return x;
-}
-
-template <typename T>
-__device__ __forceinline__ T last_lane(T x) { return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63)); }
-
 // What the workgroups leave in the workspace: a tile's partial readouts, {maximum, sum} of its rows, and
 // each request's {first place, runs}.
 template <int D>

@@ -39,6 +39,43 @@ __device__ __forceinline__ uint32_t seen_window(const TreeArgs& a, const Drafts&
   return rel >= 0 ? bits : (bits << -rel) | ((1u << -rel) - 1);
 }
 
+// Running sums over the 64 lanes, by moves inside the vector unit (a sixth of the time that moves through LDS
+// take; this is on the way of every workgroup's first load).
+template <typename T>
+__device__ __forceinline__ T scan64(T x) {
+  static_assert(sizeof(T) == 4);
+#define DAMP_SCAN_STEP(ctrl, rows) x += __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, rows, 0xf, false))
+  DAMP_SCAN_STEP(0x111, 0xf);   // from 1, 2, 4, 8 lanes below, within 16 lanes
+  DAMP_SCAN_STEP(0x112, 0xf);
+  DAMP_SCAN_STEP(0x114, 0xf);
+  DAMP_SCAN_STEP(0x118, 0xf);
+  DAMP_SCAN_STEP(0x142, 0xa);   // the sum of the 16 lanes below to the odd 16s, of the lower 32 to the upper
+  DAMP_SCAN_STEP(0x143, 0xc);
+#undef DAMP_SCAN_STEP
+  return x;
+}
+
+template <typename T>
+__device__ __forceinline__ T last_lane(T x) { return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 63)); }
+
+// Each lane's 16 bytes at src into LDS at dst + 16 lane (dst the same for the wave), without a way through
+// registers. The data is there after landed() and a barrier.
+__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Rows loaded that way lie close together in LDS. So that operands are read without bank conflicts, piece p (16
+// bytes) of row t lies at p ^ row_turn(t) where rows are read whole (one access of 16 lanes takes piece c of
+// rows 0-3 and 12-15 and piece c + 1 of rows 4-11, or the other way round), at p ^ column_turn(t) where they
+// are read transposed (32 lanes: the halves of two pieces of 8 rows). PIECES: of a row, 4, 8 or 16.
+template <int PIECES>
+__device__ __forceinline__ int row_turn(int t) { return PIECES == 4 ? -(t >> 2) & 3 : PIECES == 8 ? t >> 1 & 7 : t & 15; }
+
+template <int PIECES>
+__device__ __forceinline__ int column_turn(int t) { return PIECES == 8 ? t & 6 : (t & 3) * 2 + (t & 4) * 2; }
+
 // Maximum over the lanes l, l ^ 16, l ^ 32 and l ^ 48 (as sum_row_slots adds).
 __device__ __forceinline__ float max_row_slots(float x) {
   const uint32_t u = __float_as_uint(x);

@@ -1614,7 +1614,8 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
 damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* k_rope, const void* v,
                                        int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q, const int32_t* cu_k, int32_t B, int32_t Tq,
                                        int32_t Tk, int32_t num_heads, int32_t d, float scale, void* out, void* stream) {
-  if (B < 0 || Tq < 0 || Tk < 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d), Tq (%d) and Tk (%d) must be >= 0", B, Tq, Tk);
+  if (B < 0 || Tq < 0 || Tk < 0 || Tq > (1 << 30) || Tk > (1 << 30))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "B (%d) must be >= 0, Tq (%d) and Tk (%d) in [0, 2^30]", B, Tq, Tk);
   if (num_heads <= 0) return fail(DAMP_ERR_INVALID_ARGUMENT, "num_heads (%d) must be positive", num_heads);
   if (d != 64 && d != 128) return fail(DAMP_ERR_UNSUPPORTED, "d = %d: prompts by latents support d in {64, 128}", d);
   for (const int64_t x : {k_token_stride, v_token_stride})
