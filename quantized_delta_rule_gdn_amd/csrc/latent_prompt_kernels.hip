@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void latent_prompt_kernel(con
   }
 
   int* any_odd = reinterpret_cast<int*>(r0);
-  landed();                        // (loads into the flag's place)
+  landed();                        // (nothing may be on its way into the flag's place, or into LDS that the workgroup no longer holds)
   __syncthreads();
   if (tid == 0) *any_odd = 0;
   __syncthreads();

@@ -280,19 +280,18 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
   }
 }
 
-// Many rows: the 16 R rows of each wave are its own, and a tile of 64 tokens goes through LDS for all
-// four, the next one on its way in registers (read by every wave for itself, 64 rows would draw 64 KB a
-// tile from the L1, as long as their products take).
+// Many rows: the 16 R rows of each wave are its own, and tiles of 64 tokens are loaded into LDS for all four,
+// the next one among this one's products, with one barrier a tile (read by every wave for itself, 64 rows
+// would draw 64 KB a tile from the L1, as long as their products take).
 constexpr int kWideTile = 64;
 
 template <int D, int R, bool P16>
-__global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel(const TreeArgs a, const TokenPlan plan) {
+__global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(const TreeArgs a, const TokenPlan plan) {
   constexpr int KS = D / 32, MB = D / 16, TB = kWideTile / 16;
-  constexpr int LD = D * 2 + 32;                        // bytes between rows in LDS: an odd number of 32-byte units
-  constexpr int PW = D / 8, RL = 64 / PW, NL = 16 / RL; // 16-byte pieces of a row, rows of a load, loads for a wave's 16 rows
-  __shared__ __align__(16) uint8_t tile_k[kWideTile * LD];
-  __shared__ __align__(16) uint8_t tile_v[kWideTile * LD];
-  __shared__ uint32_t tile_live[4];
+  constexpr int PW = D / 8, RL = 64 / PW, NL = 16 / RL;   // 16-byte pieces of a row, rows of a load, loads for a wave's 16 rows
+  // (each buffer is an array of its own, so that reads of one need not keep their order with loads into another)
+  __shared__ __align__(1024) uint8_t k0[kWideTile * D * 2], k1[kWideTile * D * 2], v0[kWideTile * D * 2], v1[kWideTile * D * 2];
+  __shared__ uint32_t tile_live[2][4];
   __shared__ int any_odd;                               // values that are not finite have been taken out
 
   const int tid = __builtin_amdgcn_workitem_id_x(), lane = tid & 63;
@@ -343,99 +342,111 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
   }
   uint32_t odd = 0;
 
-  // Each wave carries 16 rows of a tile's keys and values. Their pages are looked up one tile ahead.
-  u32x4 sk[NL], sv[NL];
-  uint32_t carried = 0;              // which of the rows exist
+  // Each wave loads 16 rows of a tile's keys and values. Their pages are looked up one tile ahead.
   const int row_l = lane / PW, piece_l = lane % PW;
+  uint32_t k_off[NL], v_off[NL];
+#pragma unroll
+  for (int n = 0; n < NL; ++n) {
+    const int t = 16 * wv + n * RL + row_l;
+    k_off[n] = (n * RL + row_l) * (P16 ? D * 2 : 0) + (piece_l ^ row_turn<PW>(t)) * 16;
+    v_off[n] = (n * RL + row_l) * (P16 ? D * 2 : 0) + (piece_l ^ column_turn<PW>(t)) * 16;
+  }
   const auto page_of = [&](int t0) -> int {
     const int pos = min(t0 + 16 * wv + (P16 ? 0 : r), end - 1);
     return a.table[int64_t(b) * a.max_blocks + (pos >> a.page_log2)];
   };
-  const auto issue = [&](int t0, int pid) {
+  struct Tile {
+    int64_t at[P16 ? 1 : NL];      // bytes to the wave's rows, or to each load's
+    uint32_t live;                 // which rows exist
+  };
+  const auto tile_at = [&](int t0, int pid) -> Tile {
     const int left = min(max(end - (t0 + 16 * wv), 0), 16);
+    Tile from;
     if constexpr (P16) {
       const int id0 = __builtin_amdgcn_readfirstlane(pid);
       const bool fine = id0 >= 0 && id0 < a.num_pages && left > 0;
-      carried = fine ? (1u << left) - 1 : 0;
+      from.live = fine ? (1u << left) - 1 : 0;
       // (rows past the end lie in the same page; where there is no page, the first one's rows stand in)
-      const int64_t first = (fine ? ((int64_t(id0) * a.Hkv + kvh) << a.page_log2) + ((t0 + 16 * wv) & in_page) : 0) * (D * 2);
-      const uint8_t *kb = a.k_pages + first, *vb = a.v_pages + first;
-      const uint32_t off = row_l * (D * 2) + piece_l * 16;
-#pragma unroll
-      for (int n = 0; n < NL; ++n) {
-        sk[n] = *reinterpret_cast<const u32x4*>(kb + off + n * RL * (D * 2));
-        sv[n] = *reinterpret_cast<const u32x4*>(vb + off + n * RL * (D * 2));
-      }
+      from.at[0] = (fine ? ((int64_t(id0) * a.Hkv + kvh) << a.page_log2) + ((t0 + 16 * wv) & in_page) : 0) * (D * 2);
     } else {
       const bool fine = pid >= 0 && pid < a.num_pages && r < left;
-      carried = static_cast<uint32_t>(__ballot(fine)) & 0xffffu;
+      from.live = static_cast<uint32_t>(__ballot(fine)) & 0xffffu;
       const uint32_t mine = fine ? ((static_cast<uint32_t>(pid) * a.Hkv + kvh) << a.page_log2) + ((t0 + 16 * wv + r) & in_page) : 0;
 #pragma unroll
-      for (int n = 0; n < NL; ++n) {
-        const int64_t at = (int64_t(static_cast<uint32_t>(__shfl(static_cast<int>(mine), n * RL + row_l))) * PW + piece_l) * 16;
-        sk[n] = *reinterpret_cast<const u32x4*>(a.k_pages + at);
-        sv[n] = *reinterpret_cast<const u32x4*>(a.v_pages + at);
-      }
+      for (int n = 0; n < NL; ++n) from.at[n] = int64_t(static_cast<uint32_t>(__shfl(static_cast<int>(mine), n * RL + row_l))) * (D * 2);
     }
+    return from;
+  };
+  constexpr int kLoads = 2 * NL;
+  const auto load = [&](int n, const Tile& from, uint8_t* tile_k, uint8_t* tile_v) {
+    const int i = n % NL, to = 16 * wv * (D * 2) + i * 1024;
+    const int64_t at = from.at[P16 ? 0 : i];
+    if (n < NL) load_to_lds(a.k_pages + at + k_off[i], tile_k + to);
+    else load_to_lds(a.v_pages + at + v_off[i], tile_v + to);
   };
   int pid = 0;
   if (tid == 0) any_odd = 0;
   if (begin < end) {
-    pid = page_of(begin);
-    issue(begin, pid);
-    if (begin + kWideTile < end) pid = page_of(begin + kWideTile);
+    const Tile from = tile_at(begin, page_of(begin));
+    pid = page_of(begin + kWideTile);
+#pragma unroll
+    for (int n = 0; n < kLoads; ++n) load(n, from, k0, v0);
+    if (lane == 0) tile_live[0][wv] = from.live;
   } else {
     __syncthreads();
   }
-  for (int t0 = begin; t0 < end; t0 += kWideTile) {
-    __syncthreads();                 // the tile before is no longer read
+  // The tile at t0, which lies in the first two buffers, while the next is loaded into the others.
+  const auto step = [&](int t0, int buf, uint8_t* tile_k, uint8_t* tile_v, uint8_t* next_k, uint8_t* next_v) {
+    landed();
+    __syncthreads();                 // (the tile before is no longer read, either)
+    uint32_t live_w[4];
 #pragma unroll
-    for (int n = 0; n < NL; ++n) {
-      const int row = n * RL + row_l, at = (16 * wv + row) * LD + piece_l * 16;
-      const uint32_t keep = carried >> row & 1 ? ~0u : 0u;
-      u32x4 w = sv[n];
-      if (carried != 0xffffu) w &= rarely(keep);
-      if (t0 + kWideTile > dr.base) {
-        w = rarely(w);
+    for (int w = 0; w < 4; ++w) live_w[w] = __builtin_amdgcn_readfirstlane(tile_live[buf][w]);
+    if ((live_w[0] & live_w[1] & live_w[2] & live_w[3]) != 0xffffu || t0 + kWideTile > dr.base) {
+      // rows that do not exist become 0, and values that are not finite, which some token may not see, are taken out
+#pragma unroll
+      for (int n = 0; n < NL; ++n) {
+        u32x4* at = reinterpret_cast<u32x4*>(tile_v + 16 * wv * (D * 2) + n * 1024 + lane * 16);
+        u32x4 w = *at;
+        w &= tile_live[buf][wv] >> (n * RL + row_l) & 1 ? ~0u : 0u;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           odd |= not_finite(w[x]);
           w[x] = finite_only(w[x]);
         }
+        *at = w;
       }
-      *reinterpret_cast<u32x4*>(tile_k + at) = sk[n];
-      *reinterpret_cast<u32x4*>(tile_v + at) = w;
+      __syncthreads();
     }
-    if (lane == 0) tile_live[wv] = carried;
-    __syncthreads();
-    if (t0 + kWideTile < end) {
-      issue(t0 + kWideTile, pid);
-      if (t0 + 2 * kWideTile < end) pid = page_of(t0 + 2 * kWideTile);
+    // (after the last tile rows that exist are loaded again: no branch among the products)
+    const Tile from = tile_at(t0 + kWideTile, pid);
+    pid = page_of(t0 + 2 * kWideTile);
+    if (lane == 0) tile_live[buf ^ 1][wv] = from.live;
+    if (idle) {
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) load(n, from, next_k, next_v);
+      return;
     }
-    if (idle) continue;
 
+    // Operands are read four steps ahead (a read from LDS takes as long as some ten products), and the next tile's
+    // loads go out one by one among the products (each takes the address unit 16 cycles).
+    const auto operand = [&](int n) -> Frag {
+      const int t = 16 * (n / KS) + r;
+      return load_frag(tile_k + t * (D * 2) + ((4 * (n % KS) + g) ^ row_turn<PW>(t)) * 16);
+    };
     f32x4 s[R][TB];
+    Frag kf[4];
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb) {
+    for (int n = 0; n < 4; ++n) kf[n] = operand(n);
 #pragma unroll
-      for (int j = 0; j < R; ++j) s[j][tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < TB * KS; ++n) {
 #pragma unroll
-      for (int x = 0; x < KS; ++x) {
-        const Frag kf = load_frag(tile_k + (16 * tb + r) * LD + g * 16 + x * 64);
-#pragma unroll
-        for (int j = 0; j < R; ++j) s[j][tb] = mfma(kf, qf[j][x], s[j][tb]);
-      }
+      for (int j = 0; j < R; ++j) s[j][n / KS] = mfma(kf[n % 4], qf[j][n % KS], n % KS == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : s[j][n / KS]);
+      if (n + 4 < TB * KS) kf[n % 4] = operand(n + 4);
+      if (n % 2 == 0 && n / 2 < kLoads) load(n / 2, from, next_k, next_v);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    // (operands four steps ahead: a read from LDS takes as long as some ten products)
-    __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-#pragma unroll
-    for (int x = 0; x < TB * KS; ++x) {
-      __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    }
-    uint32_t live[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) live[h] = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(tile_live[2 * h] | tile_live[2 * h + 1] << 16));
+    const uint32_t live[2] = {live_w[0] | live_w[1] << 16, live_w[2] | live_w[3] << 16};
     if ((live[0] & live[1]) != ~0u || t0 + kWideTile > dr.base) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -476,10 +487,11 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
     }
 #pragma unroll
     for (int st = 0; st < TB / 2; ++st) {
-      const uint8_t* v = tile_v + (32 * st + 4 * g + (r >> 2)) * LD + 8 * (r & 3);
+      const int t = 32 * st + 4 * g + (r >> 2), turn = column_turn<PW>(t);    // (the row 16 further has the same turn)
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        const Frag vf = load_frag_t(reinterpret_cast<const uint16_t*>(v + 32 * m), reinterpret_cast<const uint16_t*>(v + 32 * m + 16 * LD));
+        const uint8_t* v = tile_v + t * (D * 2) + ((2 * m + (r >> 1 & 1)) ^ turn) * 16 + (r & 1) * 8;
+        const Frag vf = load_frag_t(reinterpret_cast<const uint16_t*>(v), reinterpret_cast<const uint16_t*>(v + 16 * D * 2));
 #pragma unroll
         for (int j = 0; j < R; ++j) o[j][m] = mfma(vf, pf[j][st], o[j][m]);
       }
@@ -490,7 +502,12 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
       __builtin_amdgcn_sched_group_barrier(0x008, R, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
     }
+  };
+  for (int t0 = begin; t0 < end; t0 += 2 * kWideTile) {
+    step(t0, 0, k0, v0, k1, v1);
+    if (t0 + kWideTile < end) step(t0 + kWideTile, 1, k1, v1, k0, v0);
   }
+  landed();                          // (nothing may be on its way into LDS that the workgroup no longer holds)
 
   if (__any(odd != 0)) any_odd = 1;
   __syncthreads();
@@ -534,8 +551,8 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_wide_kernel
 TokenPlan tree_plan(const TreeSizes& z, int d) {
   const int64_t rows = int64_t(z.max_new) * (z.Hq / z.Hkv);
   const int log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : rows <= 64 ? 6 : 7;
-  // workgroups that registers leave room for on the 256 CUs: 3 each, 2 with 32 or 128 rows of d = 128
-  return token_plan(z, log2, d == 128 && log2 % 2 == 1 ? 512 : 768, log2 <= 5 ? 1024 : 384);
+  // workgroups that registers and LDS leave room for on the 256 CUs: 3 each, 2 with more than 16 rows of d = 128
+  return token_plan(z, log2, d == 128 && log2 > 4 ? 512 : 768, log2 <= 5 ? 1024 : 384);
 }
 
 template <int D, int R, bool P16>
