@@ -64,7 +64,9 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All loads but the `later` youngest are back.
+template <int later = 0>
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(later) : "memory"); }
 
 // Rows loaded that way lie close together in LDS. So that operands are read without bank conflicts, piece p (16
 // bytes) of row t lies at p ^ row_turn(t) where rows are read whole (one access of 16 lanes takes piece c of
@@ -102,35 +104,30 @@ __device__ __forceinline__ T rarely(T x) {
 // An operand of ones: its product with the weights is their sum, in every row of the C tile.
 __device__ __forceinline__ Frag ones() { return Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}; }
 
-// Softmax weights of one row as an operand of the product with V, and their sum. PIECES == 1: each
-// weight rounded to bf16 (2^-9 of it), the sum over the rounded ones, so that equal values come back
-// as they are. PIECES == 2: the upper 16 bits of the weight (less 2^-12) and the rest rounded, good
-// to 2^-15 + 2^-20 of it, the rest never 0 (an infinite value times 0 would be NaN).
-template <int PIECES, int N>
-__device__ __forceinline__ void pack_pair(float x0, float x1, int i, uint32_t (&w)[PIECES][N], float& sum) {
-  if constexpr (PIECES == 1) {
-    w[0][i] = pack_bf16(x0, x1);
-    sum += bf16_lo(w[0][i]) + bf16_hi(w[0][i]);
-  } else {
-    const uint32_t w0 = __float_as_uint(x0 * 0x1.ffep-1f), w1 = __float_as_uint(x1 * 0x1.ffep-1f);
-    w[0][i] = __builtin_amdgcn_perm(w1, w0, 0x07060302u);
-    w[1][i] = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
-    sum += x0 + x1;
-  }
-}
-
-// (one piece, the sum left to a product with ones)
+// Softmax weights of one row as an operand of the product with V, in one of two ways. Rounded to bf16 (to
+// 2^-9 of each), with a sum over the rounded ones, so that equal values come back as they are: what a row
+// gets is then off by 2^-9 of the weighted mean of |v - o|, the size of its own rounding. Or in two pieces,
+// the upper 16 bits of the weight (less 2^-12) and the rest rounded, good to 2^-15 + 2^-20 of it, the rest
+// never 0 (an infinite value times 0 would be NaN): twice the products, which few rows have to spare.
 __device__ __forceinline__ Frag round_weights(const float (&p)[8]) {
   return Frag{{pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]), pack_bf16(p[6], p[7])}};
 }
 
-template <int PIECES>
-__device__ __forceinline__ void pack_weights(const float (&p)[8], Frag* pf, float& sum) {
-  uint32_t w[PIECES][4];
+__device__ __forceinline__ uint32_t round_pair(float x0, float x1, float& sum) {
+  const uint32_t w = pack_bf16(x0, x1);
+  sum += bf16_lo(w) + bf16_hi(w);
+  return w;
+}
+
+__device__ __forceinline__ void pack_weights(const float (&p)[8], Frag (&pf)[2], float& sum) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) pack_pair<PIECES>(p[2 * i], p[2 * i + 1], i, w, sum);
-#pragma unroll
-  for (int x = 0; x < PIECES; ++x) pf[x] = Frag{{w[x][0], w[x][1], w[x][2], w[x][3]}};
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = p[2 * i], x1 = p[2 * i + 1];
+    const uint32_t w0 = __float_as_uint(x0 * 0x1.ffep-1f), w1 = __float_as_uint(x1 * 0x1.ffep-1f);
+    pf[0].w[i] = __builtin_amdgcn_perm(w1, w0, 0x07060302u);
+    pf[1].w[i] = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
+    sum += x0 + x1;
+  }
 }
 
 // 0x8000 / 0x80000000 bits of the halves that hold an infinity or a NaN.

@@ -14,7 +14,7 @@ namespace {
 // tile of 32 tokens straight from the pages into registers as operands, and the waves meet in LDS
 // at the end. The rows of a product are the (drafted token, query head) pairs of one key-value head,
 // 16 R a workgroup: a tile's keys and values serve R operand groups once they are in registers.
-template <int D, int R, bool P16, int PIECES>
+template <int D, int R, bool P16>
 __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(const TreeArgs a, const TokenPlan plan) {
   constexpr int KS = D / 32;       // k steps of the score product
   constexpr int DPL = D / 16;      // value channels per lane
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
             if (!(seen >> (16 * (i >> 2) + (i & 3)) & 1)) p[j][i] = -INFINITY;
         }
       }
-      Frag pf[R][PIECES];
+      Frag pf[R][2];
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         float top = -INFINITY;
@@ -190,10 +190,8 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
         }
         const float base = mx[j] == -INFINITY ? 0.0f : mx[j];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          p[j][i] = pow2(p[j][i] - base);
-        }
-        pack_weights<PIECES>(p[j], pf[j], sum[j]);
+        for (int i = 0; i < 8; ++i) p[j][i] = pow2(p[j][i] - base);
+        pack_weights(p[j], pf[j], sum[j]);
       }
 #pragma unroll
       for (int m = 0; m < DPL; m += 2) {   // (each sum's products apart)
@@ -204,7 +202,7 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
           vf[1].w[w] = __builtin_amdgcn_perm(vr[2 * w + 1][m / 2], vr[2 * w][m / 2], 0x07060302u);
         }
 #pragma unroll
-        for (int x = 0; x < PIECES; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int j = 0; j < R; ++j) {
             o[j][m] = mfma(vf[0], pf[j][x], o[j][m]);
@@ -402,8 +400,9 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(cons
     uint32_t live_w[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) live_w[w] = __builtin_amdgcn_readfirstlane(tile_live[buf][w]);
-    if ((live_w[0] & live_w[1] & live_w[2] & live_w[3]) != 0xffffu || t0 + kWideTile > dr.base) {
-      // rows that do not exist become 0, and values that are not finite, which some token may not see, are taken out
+    const bool drafted = t0 + kWideTile > dr.base;
+    if ((live_w[0] & live_w[1] & live_w[2] & live_w[3]) != 0xffffu || drafted) {
+      // rows that do not exist become 0, and values that are not finite, where some token may not see them, are taken out
 #pragma unroll
       for (int n = 0; n < NL; ++n) {
         u32x4* at = reinterpret_cast<u32x4*>(tile_v + 16 * wv * (D * 2) + n * 1024 + lane * 16);
@@ -411,6 +410,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(cons
         w &= tile_live[buf][wv] >> (n * RL + row_l) & 1 ? ~0u : 0u;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          if (!drafted) continue;
           odd |= not_finite(w[x]);
           w[x] = finite_only(w[x]);
         }
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(cons
       __builtin_amdgcn_sched_barrier(0);
     }
     const uint32_t live[2] = {live_w[0] | live_w[1] << 16, live_w[2] | live_w[3] << 16};
-    if ((live[0] & live[1]) != ~0u || t0 + kWideTile > dr.base) {
+    if ((live[0] & live[1]) != ~0u || drafted) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -557,7 +557,7 @@ TokenPlan tree_plan(const TreeSizes& z, int d) {
 
 template <int D, int R, bool P16>
 void tree_drp(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
-  if (p.rows_log2 <= 5) hipLaunchKernelGGL((kv_tree_kernel<D, R, P16, 2>), dim3(p.groups), dim3(256), 0, s, a, p);
+  if (p.rows_log2 <= 5) hipLaunchKernelGGL((kv_tree_kernel<D, R, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
   else hipLaunchKernelGGL((kv_tree_wide_kernel<D, R, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
 }
 
