@@ -660,7 +660,11 @@ hipError_t launch_latent_append(const LatentAppendArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int64_t latent_grid(const TreeSizes& z, int32_t dc) { return token_groups(latent_plan(z), z, dc); }
+// (in workgroups of 256 threads: those of more than 16 rows have twice as many)
+int64_t latent_grid(const TreeSizes& z, int32_t dc) {
+  const TokenPlan p = latent_plan(z);
+  return std::max<int64_t>(token_groups(p, z, dc), p.rows_log2 > 4 ? int64_t(2) * p.groups : 0);
+}
 
 size_t latent_ws_bytes(const TreeSizes& z, int32_t dc) { return parts_bytes(latent_plan(z), z, dc); }
 
