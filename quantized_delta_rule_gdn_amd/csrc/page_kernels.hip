@@ -167,7 +167,7 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(const CompactArgs a, in
     for (int u = 0; u < U; ++u) {
       if (moves(j0, now, u)) {
         const uint32_t to = ((static_cast<uint32_t>(now.pt[u]) * a.Hkv + h) << a.page_log2) + ((base + j0 + u * rows + row) & in_page);
-        pages[int64_t(to) * per_row + piece] = w[u];
+        __builtin_nontemporal_store(w[u], pages + int64_t(to) * per_row + piece);
       }
       w[u] = ahead[u];
     }
