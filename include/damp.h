@@ -703,10 +703,14 @@ size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t
  *   max_new     no request has more new tokens than this (in [0, 2^30], at most 64 mask_words with a mask);
  *               further ones get no readout
  * Other arguments as kv_decode_attention; pages may be shared, nothing is stored. Scores, softmax
- * statistics and sums are binary32; the softmax weights enter the product with V as in kv_decode_attention.
+ * statistics and sums are binary32. The softmax weights enter the product with V as in kv_decode_attention
+ * where max_new * num_q_heads / num_kv_heads is at most 16, and else rounded to bf16 (2^-9 of each),
+ * over the sum of the rounded ones; they are relative to a score that the row's highest may pass by up to
+ * 2^8, so values of 2^120 and more may end infinite. Readouts do not depend on the other requests of a call;
+ * they may differ in their last bit with max_new, max_len and how the requests' lengths share out the work.
  * A NaN or infinity of a new token's value reaches only the tokens that see it. max_new * num_q_heads
- * stays at most 2^30 - 1, B * max_new * num_q_heads / 16 below 2^24. Errors: INVALID_ARGUMENT,
- * UNSUPPORTED (d, page_size), HIP. */
+ * stays at most 2^30 - 1, and B * num_kv_heads times the tiles of 64 query rows of a request's max_new tokens
+ * below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
 damp_status kv_tree_attention(const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* block_table, const int32_t* seq_lens,
                               const int32_t* cu_new, const int64_t* mask, int32_t mask_words, int32_t T,
@@ -725,6 +729,7 @@ damp_status kv_latent_append(const void* c, const void* k_rope, const int64_t* s
                              int32_t d_latent, int32_t d_rope, void* pages, int32_t num_pages,
                              int32_t page_size, void* stream);
 
+/* As kv_tree_attention_workspace_bytes, for kv_latent_attention. */
 size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t d_latent,
                                            int32_t max_new, int32_t max_len);
 
@@ -733,8 +738,8 @@ size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t
  * q dev bf16 [T][num_heads][d_latent + d_rope] (a head's query times its key up-projection, then the rotary
  * part), out dev bf16 [T][num_heads][d_latent] (the value up-projection follows). scale is that of the
  * expanded form's channels. cu_new NULL: one token per request (T == B, max_new 1, no mask). Other arguments
- * and limits as kv_tree_attention. The softmax weights enter the product rounded to bf16 (2^-9 of
- * each), over the sum of the rounded ones. */
+ * and limits as kv_tree_attention (tiles of 64 rows of all heads, below 2^23). The softmax weights enter the product
+ * rounded to bf16 (2^-9 of each), over the sum of the rounded ones, whatever the number of rows. */
 damp_status kv_latent_attention(const void* q, const void* pages, const int32_t* block_table,
                                 const int32_t* seq_lens, const int32_t* cu_new, const int64_t* mask,
                                 int32_t mask_words, int32_t T, int32_t B, int32_t max_new,
@@ -752,7 +757,7 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
  *   out         dev bf16 [Tq][num_heads][d]; a query that sees no key gives 0
  *   cu_q, cu_k  dev int32 [B + 1], ascending, kept inside [0, Tq] and [0, Tk]. Rows of out behind the last
  *               request are not written.
- * All 16-byte aligned but cu_q and cu_k. d is 64 or 128. Scores, statistics and sums are binary32, the
+ * All 16-byte aligned but cu_q and cu_k. d is 64 or 128, Tq and Tk at most 2^30. Scores, statistics and sums are binary32, the
  * weights rounded as in kv_latent_attention. A NaN or infinity of a token reaches only queries that see
  * it. (Tq / 64 + B) * num_heads stays below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d), HIP. */
 damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride,

@@ -30,7 +30,9 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppendAr
 // workgroup holds in LDS serves both products of all its rows.
 constexpr int kLatTile = 64;
 
-// Up to 16 rows: the stream of the cache is what takes longest. The 4 waves share out the scores by tokens, meet
+// Up to 16 rows: the stream of the cache is what takes longest (64 requests, 266,000 tokens, 16 heads: 67 us and 8
+// for the join; 5.3 TB/s behind the first 8 us, in which lengths, pages and the first tiles are on their way;
+// the eight waves below take the same, and 17 instead of 16 us for one request of 700 tokens). The 4 waves share out the scores by tokens, meet
 // for the maximum of each row, hand the weights over through LDS, and share out the readout by channels, so
 // that a tile is read from LDS once (scores: as rows; readout: transposed on the way). The next tile is
 // on its way in registers meanwhile.
@@ -267,6 +269,11 @@ __global__ __launch_bounds__(256, 2) void latent_kernel(const TreeArgs a, const 
 // one barrier a tile. The rows' references (what their weights are relative to) stay as they are until a
 // score passes one by 2^kSlack, as it does in a run's first tile: then, two more barriers are met, in which
 // the scoring waves agree on new ones.
+// 24 requests of up to 4,096 tokens with up to 4 drafted and 128 heads: 66 us and 11 for the join (85 with tiles
+// carried through registers, stored to LDS between two barriers), 520 TFLOP/s. A tile of 32 tokens takes some 2,400
+// cycles: 1,088 of products on each SIMD, 850 for its loads to go out (36 KB through a path of 64 bytes a cycle),
+// the rest exponentials, looking what is rare and the barrier; the loads among the products slowed both (72 us),
+// behind them too (83).
 template <int DC, int R>
 struct LatWide {
   static constexpr int DR = DC / 8, W = DC + DR, CH = W / 8;     // channels of a row, its 16-byte pieces
@@ -314,10 +321,17 @@ __global__ __launch_bounds__(512, 2) void latent_wide_kernel(const TreeArgs a, c
   // What is rare before tile i is weighed: rows that do not exist become 0, values that are not finite, which some
   // token may not see, are taken out (the scores have been taken), and the references are raised. `agree` is
   // the scoring waves' part of that.
-  const auto before_weighing = [&](int i, int buf, uint8_t* tile, auto&& publish, auto&& agree) -> bool {
-    const int last = raised[i & 1];
+  struct Rare {
+    int last;
+    uint32_t live;
+  };
+  const auto look = [&](int i, int buf) -> Rare {
     const uint4 lives = *reinterpret_cast<const uint4*>(tile_live[buf]);
-    const uint32_t live = lives.x & lives.y & lives.z & lives.w;
+    return Rare{raised[i & 1], lives.x & lives.y & lives.z & lives.w};
+  };
+  const auto before_weighing = [&](int i, Rare rare, int buf, uint8_t* tile, auto&& publish, auto&& agree) -> bool {
+    const int last = rare.last;
+    const uint32_t live = rare.live;
     const bool up = __builtin_amdgcn_readfirstlane(last) == i;
     const bool drafted = begin + (i + 1) * TILE > dr.base;
     const bool clean = drafted || __builtin_amdgcn_readfirstlane(live) != 0xffu;
@@ -444,7 +458,7 @@ __global__ __launch_bounds__(512, 2) void latent_wide_kernel(const TreeArgs a, c
     };
     const auto step = [&](int i, int buf, uint8_t* tile, const uint8_t* next) {
       if (i >= tiles) return;
-      before_weighing(i, buf, tile, publish, [&]() {
+      before_weighing(i, look(i, buf), buf, tile, publish, [&]() {
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
           const int row = row_w + 16 * j + r;
@@ -547,10 +561,11 @@ __global__ __launch_bounds__(512, 2) void latent_wide_kernel(const TreeArgs a, c
   __syncthreads();
   const auto step = [&](int i, int buf, uint8_t* tile, uint8_t* free) {
     if (i >= tiles) return;
+    const Rare rare = look(i, buf);
     const int now = pid;
     pid = page_of(i + 4);
     load(i + 3, now, (buf + 3) & 3, free);
-    if (before_weighing(i, buf, tile, []() {}, []() {})) {
+    if (before_weighing(i, rare, buf, tile, []() {}, []() {})) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
         const float shrink = row_m[16 * j + r];
@@ -630,7 +645,10 @@ __global__ __launch_bounds__(512, 2) void latent_wide_kernel(const TreeArgs a, c
 TokenPlan latent_plan(const TreeSizes& z) {
   const int64_t rows = int64_t(z.max_new) * z.Hq;
   const int log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : 6;
-  // workgroups that LDS leaves room for on the 256 CUs: two of four waves each, or one of eight
+  // Workgroups that LDS leaves room for on the 256 CUs: two of four waves each, or one of eight. 32 rows in tiles
+  // of 64 take 73 us instead of 69 (64 requests of 4,000 tokens, 32 heads). Requests of up to 256 tokens are not cut:
+  // 250 with 16 heads take 15.5 us whole and 13.7 cut, with d_latent = 256 10.3 and 13.3, 16 of them with 128 heads
+  // 22 and 29; 400 take 22.5 whole and 14.2 cut.
   return token_plan(z, log2, log2 == 4 ? 512 : 256, 256);
 }
 

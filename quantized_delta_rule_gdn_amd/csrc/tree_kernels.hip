@@ -13,9 +13,11 @@ namespace {
 // token, a request's tokens are cut into items, each of the 4 waves of a workgroup takes every fourth
 // tile of 32 tokens straight from the pages into registers as operands, and the waves meet in LDS
 // at the end. The rows of a product are the (drafted token, query head) pairs of one key-value head,
-// 16 R a workgroup: a tile's keys and values serve R operand groups once they are in registers.
-template <int D, int R, bool P16>
-__global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(const TreeArgs a, const TokenPlan plan) {
+// 16 a workgroup. Bound by the stream of the cache: 64 requests of 8,000 tokens, 8 heads of d = 128, 353 us
+// or 5.9 TB/s (reading alone reaches 7.1); short ones by latency (one request of 500 tokens 10 us, call
+// included). The weights' second piece costs nothing there.
+template <int D, bool P16>
+__global__ __launch_bounds__(256, 3) void kv_tree_kernel(const TreeArgs a, const TokenPlan plan) {
   constexpr int KS = D / 32;       // k steps of the score product
   constexpr int DPL = D / 16;      // value channels per lane
   constexpr int VW = DPL / 2;      // dwords of them
@@ -34,7 +36,7 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
   if (b < 0) return;
   const int G = a.Hq / a.Hkv;
   const Drafts dr = spot.dr;
-  const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(spot.tile) * (16 * R);
+  const int64_t rows = int64_t(min(dr.n, a.max_new)) * G, row0 = int64_t(spot.tile) * 16;
   if (row0 >= rows) return;
   const Parts<D> parts(a, plan);
   const int len = spot.len;
@@ -43,28 +45,21 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
   const int begin = min(split * share, len), end = min(begin + share, len);
   const int in_page = (1 << a.page_log2) - 1;
 
-  const int live_rows = static_cast<int>(min(rows - row0, int64_t(16 * R)));
-  int token[R];                    // of this lane's rows
-  Frag qf[R][KS];
+  const int live_rows = static_cast<int>(min(rows - row0, int64_t(16)));
+  const unsigned my_row = static_cast<unsigned>(row0) + min(r, live_rows - 1);
+  const int token = my_row / G;
+  Frag qf[KS];
+  {
+    const int64_t at = int64_t(dr.first + token) * a.Hq + kvh * G + my_row % G;
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const unsigned row = static_cast<unsigned>(row0) + min(16 * j + r, live_rows - 1);
-    token[j] = row / G;
-    const int64_t at = int64_t(dr.first + token[j]) * a.Hq + kvh * G + row % G;
-#pragma unroll
-    for (int x = 0; x < KS; ++x) qf[j][x] = load_frag(a.q + (at * D + g * 8 + x * 32) * 2);
+    for (int x = 0; x < KS; ++x) qf[x] = load_frag(a.q + (at * D + g * 8 + x * 32) * 2);
   }
 
-  f32x4 o[R][DPL];
-  float mx[R], sum[R];
+  f32x4 o[DPL];
+  float mx = -INFINITY, sum = 0.0f;
   bool taken_out = false;
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    mx[j] = -INFINITY;
-    sum[j] = 0.0f;
-#pragma unroll
-    for (int m = 0; m < DPL; ++m) o[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
+  for (int m = 0; m < DPL; ++m) o[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const uint32_t k_off = r * (D * 2) + g * 16;                  // a half tile's K rows as operands
   const uint32_t v_off = 4 * g * (D * 2) + r * (DPL * 2);       // and its V rows
   constexpr int kRun = P16 ? kAttnPages * 16 : kAttnPages;
@@ -127,18 +122,15 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
           load_v(a.v_pages + int64_t(row == kNone ? 0 : row) * (D * 2) + r * (DPL * 2), i);
         }
       }
-      float p[R][8];
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        f32x4 s[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      float p[8];
+      {
+        f32x4 s[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
         for (int x = 0; x < KS; ++x)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) s[h] = mfma(kf[h][x], qf[j][x], s[h]);
+          for (int h = 0; h < 2; ++h) s[h] = mfma(kf[h][x], qf[x], s[h]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[j][i] = s[i >> 2][i & 3] * a.scale_log2;
+        for (int i = 0; i < 8; ++i) p[i] = s[i >> 2][i & 3] * a.scale_log2;
       }
       if (__any(dead != 0) || t0 + kAttnTile > to) {
 #pragma unroll
@@ -147,8 +139,7 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (dead >> i & 1) {
-#pragma unroll
-            for (int j = 0; j < R; ++j) p[j][i] = -INFINITY;
+            p[i] = -INFINITY;
 #pragma unroll
             for (int w = 0; w < VW; ++w) vr[i][w] = 0;   // whatever lies there: 0 * NaN is NaN
           }
@@ -166,33 +157,27 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
 #pragma unroll
             for (int w = 0; w < VW; ++w) vr[i][w] = finite_only(vr[i][w]);
         }
+        const uint32_t seen = seen_window(a, dr, token, t0 - dr.base) >> (4 * g);
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-          const uint32_t seen = seen_window(a, dr, token[j], t0 - dr.base) >> (4 * g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (!(seen >> (16 * (i >> 2) + (i & 3)) & 1)) p[j][i] = -INFINITY;
-        }
+        for (int i = 0; i < 8; ++i)
+          if (!(seen >> (16 * (i >> 2) + (i & 3)) & 1)) p[i] = -INFINITY;
       }
-      Frag pf[R][2];
+      float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        float top = -INFINITY;
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, p[i]);
+      if (__any(top > mx + kSlack)) {
+        top = fmaxf(max_row_slots(top), mx);
+        const float shrink = top == -INFINITY ? 1.0f : pow2(mx - top);
+        mx = top;
+        sum *= shrink;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmaxf(top, p[j][i]);
-        if (__any(top > mx[j] + kSlack)) {
-          top = fmaxf(max_row_slots(top), mx[j]);
-          const float shrink = top == -INFINITY ? 1.0f : pow2(mx[j] - top);
-          mx[j] = top;
-          sum[j] *= shrink;
-#pragma unroll
-          for (int m = 0; m < DPL; ++m) o[j][m] *= shrink;
-        }
-        const float base = mx[j] == -INFINITY ? 0.0f : mx[j];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[j][i] = pow2(p[j][i] - base);
-        pack_weights(p[j], pf[j], sum[j]);
+        for (int m = 0; m < DPL; ++m) o[m] *= shrink;
       }
+      const float base = mx == -INFINITY ? 0.0f : mx;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[i] = pow2(p[i] - base);
+      Frag pf[2];
+      pack_weights(p, pf, sum);
 #pragma unroll
       for (int m = 0; m < DPL; m += 2) {   // (each sum's products apart)
         Frag vf[2];
@@ -202,12 +187,10 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
           vf[1].w[w] = __builtin_amdgcn_perm(vr[2 * w + 1][m / 2], vr[2 * w][m / 2], 0x07060302u);
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int j = 0; j < R; ++j) {
-            o[j][m] = mfma(vf[0], pf[j][x], o[j][m]);
-            o[j][m + 1] = mfma(vf[1], pf[j][x], o[j][m + 1]);
-          }
+        for (int x = 0; x < 2; ++x) {
+          o[m] = mfma(vf[0], pf[x], o[m]);
+          o[m + 1] = mfma(vf[1], pf[x], o[m + 1]);
+        }
       }
     }
   }
@@ -220,67 +203,62 @@ __global__ __launch_bounds__(256, R * D <= 128 ? 3 : 2) void kv_tree_kernel(cons
       const int page = a.table[int64_t(b) * a.max_blocks + (t >> a.page_log2)];
       if (page < 0 || page >= a.num_pages) continue;
       const int64_t row = (((int64_t(page) * a.Hkv + kvh) << a.page_log2) + (t & in_page)) * (D * 2);
-      bool seen[R];
-#pragma unroll
-      for (int j = 0; j < R; ++j) seen[j] = t < dr.base || (seen_window(a, dr, token[j], t - dr.base) & 1);
+      const bool seen = t < dr.base || (seen_window(a, dr, token, t - dr.base) & 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i)          // channel DPL (4 g + i) + m
 #pragma unroll
         for (int m = 0; m < DPL; m += 4) {
           const uint2 v = *reinterpret_cast<const uint2*>(a.v_pages + row + (DPL * (4 * g + i) + m) * 2);
+          const f32x4 x = add_odd(f32x4{o[m][i], o[m + 1][i], o[m + 2][i], o[m + 3][i]}, v, seen);
 #pragma unroll
-          for (int j = 0; j < R; ++j) {
-            const f32x4 x = add_odd(f32x4{o[j][m][i], o[j][m + 1][i], o[j][m + 2][i], o[j][m + 3][i]}, v, seen[j]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[j][m + k][i] = x[k];
-          }
+          for (int k = 0; k < 4; ++k) o[m + k][i] = x[k];
         }
     }
   }
 
+  sum += __shfl_xor(sum, 16);
+  sum += __shfl_xor(sum, 32);
+  if (g == 0) {
+    part_m[wv][r] = mx;
+    part_l[wv][r] = sum;
+  }
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    if (16 * j >= live_rows) break;          // (the same for all threads)
-    sum[j] += __shfl_xor(sum[j], 16);
-    sum[j] += __shfl_xor(sum[j], 32);
-    if (j > 0) __syncthreads();
-    if (g == 0) {
-      part_m[wv][r] = mx[j];
-      part_l[wv][r] = sum[j];
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < DPL; ++m) part_o[wv][r][DPL * (4 * g + i) + m] = o[m][i];
+  __syncthreads();
+  for (int x = tid; x < live_rows * D; x += 256) {
+    const int h = x / D, c = x % D;
+    const float m0 = fmaxf(fmaxf(part_m[0][h], part_m[1][h]), fmaxf(part_m[2][h], part_m[3][h]));
+    const float base = m0 == -INFINITY ? 0.0f : m0;
+    float acc = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = pow2(part_m[w][h] - base);
+      acc = fmaf(f, part_o[w][h][c], acc);
+      l = fmaf(f, part_l[w][h], l);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int m = 0; m < DPL; ++m) part_o[wv][r][DPL * (4 * g + i) + m] = o[j][m][i];
-    __syncthreads();
-    const int live = min(live_rows - 16 * j, 16);
-    for (int x = tid; x < live * D; x += 256) {
-      const int h = x / D, c = x % D;
-      const float m0 = fmaxf(fmaxf(part_m[0][h], part_m[1][h]), fmaxf(part_m[2][h], part_m[3][h]));
-      const float base = m0 == -INFINITY ? 0.0f : m0;
-      float acc = 0.0f, l = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = pow2(part_m[w][h] - base);
-        acc = fmaf(f, part_o[w][h][c], acc);
-        l = fmaf(f, part_l[w][h], l);
-      }
-      if (splits == 1) {
-        const unsigned row = static_cast<unsigned>(row0) + 16 * j + h;
-        const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * D + c;
-        reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc / l);
-      } else {
-        const int64_t at = int64_t(spot.at) * plan.heads + 16 * j + h;
-        parts.o[at * D + c] = acc;
-        if (c == 0) parts.ml[at] = make_float2(m0, l);
-      }
+    if (splits == 1) {
+      const unsigned row = static_cast<unsigned>(row0) + h;
+      const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * D + c;
+      reinterpret_cast<uint16_t*>(a.out)[at] = float_to_bf16_bits(l == 0.0f ? 0.0f : acc / l);
+    } else {
+      const int64_t at = int64_t(spot.at) * plan.heads + h;
+      parts.o[at * D + c] = acc;
+      if (c == 0) parts.ml[at] = make_float2(m0, l);
     }
   }
 }
 
 // Many rows: the 16 R rows of each wave are its own, and tiles of 64 tokens are loaded into LDS for all four,
 // the next one among this one's products, with one barrier a tile (read by every wave for itself, 64 rows
-// would draw 64 KB a tile from the L1, as long as their products take).
+// would draw 64 KB a tile from the L1, as long as their products take). The weights are rounded once: a
+// second piece took 15 to 20% more time (48 requests 127 -> 142 us, 4 long ones 166 -> 203, before the tiles were
+// loaded ahead). 48 requests of up to 4,096 tokens, 128 rows, 8 heads of d = 128: 97 us and 14 for the join,
+// which is 4.4 TB/s; the matrix cores are busy for a fifth of the time, the waves wait for the stream (a third
+// tile on its way did not help: 119 us with it, 114 without). 4 requests of up to 65,536 tokens, 512 rows
+// of d = 64: 85 us and 11, 660 TFLOP/s; matrix cores busy 37%, vector unit 55%: for 16 x 16 scores the products take
+// 72 cycles, the exponentials alone 64 and the rest of the softmax 40.
 constexpr int kWideTile = 64;
 
 template <int D, int R, bool P16>
@@ -546,32 +524,35 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(cons
   }
 }
 
-// How a call's rows are taken. Up to 32 rows a key-value head: by every wave for itself (the R = 1 and 2 of
-// kv_tree_kernel); more: through LDS, 64 or 128 rows a workgroup.
+// How a call's rows are taken (us, call included).
+// - Up to 16 rows a key-value head: by kv_tree_kernel. A request of 500 tokens takes 10 and by the wide one 13;
+//   48 of 2,000, 8 heads of d = 128, take 80 and 84. With 32 rows these take 86 and 76.
+// - Else in tiles of 64 rows through LDS, or of 128 where there are enough of them: one request of 300 tokens with
+//   128 rows and 2 heads takes 10.1 in tiles of 64 and 13.3 in one of 128, 4 of 20,000 with 4 heads 33 and
+//   38; 8 of 30,000 with 4 heads 64 and 59, 48 of 2,000 with 8 heads 126 and 119.
+// - Workgroups at once: with 3 a CU instead of 2, 20 requests of 5,000 tokens with 16 rows take 86 instead of 81
+//   (with 1.5, 91); the wide ones of d = 64, which hold the least LDS, 97 with 3 and 100 with 2.
+// - Not cut up to 1,024 tokens (16 rows; 900 of d = 64 take 10.2 whole and 13.5 cut, of d = 128 14.4 and 13.5) or
+//   512 (500 take 12.6 whole and 13.4 cut, of d = 64 10.5 and 13.4; 700 with 128 rows 20.5 and 15).
 TokenPlan tree_plan(const TreeSizes& z, int d) {
-  const int64_t rows = int64_t(z.max_new) * (z.Hq / z.Hkv);
-  const int log2 = rows <= 16 ? 4 : rows <= 32 ? 5 : rows <= 64 ? 6 : 7;
-  // workgroups that registers and LDS leave room for on the 256 CUs: 3 each, 2 with more than 16 rows of d = 128
-  return token_plan(z, log2, d == 128 && log2 > 4 ? 512 : 768, log2 <= 5 ? 1024 : 384);
+  const int64_t rows = int64_t(z.max_new) * (z.Hq / z.Hkv), units = int64_t(z.B) * z.Hkv * ((rows + 127) / 128);
+  const int log2 = rows <= 16 ? 4 : rows <= 64 || units < 24 ? 6 : 7;
+  // workgroups that registers and LDS leave room for on the 256 CUs: 2 each, 3 of the wide ones with d = 64
+  return token_plan(z, log2, d == 64 && log2 > 4 ? 768 : 512, log2 == 4 ? 1024 : 512);
 }
 
-template <int D, int R, bool P16>
-void tree_drp(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
-  if (p.rows_log2 <= 5) hipLaunchKernelGGL((kv_tree_kernel<D, R, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
-  else hipLaunchKernelGGL((kv_tree_wide_kernel<D, R, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
-}
-
-template <int D, int R>
-void tree_dr(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
-  if (a.page_log2 >= 4) tree_drp<D, R, true>(a, p, s);
-  else tree_drp<D, R, false>(a, p, s);
+template <int D, bool P16>
+void tree_dp(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
+  if (p.rows_log2 == 4) hipLaunchKernelGGL((kv_tree_kernel<D, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
+  else if (p.rows_log2 == 6) hipLaunchKernelGGL((kv_tree_wide_kernel<D, 1, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
+  else hipLaunchKernelGGL((kv_tree_wide_kernel<D, 2, P16>), dim3(p.groups), dim3(256), 0, s, a, p);
 }
 
 template <int D>
 hipError_t tree_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
   const TokenPlan p = tree_plan(z, D);
-  if (p.rows_log2 % 2 == 0) tree_dr<D, 1>(a, p, s);
-  else tree_dr<D, 2>(a, p, s);
+  if (a.page_log2 >= 4) tree_dp<D, true>(a, p, s);
+  else tree_dp<D, false>(a, p, s);
   launch_join<D>(a, p, s);
   return hipGetLastError();
 }

@@ -73,8 +73,8 @@ def test_free_refusals(change, status, text):
 
 def test_free_workspace_sizes():
     size = lib.load().kv_free_pages_workspace_bytes
-    assert [size(n) for n in (-1, 0, 1, 65536)] == [0] * 4
-    assert 0 < size(65537) <= size(2 ** 24) <= size(2 ** 31 - 1) <= 2 ** 31
+    assert [size(n) for n in (-1, 0, 1, 8192)] == [0] * 4
+    assert 0 < size(8193) <= size(65537) <= size(2 ** 24) <= size(2 ** 31 - 1) <= 2 ** 31
     need = size(70000)
     _refused("kv_free_pages", FREE, dict(wsn=need - 1), BAD, f"{need} bytes")
 

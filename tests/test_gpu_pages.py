@@ -197,7 +197,7 @@ def _free(keep, lens, table, shares, page):
     assert torch.equal(tab, was)
 
 
-@pytest.mark.parametrize("pages", [1, 63, 4096, 4097, 20000, 65536, 65537, 300000])
+@pytest.mark.parametrize("pages", [1, 63, 4096, 4097, 8192, 8193, 20000, 65536, 65537, 300000])
 def test_free_random(pages):
     rng = np.random.default_rng(pages)
     B, page = min(pages, 40), 16
@@ -232,7 +232,7 @@ def test_free_edges():
 
 
 def test_free_workspace_and_refusals():
-    assert lib.kv_free_pages_workspace_bytes(65536) == 0 and lib.kv_free_pages_workspace_bytes(65537) > 0
+    assert lib.kv_free_pages_workspace_bytes(8192) == 0 and lib.kv_free_pages_workspace_bytes(8193) > 0
     z, t = _i32([0]), _i32([[0]])
     args = [z, _i32([5]), t, z, 16, z.clone(), z.clone()]
     for i, bad in ((0, _i32([0, 0])), (1, z.float()), (2, z), (3, t), (5, _i32([0, 0])), (6, _i32([0, 0])), (5, z.cpu())):

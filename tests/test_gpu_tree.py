@@ -16,8 +16,8 @@ PIECES = 2.0 ** -15 + 2.0 ** -20
 
 
 def weight(rows):
-    """What a weight is off by: two bf16 pieces for up to 32 query rows a key-value head, one rounding for more."""
-    return PIECES if rows <= 32 else ref.BF16
+    """What a weight is off by: two bf16 pieces for up to 16 query rows a key-value head, one rounding for more."""
+    return PIECES if rows <= 16 else ref.BF16
 
 
 
@@ -227,7 +227,11 @@ def test_lengths_that_do_not_fit():
     out = run([5, 40], [0, 5, 9], max_new=2)               # later ones get no readout
     assert bool((out[2:5] == 7.0).all()) and bool((out[7:] == 7.0).all()) and not bool((out[:2] == 7.0).any())
     whole = run([5, 40], [0, 5, 9])
-    assert torch.equal(out[:2], whole[:2]) and torch.equal(out[5:7], whole[5:7])
+    for b, (at, n, m) in enumerate(((0, 5, 5), (5, 4, 40))):    # (other bounds may take other kernels: the same values, not the same bits)
+        o, mag, e = ref.attend(q[at:at + n].double(), *(x.double() for x in keys[b]), ref.seen(n, m), 64 ** -0.5)
+        tol = ref.tolerance(o, mag, e, m, weight(24))
+        ref.is_close(whole[at:at + n], o, tol, "all")
+        ref.is_close(out[at:at + 2], o[:2], tol[:2], "the first two")
     out = run([5, 40], [-7, 5, 900])
     assert torch.equal(out[:5], whole[:5])
     run([5, 40], [9, 3, 1])
