@@ -13,19 +13,26 @@ namespace {
 // ---- how the work is shared out --------------------------------------------------------------------
 // A request's query rows (its new tokens' heads of one key-value head) are taken in tiles of `rows`, and
 // its cached tokens in runs; a workgroup takes one (run, key-value head, tile). The runs are cut on the
-// device, where the lengths are: by the least chunk with which the workgroups are no more than the chip
-// holds at once, as often over as one workgroup for each (request, head, tile) needs, so that a launch
-// is whole rounds of much the same length. (More runs even ragged lengths out better and cost their parts,
-// a write and a read of 8 bytes a row and channel: half as many again took as long for 48 requests of 200 to
-// 4,096 tokens with 128 rows each, 114 us, and 118 instead of 94 us for 48 of 2,000.)
+// device, where the lengths are. Where the (request, head, row tile) units are few, by the least chunk with
+// which the workgroups are no more than the chip holds at once: one round of runs of much the same length. Where
+// they are many, only what is longer than a workgroup's fair share, as others fill the chip meanwhile. (Cutting costs the parts, a write and a read of 4 bytes a row and channel: 48 requests of 2,000 tokens
+// with 128 rows, 384 units, take 118 us in two rounds of runs and 90 whole. 256 requests of 1,500 tokens of which
+// one has 100,000, 2,048 units, take 1,450 us with none cut, 356 so.)
 struct TokenPlan {
   int rows_log2;  // query rows of a tile
   int heads;      // rows of the largest tile there is
   int tiles;      // row tiles of a request with the most new tokens
   int slots;      // workgroups that the chip holds at once
-  int groups;     // of the launch
+  int groups;     // of the launch: whole rounds of the dies, at least what runs_of gives
   int whole;      // no request is cut
 };
+
+// Runs that units are cut into, at most.
+__host__ __device__ inline bool few_units(int64_t units, int slots) { return 4 * units <= 3 * int64_t(slots); }
+__host__ __device__ inline int64_t runs_of(int64_t units, int slots) { return few_units(units, slots) ? slots : units + slots / 2; }
+
+// Neighbouring parts that a die takes at a time.
+__host__ __device__ inline int dealt(int tiles) { return tiles < 16 ? tiles : 16; }
 
 // One workgroup's part. b < 0: none.
 struct Spot {
@@ -69,8 +76,9 @@ inline size_t parts_bytes(const TokenPlan& p, const TreeSizes& z, int32_t d) {
 }
 
 // Every wave finds its workgroup's part for itself, its lanes taking a request each. Workgroups go round the 8
-// dies, which have an L2 each: a die takes neighbouring parts of the list (request, run, head, tile), so
-// that row tiles that read the same keys meet in one L2.
+// dies, which have an L2 each: a die takes as many neighbouring parts of the list (request, run, head, tile) at
+// a time as there may be row tiles (up to 16), so that those that read the same keys meet in one L2. Where the list is
+// longer than a round, requests that are cut come first: the last ones to start are then short.
 template <int GRAIN, int D>
 __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan) {
   const unsigned id = __builtin_amdgcn_workgroup_id_x();
@@ -82,31 +90,58 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
     return Spot{b, unit / plan.tiles, unit % plan.tiles, 0, 1, 0, drafts_of(a, b), length_of(a, b)};
   }
   const int lane = __builtin_amdgcn_workitem_id_x() & 63;
-  const Share own = lane < a.B ? share_of(a, plan, lane) : Share{};
-  const auto over_requests = [&](auto&& f) {
-    auto x = f(own);
-    for (int b = lane + 64; b < a.B; b += 64) x += f(share_of(a, plan, b));
-    return last_lane(scan64(x));
+  const auto share = [&](int b) -> Share {           // none behind the last request
+    Share s = share_of(a, plan, min(b, a.B - 1));
+    if (b >= a.B) s.tiles = 0;
+    return s;
   };
-  const int least = over_requests([](const Share& s) { return s.tiles; }) * a.Hkv;
-  const int budget = max((least + plan.slots - 1) / plan.slots, 1) * plan.slots;   // at most plan.groups
-  // (a first guess in binary32, the same in every wave; the count that it is held to is exact)
-  const float work = over_requests([](const Share& s) { return static_cast<float>(s.tiles) * static_cast<float>(s.len); }) * a.Hkv;
+  const Share own = share(lane);
+  const auto each_request = [&](auto&& f) {          // (four at a time: their loads wait for each other's no longer)
+    f(own);
+    for (int b = 64; b < a.B; b += 256) {
+      const Share s[4] = {share(b + lane), share(b + 64 + lane), share(b + 128 + lane), share(b + 192 + lane)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f(s[k]);
+    }
+  };
+  int least = 0;
+  float work = 0.0f;                                 // (a first guess in binary32, the same in every wave; the count that it is held to is exact)
+  each_request([&](const Share& s) {
+    least += s.tiles;
+    work += static_cast<float>(s.tiles) * static_cast<float>(s.len);
+  });
+  least = last_lane(scan64(least)) * a.Hkv;
+  work = last_lane(scan64(work)) * a.Hkv;
+  const int budget = static_cast<int>(runs_of(least, plan.slots));   // at most plan.groups
   constexpr float kMost = 0x1p30f;
-  float guess = work / budget;
-  int chunk, n;
+  float guess = work / plan.slots;
+  int chunk, n, cut;
   for (int round = 0;; ++round) {
     chunk = (static_cast<int>(fminf(guess, kMost - GRAIN)) / GRAIN + 1) * GRAIN;
-    n = over_requests([&](const Share& s) { return s.tiles * items_of(s.len, chunk); }) * a.Hkv;
+    n = cut = 0;
+    each_request([&](const Share& s) {
+      const int runs = items_of(s.len, chunk);
+      n += s.tiles * runs;
+      cut += runs > 1 ? s.tiles * runs : 0;
+    });
+    n = last_lane(scan64(n)) * a.Hkv;
     if (n <= budget || guess >= kMost) break;
     // as much longer as there are too many (twice, where that has not done for a while)
     guess = fmaxf(round < 6 ? chunk * (static_cast<float>(n) / budget) : 2.0f * chunk, chunk + GRAIN * 0.5f);
   }
-  const int per_die = (n + 7) / 8, at = static_cast<int>(id % 8) * per_die + static_cast<int>(id / 8);
-  if (static_cast<int>(id / 8) >= per_die || at >= n) return Spot{-1};
-  for (int b0 = 0, before = 0; b0 < a.B; b0 += 64) {
-    const Share s = b0 == 0 ? own : b0 + lane < a.B ? share_of(a, plan, b0 + lane) : Share{};
-    const int runs = items_of(s.len, chunk), mine = s.tiles * runs * a.Hkv, incl = scan64(mine), first = before + incl - mine;
+  const unsigned deal = dealt(plan.tiles), turn = id / 8;
+  const int at = static_cast<int>((turn / deal * 8 + id % 8) * deal + turn % deal);
+  if (at >= n) return Spot{-1};
+  const bool cut_first = n > plan.slots;
+  cut = cut_first ? last_lane(scan64(cut)) * a.Hkv : 0;
+  Share next = own;
+  for (int b0 = 0, before[2] = {cut, 0}; b0 < a.B; b0 += 64) {
+    const Share s = next;
+    if (b0 + 64 < a.B) next = share(b0 + 64 + lane);
+    const int runs = items_of(s.len, chunk), mine = s.tiles * runs * a.Hkv;
+    const bool early = cut_first && runs > 1;
+    const int early_to = before[1] + scan64(early ? mine : 0), to = before[0] + scan64(early ? 0 : mine);
+    const int first = (early ? early_to : to) - mine;
     if (const uint64_t here = __ballot(at >= first && at < first + mine); here != 0) {
       const int l = __builtin_ctzll(here);
       const auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
@@ -114,7 +149,8 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
       if (local == 0 && __builtin_amdgcn_workitem_id_x() == 0) Parts<D>(a, plan).info[b0 + l] = make_int2(first_l, splits);
       return Spot{b0 + l, unit % a.Hkv, local % tiles, unit / a.Hkv, splits, at, Drafts{of(s.dr.first), of(s.dr.n), of(s.dr.base)}, of(s.len)};
     }
-    before += last_lane(incl);
+    before[0] = last_lane(to);
+    before[1] = last_lane(early_to);
   }
   return Spot{-1};
 }
@@ -178,8 +214,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
   reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack_bf16(acc.x * back, acc.y * back), pack_bf16(acc.z * back, acc.w * back));
 }
 
-// Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where they alone
-// fill the chip four times over.
+// Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where there are more
+// than kManyRequests, which alone fill the chip four times over.
+constexpr int kManyRequests = 512;
+
 inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int whole) {
   const int64_t all = int64_t(z.max_new) * (z.Hq / z.Hkv), rows = int64_t(1) << rows_log2;
   TokenPlan p;
@@ -188,8 +226,8 @@ inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int wh
   p.heads = static_cast<int>(std::min<int64_t>(all, rows));
   p.slots = slots;
   const int64_t most = int64_t(z.B) * z.Hkv * p.tiles;
-  p.whole = z.max_len <= whole || most >= 4 * slots;
-  const int64_t groups = !p.whole ? (most + slots - 1) / slots * slots : p.tiles * z.Hkv == 1 ? most : (most + 7) / 8 * 8;
+  p.whole = z.max_len <= whole || (most >= 4 * slots && z.B > kManyRequests);
+  const int64_t deal = 8 * dealt(p.tiles), groups = !p.whole ? (runs_of(most, slots) + deal - 1) / deal * deal : p.tiles * z.Hkv == 1 ? most : (most + 7) / 8 * 8;
   p.groups = static_cast<int>(std::min<int64_t>(groups, 0x7fffffff));
   return p;
 }

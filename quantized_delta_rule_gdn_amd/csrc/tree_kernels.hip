@@ -526,7 +526,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(cons
 
 // How a call's rows are taken (us, call included).
 // - Up to 16 rows a key-value head: by kv_tree_kernel. A request of 500 tokens takes 10 and by the wide one 13;
-//   48 of 2,000, 8 heads of d = 128, take 80 and 84. With 32 rows these take 86 and 76.
+//   48 of 2,000, 8 heads of d = 128, take 80 and 84. With 32 rows these take 86 and 73.
 // - Else in tiles of 64 rows through LDS, or of 128 where there are enough of them: one request of 300 tokens with
 //   128 rows and 2 heads takes 10.1 in tiles of 64 and 13.3 in one of 128, 4 of 20,000 with 4 heads 33 and
 //   38; 8 of 30,000 with 4 heads 64 and 59, 48 of 2,000 with 8 heads 126 and 119.
