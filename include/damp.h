@@ -655,7 +655,7 @@ damp_status kv_copy_pages(const int32_t* src, const int32_t* dst, const int32_t*
  *             the j-th of those positions. A list that does not ascend leaves unspecified rows
  *             (inside the request's pages); an entry past the new tokens moves nothing.
  *   out_lens  dev int32 [B] (output): seq_lens[b] - new_lens[b] + the number kept (keep_lens of
- *             kv_free_pages). It must not be seq_lens or new_lens.
+ *             kv_free_pages); none of the other arrays
  * The pages that tokens move in must be the request's alone. Called once per layer. */
 damp_status kv_compact(const int32_t* kept, const int32_t* cu_kept, int32_t num_kept,
                        const int32_t* seq_lens, const int32_t* new_lens, int32_t B,

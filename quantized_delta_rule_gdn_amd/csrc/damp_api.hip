@@ -510,6 +510,12 @@ damp_status check_cache(int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_
 
 constexpr double kLog2E = 1.4426950408889634;
 
+// Two int32 arrays share memory.
+bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + static_cast<uintptr_t>(nq) * 4 && b < a + static_cast<uintptr_t>(np) * 4;
+}
+
 // Pages of any row that is whole 16-byte pieces, for the calls that only move rows.
 damp_status check_rows(int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_size) {
   if (d < 8 || d % 8 || d > 2048)
@@ -1437,6 +1443,8 @@ damp_status kv_compact(const int32_t* kept, const int32_t* cu_kept, int32_t num_
   if (!aligned(kept, 4) || !aligned(cu_kept, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) || !aligned(out_lens, 4) ||
       !aligned(k_pages, 16) || !aligned(v_pages, 16))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "the pages must be 16-byte, the other arrays 4-byte aligned");
+  if (overlap(out_lens, B, seq_lens, B) || overlap(out_lens, B, new_lens, B) || overlap(out_lens, B, cu_kept, int64_t(B) + 1) || overlap(out_lens, B, kept, num_kept))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "out_lens overlaps seq_lens, new_lens, cu_kept or kept");
   if (static_cast<int64_t>(B) * num_kv_heads > kMaxGroups / 2)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "B * num_kv_heads = %lld exceeds the grid limit", static_cast<long long>(B) * num_kv_heads);
   damp::CompactArgs a{};
@@ -1469,6 +1477,8 @@ damp_status kv_free_pages(const int32_t* keep_lens, const int32_t* seq_lens, int
     return fail(DAMP_ERR_INVALID_ARGUMENT, "NULL device pointer among seq_lens/block_table/shares/freed/num_freed");
   if (!aligned(keep_lens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(shares, 4) || !aligned(freed, 4) || !aligned(num_freed, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned pointer (need natural alignment)");
+  if (overlap(freed, num_pages, shares, num_pages) || overlap(num_freed, 1, shares, num_pages) || overlap(num_freed, 1, freed, num_pages))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "shares, freed and num_freed overlap");
   if (B > kMaxGroups) return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d exceeds the grid limit", B);
   st = check_workspace(workspace, workspace_bytes, damp::kv_free_ws_bytes(num_pages));
   if (st != DAMP_OK) return st;

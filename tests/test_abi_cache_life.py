@@ -9,6 +9,7 @@ from quantized_delta_rule_gdn_amd import lib
 
 OK, BAD, UNSUP = lib.DAMP_OK, lib.DAMP_ERR_INVALID_ARGUMENT, lib.DAMP_ERR_UNSUPPORTED
 X = 0x100000   # never dereferenced: every case is settled on the host
+Y, Z = X + 2 ** 26, X + 2 ** 27
 
 
 def _call(name, base, **change):
@@ -46,27 +47,29 @@ def test_copy_refusals(change, status, text):
     assert _call("kv_copy_pages", COPY, n=0, src=None, k=None) == OK
 
 
-KEEP = dict(kept=X, cu=X, num=5, lens=X, new=X, B=2, table=X, blocks=4, k=X, v=None, pages=9, H=2, page=16, d=64, out=X, stream=None)
+KEEP = dict(kept=X, cu=X, num=5, lens=X, new=X, B=2, table=X, blocks=4, k=X, v=None, pages=9, H=2, page=16, d=64, out=Y, stream=None)
 
 
 @pytest.mark.parametrize("change,status,text", [
     (dict(num=-1), BAD, "num_kept"), (dict(num=2 ** 30 + 1), BAD, "num_kept"), (dict(B=-1), BAD, "B"), (dict(blocks=-1), BAD, "max_blocks"), (dict(d=4), UNSUP, "multiples of 8"),
     (dict(H=-1), BAD, "positive"), (dict(page=0), UNSUP, "power of two"), *[(dict([(k, None)]), BAD, "NULL") for k in ("kept", "cu", "lens", "new", "table", "k", "out")],
     *[(dict([(k, X + 2)]), BAD, "4-byte") for k in ("kept", "cu", "lens", "new", "table", "out")], (dict(k=X + 8), BAD, "16-byte"), (dict(v=X + 4), BAD, "16-byte"),
-    (dict(B=2 ** 24, H=2), BAD, "grid limit")])
+    (dict(B=2 ** 24, H=2, out=X + 2 ** 30), BAD, "grid limit"), (dict(out=X), BAD, "overlaps"), (dict(out=X + 4), BAD, "overlaps"), (dict(out=X - 4), BAD, "overlaps"),
+    (dict(lens=Z, new=Z, cu=Z, out=X + 16), BAD, "overlaps")])
 def test_keep_refusals(change, status, text):
     _refused("kv_compact", KEEP, change, status, text)
     assert _call("kv_compact", KEEP, B=0, cu=None, lens=None) == OK
 
 
-FREE = dict(keep=None, lens=X, B=2, table=X, blocks=4, shares=X, pages=70000, page=16, freed=X, count=X, ws=X, wsn=1 << 40, stream=None)
+FREE = dict(keep=None, lens=X, B=2, table=X, blocks=4, shares=X, pages=70000, page=16, freed=Y, count=Z, ws=X, wsn=1 << 40, stream=None)
 
 
 @pytest.mark.parametrize("change,status,text", [
     (dict(B=-1), BAD, "B"), (dict(blocks=-1), BAD, "max_blocks"), (dict(pages=0), BAD, "num_pages"), (dict(page=6), UNSUP, "power of two"),
     *[(dict([(k, None)]), BAD, "NULL") for k in ("lens", "table", "shares", "freed", "count")],
     *[(dict([(k, X + 2)]), BAD, "misaligned") for k in ("keep", "lens", "table", "shares", "freed", "count")],
-    (dict(B=2 ** 24), BAD, "grid limit"), (dict(ws=None), BAD, "workspace"), (dict(ws=X + 8), BAD, "workspace"), (dict(wsn=16), BAD, "workspace")])
+    (dict(B=2 ** 24), BAD, "grid limit"), (dict(ws=None), BAD, "workspace"), (dict(ws=X + 8), BAD, "workspace"), (dict(wsn=16), BAD, "workspace"), (dict(freed=X + 4 * 69999), BAD, "overlap"),
+    (dict(count=X + 400), BAD, "overlap"), (dict(count=Y), BAD, "overlap")])
 def test_free_refusals(change, status, text):
     _refused("kv_free_pages", FREE, change, status, text)
 

@@ -15,7 +15,8 @@ pytestmark = [pytest.mark.gpu,
 
 import cache_ref as ref  # noqa: E402
 from quantized_delta_rule_gdn_amd import lib  # noqa: E402
-from test_gpu_tree import _i32, build, random_bits, weight  # noqa: E402
+from test_gpu_latent import _absorbed  # noqa: E402
+from test_gpu_tree import _attend, _i32, build, random_bits, weight  # noqa: E402
 
 
 class Server:
@@ -406,3 +407,31 @@ def test_one_page_twice_and_one_for_all():
     for b in range(2):
         o, mag, e = ref.attend(q[3 * b:3 * b + 3].double(), k[b].double(), v[b].double(), ref.seen(3, 64), 0.125)
         ref.is_close(out[3 * b:3 * b + 3], o, ref.tolerance(o, mag, e, 64, weight(12)), f"request {b}")
+
+
+def _ragged(B, long, at, most, seed):
+    rng = np.random.default_rng(seed)
+    lens = [int(x) for x in rng.integers(0, 180, B)]
+    lens[at % B] = long
+    return lens, [int(min(x, y)) for x, y in zip(lens, rng.integers(0, most + 1, B))]
+
+
+@pytest.mark.parametrize("at", [0, 77, -1])
+@pytest.mark.parametrize("B,long,most,Hq,Hkv", [(64, 3001, 2, 4, 2), (65, 2000, 20, 8, 1), (300, 4000, 3, 2, 1), (130, 3500, 40, 4, 1), (512, 2500, 2, 4, 4), (520, 1500, 2, 4, 4)])
+def test_one_long_request_among_many(at, B, long, most, Hq, Hkv):
+    """Few units and many, one row tile and several, more requests than are cut: every run is taken once."""
+    lens, new = _ragged(B, long, at, most, B + most)
+    _attend(lens, new, Hq, Hkv, 64, 16, "tree" if most <= 3 else None, max_new=most)
+
+
+@pytest.mark.parametrize("at", [0, -1])
+@pytest.mark.parametrize("B,long,most,H", [(40, 3000, 2, 4), (150, 2500, 3, 40), (300, 2000, 1, 16), (257, 2000, 1, 33)])
+def test_one_long_latent_request_among_many(at, B, long, most, H):
+    lens, new = _ragged(B, long, at, most, B + H)
+    _absorbed(lens, new, H, 256, 16, None)
+
+
+def test_more_row_tiles_than_are_dealt_at_a_time():
+    _attend([2600, 40], [290, 7], 8, 1, 64, 16, None)              # 37 tiles of 64 rows, 19 of 128
+    _attend([1300] * 3, [150, 3, 150], 16, 1, 64, 16, None)
+    _absorbed([1500, 30], [20, 3], 64, 256, 16, None)
