@@ -155,11 +155,11 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
   return Spot{-1};
 }
 
-// The runs of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels a
-// thread, 1,024 / D rows a workgroup, eight runs at a time. Bound by the stream of the parts.
-template <int D>
+// The runs of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels of K rows a
+// thread, K 1,024 / D rows a workgroup, U runs at a time. Bound by the launch and by dependent loads.
+template <int D, int K, int U>
 __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const TokenPlan plan, int groups) {
-  constexpr int LPR = D / 4, RPG = 256 / LPR, U = 8;   // threads a row, rows a workgroup
+  constexpr int LPR = D / 4, RPG = 256 / LPR;      // threads a row, rows at once
   const int tid = __builtin_amdgcn_workitem_id_x();
   const unsigned id = __builtin_amdgcn_workgroup_id_x();
   const int units = a.Hkv * plan.tiles;
@@ -168,50 +168,64 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
   const Parts<D> parts(a, plan);
   const int2 info = parts.info[b];                 // (not written where a request has no rows: not used either)
   const Drafts dr = drafts_of(a, b);
-  const int rows = min(dr.n, a.max_new) * G, tile0 = tile << plan.rows_log2;
-  if (tile0 + group * RPG >= rows || info.y == 1) return;   // (one run: it has its readout already)
-  const int in_tile = group * RPG + tid / LPR, row = tile0 + in_tile;
-  if (in_tile >= plan.heads || row >= rows) return;
-  const int tiles = (rows + (1 << plan.rows_log2) - 1) >> plan.rows_log2;
+  const int rows = min(min(dr.n, a.max_new) * G - (tile << plan.rows_log2), plan.heads);    // of this tile
+  if (group * (K * RPG) >= rows || info.y == 1) return;     // (one run: it has its readout already)
+  const int tiles = (min(dr.n, a.max_new) * G + (1 << plan.rows_log2) - 1) >> plan.rows_log2;
   const int64_t step = int64_t(a.Hkv) * tiles * plan.heads;      // between a tile's runs
-  const int64_t first = (int64_t(info.x) + kvh * tiles + tile) * plan.heads + in_tile;
-  const float4* po = reinterpret_cast<const float4*>(parts.o + first * D) + tid % LPR;
-  const float2* ml = parts.ml + first;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float m = -INFINITY, l = 0.0f;
+  const int64_t first = (int64_t(info.x) + kvh * tiles + tile) * plan.heads;
+  int in_tile[K];
+  float4 acc[K];
+  float m[K], l[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    in_tile[k] = group * (K * RPG) + k * RPG + tid / LPR;
+    acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    m[k] = -INFINITY;
+    l[k] = 0.0f;
+  }
   for (int s0 = 0; s0 < info.y; s0 += U) {
-    float2 x[U];
-    float4 v[U];
+    float2 x[K][U];
+    float4 v[K][U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int s = min(s0 + i, info.y - 1);
-      x[i] = ml[s * step];
-      v[i] = po[s * step * LPR];
-    }
-    float top = m;
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (s0 + i >= info.y) x[i] = make_float2(-INFINITY, 0.0f);
-      top = fmaxf(top, x[i].x);
-    }
-    const float base = top == -INFINITY ? 0.0f : top, shrink = pow2(m - base);
-    m = top;
-    l *= shrink;
-    acc.x *= shrink; acc.y *= shrink; acc.z *= shrink; acc.w *= shrink;
+      for (int i = 0; i < U; ++i) {
+        const int64_t at = first + min(in_tile[k], rows - 1) + min(s0 + i, info.y - 1) * step;
+        x[k][i] = parts.ml[at];
+        v[k][i] = reinterpret_cast<const float4*>(parts.o + at * D)[tid % LPR];
+      }
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      if (s0 + i >= info.y) break;                 // (its values stand in for none)
-      const float f = pow2(x[i].x - base);
-      l = fmaf(f, x[i].y, l);
-      acc.x = fmaf(f, v[i].x, acc.x);
-      acc.y = fmaf(f, v[i].y, acc.y);
-      acc.z = fmaf(f, v[i].z, acc.z);
-      acc.w = fmaf(f, v[i].w, acc.w);
+    for (int k = 0; k < K; ++k) {
+      float top = m[k];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (s0 + i >= info.y) x[k][i] = make_float2(-INFINITY, 0.0f);
+        top = fmaxf(top, x[k][i].x);
+      }
+      const float base = top == -INFINITY ? 0.0f : top, shrink = pow2(m[k] - base);
+      m[k] = top;
+      l[k] *= shrink;
+      acc[k].x *= shrink; acc[k].y *= shrink; acc[k].z *= shrink; acc[k].w *= shrink;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (s0 + i >= info.y) break;               // (its values stand in for none)
+        const float f = pow2(x[k][i].x - base);
+        l[k] = fmaf(f, x[k][i].y, l[k]);
+        acc[k].x = fmaf(f, v[k][i].x, acc[k].x);
+        acc[k].y = fmaf(f, v[k][i].y, acc[k].y);
+        acc[k].z = fmaf(f, v[k][i].z, acc[k].z);
+        acc[k].w = fmaf(f, v[k][i].w, acc[k].w);
+      }
     }
   }
-  const float back = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * LPR + tid % LPR;
-  reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack_bf16(acc.x * back, acc.y * back), pack_bf16(acc.z * back, acc.w * back));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (in_tile[k] >= rows) continue;
+    const int row = (tile << plan.rows_log2) + in_tile[k];
+    const float back = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+    const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * LPR + tid % LPR;
+    reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack_bf16(acc[k].x * back, acc[k].y * back), pack_bf16(acc[k].z * back, acc[k].w * back));
+  }
 }
 
 // Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where there are more
@@ -232,20 +246,22 @@ inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int wh
   return p;
 }
 
-// Workgroups that a (request, head, row tile) takes to join.
-inline int64_t join_groups(const TokenPlan& p, int d) { return (p.heads + 1024 / d - 1) / (1024 / d); }
+// Workgroups that a (request, head, row tile) takes to join, with k rows a thread.
+inline int64_t join_groups(const TokenPlan& p, int d, int k) { return (p.heads + k * 1024 / d - 1) / (k * 1024 / d); }
 
 // Workgroups of the larger launch.
 inline int64_t token_groups(const TokenPlan& p, const TreeSizes& z, int d) {
-  return p.whole ? p.groups : std::max<int64_t>(p.groups, int64_t(z.B) * z.Hkv * p.tiles * join_groups(p, d));
+  return p.whole ? p.groups : std::max<int64_t>(p.groups, int64_t(z.B) * z.Hkv * p.tiles * join_groups(p, d, 1));
 }
 
+// Two rows a thread where one each would not fit the chip at once (6,144 workgroups, most without work: 14 us with
+// one, 7.5 with two), else more runs at a time (48 runs: 11.7 us eight at a time, 13.7 by two rows and four).
 template <int D>
 void launch_join(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
   if (p.whole) return;
-  const int64_t groups = join_groups(p, D);
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(static_cast<unsigned>(int64_t(a.B) * a.Hkv * p.tiles * groups)), dim3(256), 0, s, a, p,
-                     static_cast<int>(groups));
+  const int64_t units = int64_t(a.B) * a.Hkv * p.tiles, one = join_groups(p, D, 1), two = join_groups(p, D, 2);
+  if (units * one > 2048) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4>), dim3(static_cast<unsigned>(units * two)), dim3(256), 0, s, a, p, static_cast<int>(two));
+  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8>), dim3(static_cast<unsigned>(units * one)), dim3(256), 0, s, a, p, static_cast<int>(one));
 }
 
 }  // namespace
