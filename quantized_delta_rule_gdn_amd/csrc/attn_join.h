@@ -156,11 +156,13 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
 }
 
 // The runs of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels of K rows a
-// thread, K 1,024 / D rows a workgroup, U runs at a time. Bound by the launch and by dependent loads.
-template <int D, int K, int U>
+// thread, U runs at a time; S threads share out the runs of a row, and meet in LDS. K 1,024 / (D S) rows a
+// workgroup. Bound by the launch and by dependent loads.
+template <int D, int K, int U, int S>
 __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const TokenPlan plan, int groups) {
-  constexpr int LPR = D / 4, RPG = 256 / LPR;      // threads a row, rows at once
-  const int tid = __builtin_amdgcn_workitem_id_x();
+  constexpr int LPR = D / 4, RPG = 256 / LPR / S;  // threads for a row's channels, rows at once
+  static_assert(S == 1 || K == 1);
+  const int tid = __builtin_amdgcn_workitem_id_x(), seg = tid / (256 / S), lane = tid % (256 / S);
   const unsigned id = __builtin_amdgcn_workgroup_id_x();
   const int units = a.Hkv * plan.tiles;
   const int group = static_cast<int>(id % groups), unit = static_cast<int>(id / groups % units), b = static_cast<int>(id / groups / units);
@@ -178,28 +180,28 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
   float m[K], l[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    in_tile[k] = group * (K * RPG) + k * RPG + tid / LPR;
+    in_tile[k] = group * (K * RPG) + k * RPG + lane / LPR;
     acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     m[k] = -INFINITY;
     l[k] = 0.0f;
   }
-  for (int s0 = 0; s0 < info.y; s0 += U) {
+  for (int s0 = seg; s0 < info.y; s0 += U * S) {
     float2 x[K][U];
     float4 v[K][U];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int64_t at = first + min(in_tile[k], rows - 1) + min(s0 + i, info.y - 1) * step;
+        const int64_t at = first + min(in_tile[k], rows - 1) + min(s0 + i * S, info.y - 1) * step;
         x[k][i] = parts.ml[at];
-        v[k][i] = reinterpret_cast<const float4*>(parts.o + at * D)[tid % LPR];
+        v[k][i] = reinterpret_cast<const float4*>(parts.o + at * D)[lane % LPR];
       }
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float top = m[k];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (s0 + i >= info.y) x[k][i] = make_float2(-INFINITY, 0.0f);
+        if (s0 + i * S >= info.y) x[k][i] = make_float2(-INFINITY, 0.0f);
         top = fmaxf(top, x[k][i].x);
       }
       const float base = top == -INFINITY ? 0.0f : top, shrink = pow2(m[k] - base);
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
       acc[k].x *= shrink; acc[k].y *= shrink; acc[k].z *= shrink; acc[k].w *= shrink;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        if (s0 + i >= info.y) break;               // (its values stand in for none)
+        if (s0 + i * S >= info.y) break;               // (its values stand in for none)
         const float f = pow2(x[k][i].x - base);
         l[k] = fmaf(f, x[k][i].y, l[k]);
         acc[k].x = fmaf(f, v[k][i].x, acc[k].x);
@@ -218,12 +220,36 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
       }
     }
   }
+  if constexpr (S > 1) {
+    __shared__ float4 part_o[S][256 / S];
+    __shared__ float2 part_ml[S][256 / S];
+    part_o[seg][lane] = acc[0];
+    part_ml[seg][lane] = make_float2(m[0], l[0]);
+    __syncthreads();
+    if (seg > 0) return;
+    float top = m[0];
+#pragma unroll
+    for (int i = 1; i < S; ++i) top = fmaxf(top, part_ml[i][lane].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    acc[0] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    l[0] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const float f = pow2(part_ml[i][lane].x - base);
+      const float4 v = part_o[i][lane];
+      l[0] = fmaf(f, part_ml[i][lane].y, l[0]);
+      acc[0].x = fmaf(f, v.x, acc[0].x);
+      acc[0].y = fmaf(f, v.y, acc[0].y);
+      acc[0].z = fmaf(f, v.z, acc[0].z);
+      acc[0].w = fmaf(f, v.w, acc[0].w);
+    }
+  }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (in_tile[k] >= rows) continue;
     const int row = (tile << plan.rows_log2) + in_tile[k];
     const float back = l[k] == 0.0f ? 0.0f : 1.0f / l[k];
-    const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * LPR + tid % LPR;
+    const int64_t at = (int64_t(dr.first + row / G) * a.Hq + kvh * G + row % G) * LPR + lane % LPR;
     reinterpret_cast<uint2*>(a.out)[at] = make_uint2(pack_bf16(acc[k].x * back, acc[k].y * back), pack_bf16(acc[k].z * back, acc[k].w * back));
   }
 }
@@ -246,22 +272,26 @@ inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int wh
   return p;
 }
 
-// Workgroups that a (request, head, row tile) takes to join, with k rows a thread.
-inline int64_t join_groups(const TokenPlan& p, int d, int k) { return (p.heads + k * 1024 / d - 1) / (k * 1024 / d); }
+// Workgroups that a (request, head, row tile) takes to join, with so many rows each.
+inline int64_t join_groups(const TokenPlan& p, int rows) { return (p.heads + rows - 1) / rows; }
+
+inline constexpr int join_shares(int d) { return d == 512 ? 2 : 4; }   // (a workgroup holds a row of each share)
 
 // Workgroups of the larger launch.
 inline int64_t token_groups(const TokenPlan& p, const TreeSizes& z, int d) {
-  return p.whole ? p.groups : std::max<int64_t>(p.groups, int64_t(z.B) * z.Hkv * p.tiles * join_groups(p, d, 1));
+  return p.whole ? p.groups : std::max<int64_t>(p.groups, int64_t(z.B) * z.Hkv * p.tiles * join_groups(p, 1024 / d / join_shares(d)));
 }
 
 // Two rows a thread where one each would not fit the chip at once (6,144 workgroups, most without work: 14 us with
-// one, 7.5 with two), else more runs at a time (48 runs: 11.7 us eight at a time, 13.7 by two rows and four).
+// one, 7.5 with two), else the runs shared out (48 runs of 512 rows: 11.7 us by one thread a piece, 8.0 by four; 13
+// runs of 64 rows 7.1 and 4.6).
 template <int D>
 void launch_join(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
   if (p.whole) return;
-  const int64_t units = int64_t(a.B) * a.Hkv * p.tiles, one = join_groups(p, D, 1), two = join_groups(p, D, 2);
-  if (units * one > 2048) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4>), dim3(static_cast<unsigned>(units * two)), dim3(256), 0, s, a, p, static_cast<int>(two));
-  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8>), dim3(static_cast<unsigned>(units * one)), dim3(256), 0, s, a, p, static_cast<int>(one));
+  constexpr int S = join_shares(D), FEW = 1024 / D / S, MANY = 2 * 1024 / D;
+  const int64_t units = int64_t(a.B) * a.Hkv * p.tiles, few = join_groups(p, FEW), many = join_groups(p, MANY);
+  if (units * few > 2048) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4, 1>), dim3(static_cast<unsigned>(units * many)), dim3(256), 0, s, a, p, static_cast<int>(many));
+  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8, S>), dim3(static_cast<unsigned>(units * few)), dim3(256), 0, s, a, p, static_cast<int>(few));
 }
 
 }  // namespace

@@ -257,7 +257,7 @@ __global__ __launch_bounds__(256, 3) void kv_tree_kernel(const TreeArgs a, const
 // loaded ahead). 48 requests of up to 4,096 tokens, 128 rows, 8 heads of d = 128: 97 us and 8 for the join,
 // which is 4.4 TB/s; the matrix cores are busy for a fifth of the time, the waves wait for the stream (a third
 // tile on its way did not help: 119 us with it, 114 without). 4 requests of up to 65,536 tokens, 512 rows
-// of d = 64: 85 us and 11, 660 TFLOP/s; matrix cores busy 37%, vector unit 55%: for 16 x 16 scores the products take
+// of d = 64: 85 us and 8, 660 TFLOP/s; matrix cores busy 37%, vector unit 55%: for 16 x 16 scores the products take
 // 72 cycles, the exponentials alone 64 and the rest of the softmax 40.
 constexpr int kWideTile = 64;
 

@@ -435,3 +435,32 @@ def test_more_row_tiles_than_are_dealt_at_a_time():
     _attend([2600, 40], [290, 7], 8, 1, 64, 16, None)              # 37 tiles of 64 rows, 19 of 128
     _attend([1300] * 3, [150, 3, 150], 16, 1, 64, 16, None)
     _absorbed([1500, 30], [20, 3], 64, 256, 16, None)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_key_that_is_not_finite_in_one_run(value):
+    """A cached key in one of many runs: the formula's NaN in every row, or a weight of 0, as binary64 has it."""
+    for most, Hq in ((1, 8), (6, 8), (20, 8)):
+        gen, kp, vp, table, keys = build([4000], [most], 1, 64, 16)
+        for t in (0, 1990, 2500):
+            kp[int(table[0, t // 16]), 0, t % 16, 3] = value
+            keys[0][0][t, 0, 3] = value
+        q = torch.randn((most, Hq, 64), generator=gen).bfloat16()
+        q[..., 3] = q[..., 3].abs() + 1.0
+        out = torch.zeros_like(q, device="cuda")
+        lib.kv_tree_attention(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), _i32([4000]), _i32([0, most]), out)
+        if value == float("-inf"):
+            live = ref.seen(most, 4000)
+            live[:, [0, 1990, 2500]] = False
+            k = torch.nan_to_num(keys[0][0].double(), neginf=0.0)
+            o, mag, e = ref.attend(q.double(), k, keys[0][1].double(), live, 0.125)
+            ref.is_close(out, o, ref.tolerance(o, mag, e, 4000, weight(most * Hq)), f"{most}")
+        else:
+            assert bool(torch.isnan(out).all())
+    for H in (4, 40):
+        gen, pages, _, table, _ = build([3000], [1], 1, 256, 16, latent=288)
+        for t in range(1984, 2048):
+            pages[int(table[0, t // 16]), t % 16, 260] = float("nan")
+        out = torch.zeros((1, H, 256), dtype=torch.bfloat16, device="cuda")
+        lib.kv_latent_attention(torch.randn((1, H, 288), generator=gen).bfloat16().cuda(), pages.cuda(), table.cuda(), _i32([3000]), out, 0.1)
+        assert bool(torch.isnan(out).all())
