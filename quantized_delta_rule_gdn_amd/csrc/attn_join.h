@@ -272,26 +272,36 @@ inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int wh
   return p;
 }
 
-// Workgroups that a (request, head, row tile) takes to join, with so many rows each.
-inline int64_t join_groups(const TokenPlan& p, int rows) { return (p.heads + rows - 1) / rows; }
+// The launch that joins. Two rows a thread where one each would not fit the chip at once (6,144 workgroups, most
+// without work: 14 us with one, 7.5 with two), else the runs shared out (48 runs of 512 rows: 11.7 us by one thread
+// a piece, 8.0 by four; 13 runs of 64 rows 7.1 and 4.6).
+constexpr int join_shares(int d) { return d == 512 ? 2 : 4; }   // (a workgroup holds a row of each share)
 
-inline constexpr int join_shares(int d) { return d == 512 ? 2 : 4; }   // (a workgroup holds a row of each share)
+struct JoinPlan {
+  bool many;
+  int per_unit;          // workgroups that a (request, head, row tile) takes
+  int64_t groups;
+};
+
+inline JoinPlan join_plan(const TokenPlan& p, int64_t B, int64_t Hkv, int d) {
+  const int few_rows = 1024 / d / join_shares(d), many_rows = 2 * 1024 / d;
+  const int64_t units = B * Hkv * p.tiles, few = (p.heads + few_rows - 1) / few_rows, many = (p.heads + many_rows - 1) / many_rows;
+  const bool is_many = units * few > 2048;
+  return JoinPlan{is_many, static_cast<int>(is_many ? many : few), units * (is_many ? many : few)};
+}
 
 // Workgroups of the larger launch.
 inline int64_t token_groups(const TokenPlan& p, const TreeSizes& z, int d) {
-  return p.whole ? p.groups : std::max<int64_t>(p.groups, int64_t(z.B) * z.Hkv * p.tiles * join_groups(p, 1024 / d / join_shares(d)));
+  return p.whole ? p.groups : std::max<int64_t>(p.groups, join_plan(p, z.B, z.Hkv, d).groups);
 }
 
-// Two rows a thread where one each would not fit the chip at once (6,144 workgroups, most without work: 14 us with
-// one, 7.5 with two), else the runs shared out (48 runs of 512 rows: 11.7 us by one thread a piece, 8.0 by four; 13
-// runs of 64 rows 7.1 and 4.6).
 template <int D>
 void launch_join(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
   if (p.whole) return;
-  constexpr int S = join_shares(D), FEW = 1024 / D / S, MANY = 2 * 1024 / D;
-  const int64_t units = int64_t(a.B) * a.Hkv * p.tiles, few = join_groups(p, FEW), many = join_groups(p, MANY);
-  if (units * few > 2048) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4, 1>), dim3(static_cast<unsigned>(units * many)), dim3(256), 0, s, a, p, static_cast<int>(many));
-  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8, S>), dim3(static_cast<unsigned>(units * few)), dim3(256), 0, s, a, p, static_cast<int>(few));
+  const JoinPlan j = join_plan(p, a.B, a.Hkv, D);
+  const dim3 grid(static_cast<unsigned>(j.groups));
+  if (j.many) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4, 1>), grid, dim3(256), 0, s, a, p, j.per_unit);
+  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8, join_shares(D)>), grid, dim3(256), 0, s, a, p, j.per_unit);
 }
 
 }  // namespace
