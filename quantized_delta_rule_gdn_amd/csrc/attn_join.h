@@ -27,7 +27,8 @@ struct TokenPlan {
   int whole;      // no request is cut
 };
 
-// Runs that units are cut into, at most.
+// Runs that units are cut into, at most. Few are up to three quarters of the workgroups that the chip holds (with half
+// instead, 384 units of 200 to 4,096 tokens on 512 took 122 us instead of 115, 138 of latents on 256 92 instead of 75).
 __host__ __device__ inline bool few_units(int64_t units, int slots) { return 4 * units <= 3 * int64_t(slots); }
 __host__ __device__ inline int64_t runs_of(int64_t units, int slots) { return few_units(units, slots) ? slots : units + slots / 2; }
 
@@ -255,7 +256,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
 }
 
 // Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where there are more
-// than kManyRequests, which alone fill the chip four times over.
+// than kManyRequests, which alone fill the chip four times over: each workgroup finding its part among 1,024 of 1,100
+// tokens, 8 heads of d = 64, takes 449 us, whole ones 385; but 756 and 1,000 where one of them has 60,000. Among 512
+// it costs nothing.
 constexpr int kManyRequests = 512;
 
 inline TokenPlan token_plan(const TreeSizes& z, int rows_log2, int slots, int whole) {
