@@ -15,9 +15,10 @@ namespace {
 // its cached tokens in runs; a workgroup takes one (run, key-value head, tile). The runs are cut on the
 // device, where the lengths are. Where the (request, head, row tile) units are few, by the least chunk with
 // which the workgroups are no more than the chip holds at once: one round of runs of much the same length. Where
-// they are many, only what is longer than a workgroup's fair share, as others fill the chip meanwhile. (Cutting costs the parts, a write and a read of 4 bytes a row and channel: 48 requests of 2,000 tokens
-// with 128 rows, 384 units, take 118 us in two rounds of runs and 90 whole. 256 requests of 1,500 tokens of which
-// one has 100,000, 2,048 units, take 1,450 us with none cut, 356 so.)
+// they are many, only what is longer than a workgroup's fair share, as others fill the chip meanwhile. (Cutting
+// costs the parts, a write and a read of 4 bytes a row and channel: 48 requests of 2,000 tokens with 128 rows,
+// 384 units, take 118 us in two rounds of runs and 90 whole. 256 requests of 1,500 tokens of which one has 100,000,
+// 2,048 units, take 1,450 us with none cut, 356 so.)
 struct TokenPlan {
   int rows_log2;  // query rows of a tile
   int heads;      // rows of the largest tile there is

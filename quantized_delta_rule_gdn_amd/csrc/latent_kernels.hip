@@ -32,10 +32,10 @@ constexpr int kLatTile = 64;
 
 // Up to 16 rows: the stream of the cache is what takes longest (64 requests, 266,000 tokens, 16 heads: 67 us and 6
 // for the join; 5.3 TB/s behind the first 8 us, in which lengths, pages and the first tiles are on their way;
-// the eight waves below take the same, and 17 instead of 16 us for one request of 700 tokens). The 4 waves share out the scores by tokens, meet
-// for the maximum of each row, hand the weights over through LDS, and share out the readout by channels, so
-// that a tile is read from LDS once (scores: as rows; readout: transposed on the way). The next tile is
-// on its way in registers meanwhile.
+// the eight waves below take the same, and 17 instead of 16 us for one request of 700 tokens). The 4 waves
+// share out the scores by tokens, meet for the maximum of each row, hand the weights over through LDS, and
+// share out the readout by channels, so that a tile is read from LDS once (scores: as rows; readout:
+// transposed on the way). The next tile is on its way in registers meanwhile.
 template <int DC>
 struct LatGeo {
   static constexpr int DR = DC / 8, W = DC + DR;     // channels of a row

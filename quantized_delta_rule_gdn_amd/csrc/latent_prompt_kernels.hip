@@ -309,7 +309,8 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void latent_prompt_kernel(con
 }
 
 // Row tiles there may be, whatever the lists hold. 128 rows where that gives a workgroup to every CU, else 64 (203
-// tokens of 4 prompts with 8 heads take 5.4 us with 64).
+// tokens of 4 prompts, 8 heads of d = 64, take 7.4 us with 128 and 5.5 with 64; 12,288 of 8, 16 heads of d = 128, 210
+// and 270).
 int64_t prompt_items(int64_t B, int64_t Tq, int rows) { return std::min(Tq, Tq / rows + B); }
 
 template <int D>
