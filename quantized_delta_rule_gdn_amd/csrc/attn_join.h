@@ -206,14 +206,14 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
         if (s0 + i * S >= info.y) x[k][i] = make_float2(-INFINITY, 0.0f);
         top = fmaxf(top, x[k][i].x);
       }
-      const float base = top == -INFINITY ? 0.0f : top, shrink = pow2(m[k] - base);
+      const float base = top == -INFINITY ? 0.0f : top, shrink = part_factor(m[k] - base);
       m[k] = top;
       l[k] *= shrink;
       acc[k].x *= shrink; acc[k].y *= shrink; acc[k].z *= shrink; acc[k].w *= shrink;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         if (s0 + i * S >= info.y) break;               // (its values stand in for none)
-        const float f = pow2(x[k][i].x - base);
+        const float f = part_factor(x[k][i].x - base);
         l[k] = fmaf(f, x[k][i].y, l[k]);
         acc[k].x = fmaf(f, v[k][i].x, acc[k].x);
         acc[k].y = fmaf(f, v[k][i].y, acc[k].y);
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
     l[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const float f = pow2(part_ml[i][lane].x - base);
+      const float f = part_factor(part_ml[i][lane].x - base);
       const float4 v = part_o[i][lane];
       l[0] = fmaf(f, part_ml[i][lane].y, l[0]);
       acc[0].x = fmaf(f, v.x, acc[0].x);

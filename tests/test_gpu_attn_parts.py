@@ -1,0 +1,62 @@
+"""Attention of several new tokens where its parts meet: the waves of a workgroup, and the runs of a request that
+was cut. References: cache_ref in 64 bits, bounds cache_ref.tolerance."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+import cache_ref as ref  # noqa: E402
+from quantized_delta_rule_gdn_amd import lib  # noqa: E402
+from test_gpu_tree import _i32, build, weight  # noqa: E402
+
+LOW = -17.5     # a key's channel that puts a token's score 140 below the others' (a weight of 2^-202)
+
+
+def _one_value(lens, most, Hq, Hkv, d, value, low=range(0), missing=0, page=16):
+    """Request 0's last token holds `value` in channel 7, its tokens `low` score far below the others, and its first
+    `missing` pages do not exist. Every new token of every request against the formula."""
+    new = [min(most, n) for n in lens]
+    gen, kp, vp, table, keys = build(lens, new, Hkv, d, page)
+    for b, (k, v) in enumerate(keys):
+        k[:] = (k.float() / 64).bfloat16()
+        k[..., 5] = 0.0
+        if b == 0:
+            k[list(low), :, 5] = LOW
+            v[-1, :, 7] = value
+        pos = torch.arange(lens[b])
+        p = table[b, pos // page].long()
+        kp[p, :, pos % page], vp[p, :, pos % page] = k, v
+    table[0, :missing] = -1
+    T, cu = sum(new), [sum(new[:b]) for b in range(len(new) + 1)]
+    q = torch.randn((T, Hq, d), generator=gen).bfloat16()
+    q[..., 5] = 8.0
+    out = torch.full_like(q, 7.0, device="cuda")
+    lib.kv_tree_attention(q.cuda(), kp.cuda(), vp.cuda(), table.cuda(), _i32(lens), _i32(cu), out, max_new=most, scale=1.0)
+    for b, n in enumerate(new):
+        there = torch.arange(lens[b]) >= (missing * page if b == 0 else 0)
+        k, v = (x[there].double() for x in keys[b])
+        o, mag, e = ref.attend(q[cu[b]:cu[b + 1]].double(), k, v, ref.seen(n, lens[b])[:, there], 1.0)
+        ref.is_close(out[cu[b]:cu[b + 1]], o, ref.tolerance(o, mag, e, lens[b], weight(most * Hq // Hkv)), f"request {b}")
+
+
+VALUES = pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+
+
+@VALUES
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("most,Hq,Hkv", [(1, 1, 1), (1, 8, 2), (5, 6, 2), (12, 4, 2)])
+def test_a_value_that_one_wave_took_out(value, d, most, Hq, Hkv):
+    """An infinite value of a new token comes back as it is where the first tiles' tokens do not exist, or weigh nothing beside it."""
+    _one_value([60], most, Hq, Hkv, d, value, missing=2)
+    _one_value([60], most, Hq, Hkv, d, value, low=range(32))
+    _one_value([150, 40], most, Hq, Hkv, d, value, low=[t for t in range(150) if t // 32 % 4 == 0])
+
+
+@VALUES
+@pytest.mark.parametrize("lens,most,Hq,Hkv,d", [([4000], 1, 8, 2, 64), ([4000], 12, 4, 4, 128), ([4000], 30, 4, 2, 64), ([4000, 7], 20, 8, 2, 128), ([4000] + [9] * 39, 8, 32, 4, 64)])
+def test_a_value_in_a_run_that_weighs_nothing(value, lens, most, Hq, Hkv, d):
+    """A run of the last tokens scores far below the others, so that its readouts count next to nothing; an infinity among them still does."""
+    _one_value(lens, most, Hq, Hkv, d, value, low=range(2100, 4000))
+    _one_value(lens, most, Hq, Hkv, d, value, low=range(0, 2000))
