@@ -40,7 +40,7 @@ __host__ __device__ inline int dealt(int tiles) { return tiles < 16 ? tiles : 16
 struct Spot {
   int b, kvh, tile;
   int split, splits;     // its part of the request's tokens
-  int at;                // its place in the workspace
+  int at;                // its place in the list of parts; of one that is cut, in the workspace too
   Drafts dr;
   int len;               // tokens of the request
 };
@@ -59,14 +59,17 @@ __device__ __forceinline__ Share share_of(const TreeArgs& a, const TokenPlan& pl
 }
 
 // What the workgroups leave in the workspace: a tile's partial readouts, {maximum, sum} of its rows, and
-// each request's {first place, runs}.
+// each request's {first place, runs}. Only parts of requests that are cut are written, and they lie in the first
+// `slots` places however many units there are: a list of no more parts than that needs no more, and in a longer
+// one requests that are cut come first. That list has units + slots / 2 parts at most, so units that are cut into
+// r >= 2 runs each add r - 1 >= r / 2 parts to it, slots / 2 in all, and have slots at most.
 template <int D>
 struct Parts {
   float* o;
   float2* ml;
   int2* info;
   __device__ Parts(const TreeArgs& a, const TokenPlan& plan) {
-    const int64_t n = int64_t(plan.groups) * plan.heads;
+    const int64_t n = int64_t(plan.slots) * plan.heads;
     o = a.ws;
     ml = reinterpret_cast<float2*>(a.ws + n * D);
     info = reinterpret_cast<int2*>(ml + n);
@@ -74,7 +77,7 @@ struct Parts {
 };
 
 inline size_t parts_bytes(const TokenPlan& p, const TreeSizes& z, int32_t d) {
-  return p.whole ? 0 : static_cast<size_t>(p.groups) * p.heads * (static_cast<size_t>(d) + 2) * 4 + static_cast<size_t>(z.B) * 8;
+  return p.whole ? 0 : static_cast<size_t>(p.slots) * p.heads * (static_cast<size_t>(d) + 2) * 4 + static_cast<size_t>(z.B) * 8;
 }
 
 // Every wave finds its workgroup's part for itself, its lanes taking a request each. Workgroups go round the 8

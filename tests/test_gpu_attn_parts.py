@@ -60,3 +60,65 @@ def test_a_value_in_a_run_that_weighs_nothing(value, lens, most, Hq, Hkv, d):
     """A run of the last tokens scores far below the others, so that its readouts count next to nothing; an infinity among them still does."""
     _one_value(lens, most, Hq, Hkv, d, value, low=range(2100, 4000))
     _one_value(lens, most, Hq, Hkv, d, value, low=range(0, 2000))
+
+
+def _guarded(need, call, out):
+    """A call with a workspace of exactly its bytes, which hold NaN before, and a region behind it that stays as it is."""
+    assert need > 0
+    guard = 2 ** 24
+    ws = torch.full((need + guard,), 0xff, dtype=torch.uint8, device="cuda")
+    out.fill_(7.0)
+    call(ws[:need])
+    torch.cuda.synchronize()
+    assert bool((ws[need:] == 0xff).all()), "written behind the workspace"
+    got = out.clone()
+    call(torch.zeros(need + guard, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(got, out)
+    return got
+
+
+def _ones(lens, new, page):
+    """A table over pages in order, which of their rows hold a token, and the running sums of the new tokens."""
+    need = [-(-n // page) for n in lens]
+    first = [sum(need[:b]) for b in range(len(need))]
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    live = torch.zeros((sum(need), page), dtype=torch.bool)
+    for b, n in enumerate(lens):
+        table[b, :need[b]] = torch.arange(first[b], first[b] + need[b])
+        live[first[b]:first[b] + need[b]] = (torch.arange(need[b] * page) < n).reshape(-1, page)
+    return table.cuda(), live.cuda(), _i32([sum(new[:b]) for b in range(len(new) + 1)])
+
+
+# few units and many, of which none, one, some and nearly all are cut
+LENGTHS = {"one long": [4000], "few": [3000, 17, 900, 2048], "ladder": [60 * (i + 1) for i in range(100)], "one of many": [100] * 299 + [9000],
+           "two sizes": [40] * 200 + [2500] * 200, "even": [1500] * 128}
+
+
+@pytest.mark.parametrize("what", LENGTHS)
+@pytest.mark.parametrize("most,Hq,Hkv,d", [(2, 8, 4, 64), (12, 8, 4, 64), (40, 8, 2, 128)])
+def test_the_workspace_of_cut_requests(what, most, Hq, Hkv, d):
+    lens = LENGTHS[what]
+    new = [min(n, most - b % 2) for b, n in enumerate(lens)]
+    table, live, cu = _ones(lens, new, 16)
+    kp = torch.randn((live.shape[0], Hkv, 16, d), device="cuda").bfloat16()
+    vp = torch.where(live[:, None, :, None], 1.0, float("nan")).bfloat16().expand(-1, Hkv, -1, d).contiguous()
+    q = torch.randn((sum(new), Hq, d), device="cuda").bfloat16()
+    out, ln = torch.empty_like(q), _i32(lens)
+    got = _guarded(lib.kv_tree_attention_workspace_bytes(len(lens), Hq, Hkv, d, most, max(lens)),
+                   lambda ws: lib.kv_tree_attention(q, kp, vp, table, ln, cu, out, max_new=most, max_len=max(lens), workspace=ws), out)
+    assert bool((got == 1.0).all())
+
+
+@pytest.mark.parametrize("what", LENGTHS)
+@pytest.mark.parametrize("most,H,dc", [(1, 16, 512), (2, 16, 256), (3, 40, 512)])
+def test_the_workspace_of_cut_latents(what, most, H, dc):
+    lens = LENGTHS[what]
+    new = [min(n, most) for n in lens]
+    table, live, cu = _ones(lens, new, 16)
+    pages = torch.randn((live.shape[0], 16, dc + dc // 8), device="cuda").bfloat16()
+    pages[..., :dc] = torch.where(live[..., None], 1.0, float("nan")).bfloat16()
+    q = torch.randn((sum(new), H, dc + dc // 8), device="cuda").bfloat16()
+    out, ln = torch.empty((sum(new), H, dc), dtype=torch.bfloat16, device="cuda"), _i32(lens)
+    got = _guarded(lib.kv_latent_attention_workspace_bytes(len(lens), H, dc, most, max(lens)),
+                   lambda ws: lib.kv_latent_attention(q, pages, table, ln, out, 0.05, cu_new=cu, max_new=most, max_len=max(lens), workspace=ws), out)
+    assert bool((got == 1.0).all())
