@@ -710,7 +710,7 @@ size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t
  * they may differ in their last bit with max_new, max_len and how the requests' lengths share out the work.
  * A NaN or infinity of a new token's value reaches only the tokens that see it. max_new * num_q_heads
  * stays at most 2^30 - 1, and B * num_kv_heads times the tiles of 64 query rows of a request's max_new tokens
- * below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
+ * at most 2^24 - 2^10. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
 damp_status kv_tree_attention(const void* q, const void* k_pages, const void* v_pages,
                               const int32_t* block_table, const int32_t* seq_lens,
                               const int32_t* cu_new, const int64_t* mask, int32_t mask_words, int32_t T,
@@ -738,7 +738,7 @@ size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t
  * q dev bf16 [T][num_heads][d_latent + d_rope] (a head's query times its key up-projection, then the rotary
  * part), out dev bf16 [T][num_heads][d_latent] (the value up-projection follows). scale is that of the
  * expanded form's channels. cu_new NULL: one token per request (T == B, max_new 1, no mask). Other arguments
- * and limits as kv_tree_attention (tiles of 64 rows of all heads, below 2^23). The softmax weights enter the product
+ * and limits as kv_tree_attention (tiles of 64 rows of all heads, at most 2^23 - 2^10). The softmax weights enter the product
  * rounded to bf16 (2^-9 of each), over the sum of the rounded ones, whatever the number of rows. */
 damp_status kv_latent_attention(const void* q, const void* pages, const int32_t* block_table,
                                 const int32_t* seq_lens, const int32_t* cu_new, const int64_t* mask,

@@ -164,11 +164,10 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
 // thread, U runs at a time; S threads share out the runs of a row, and meet in LDS. K 1,024 / (D S) rows a
 // workgroup. Bound by the launch and by dependent loads.
 template <int D, int K, int U, int S>
-__global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const TokenPlan plan, int groups) {
+__device__ __forceinline__ void join_piece(const TreeArgs& a, const TokenPlan& plan, int groups, unsigned id) {
   constexpr int LPR = D / 4, RPG = 256 / LPR / S;  // threads for a row's channels, rows at once
   static_assert(S == 1 || K == 1);
   const int tid = __builtin_amdgcn_workitem_id_x(), seg = tid / (256 / S), lane = tid % (256 / S);
-  const unsigned id = __builtin_amdgcn_workgroup_id_x();
   const int units = a.Hkv * plan.tiles;
   const int group = static_cast<int>(id % groups), unit = static_cast<int>(id / groups % units), b = static_cast<int>(id / groups / units);
   const int tile = unit % plan.tiles, kvh = unit / plan.tiles, G = a.Hq / a.Hkv;
@@ -259,6 +258,17 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const 
   }
 }
 
+// Each workgroup takes every step-th of `pieces` (with one row a thread there is a workgroup for each).
+template <int D, int K, int U, int S>
+__global__ __launch_bounds__(256) void attn_join_kernel(const TreeArgs a, const TokenPlan plan, int groups, unsigned pieces, unsigned step) {
+  const unsigned first = __builtin_amdgcn_workgroup_id_x();
+  if constexpr (K == 1) {
+    join_piece<D, K, U, S>(a, plan, groups, first);
+  } else {
+    for (unsigned id = first; id < pieces; id += step) join_piece<D, K, U, S>(a, plan, groups, id);
+  }
+}
+
 // Rows and slots are the kernel's. Requests of up to `whole` tokens are not cut, nor are any where there are more
 // than kManyRequests, which alone fill the chip four times over: each workgroup finding its part among 1,024 of 1,100
 // tokens, 8 heads of d = 64, takes 449 us, whole ones 385; but 756 and 1,000 where one of them has 60,000. Among 512
@@ -286,9 +296,12 @@ constexpr int join_shares(int d) { return d == 512 ? 2 : 4; }   // (a workgroup 
 
 struct JoinPlan {
   bool many;
-  int per_unit;          // workgroups that a (request, head, row tile) takes
-  int64_t groups;
+  int per_unit;          // pieces of a (request, head, row tile)
+  int64_t pieces;
 };
+
+// Workgroups that the launch has at most, so that its size bounds no call; a call's units may have 16 pieces each.
+constexpr int64_t kJoinGroups = 65536;
 
 inline JoinPlan join_plan(const TokenPlan& p, int64_t B, int64_t Hkv, int d) {
   const int few_rows = 1024 / d / join_shares(d), many_rows = 2 * 1024 / d;
@@ -297,18 +310,13 @@ inline JoinPlan join_plan(const TokenPlan& p, int64_t B, int64_t Hkv, int d) {
   return JoinPlan{is_many, static_cast<int>(is_many ? many : few), units * (is_many ? many : few)};
 }
 
-// Workgroups of the larger launch.
-inline int64_t token_groups(const TokenPlan& p, const TreeSizes& z, int d) {
-  return p.whole ? p.groups : std::max<int64_t>(p.groups, join_plan(p, z.B, z.Hkv, d).groups);
-}
-
 template <int D>
 void launch_join(const TreeArgs& a, const TokenPlan& p, hipStream_t s) {
   if (p.whole) return;
   const JoinPlan j = join_plan(p, a.B, a.Hkv, D);
-  const dim3 grid(static_cast<unsigned>(j.groups));
-  if (j.many) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4, 1>), grid, dim3(256), 0, s, a, p, j.per_unit);
-  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8, join_shares(D)>), grid, dim3(256), 0, s, a, p, j.per_unit);
+  const unsigned pieces = static_cast<unsigned>(j.pieces), groups = static_cast<unsigned>(std::min(j.pieces, kJoinGroups));
+  if (j.many) hipLaunchKernelGGL((attn_join_kernel<D, 2, 4, 1>), dim3(groups), dim3(256), 0, s, a, p, j.per_unit, pieces, groups);
+  else hipLaunchKernelGGL((attn_join_kernel<D, 1, 8, join_shares(D)>), dim3(groups), dim3(256), 0, s, a, p, j.per_unit, pieces, groups);
 }
 
 }  // namespace

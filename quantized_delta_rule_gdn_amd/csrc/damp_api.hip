@@ -545,7 +545,7 @@ damp_status check_workspace(const void* workspace, size_t have, size_t need) {
   return DAMP_OK;
 }
 
-// The attentions of several tokens take no more of them than there are rows.
+// (with max_new 0 the workspace's size is that of one token)
 damp::TreeSizes tree_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t max_new, int32_t max_len) {
   return damp::TreeSizes{B, Hq, Hkv, std::max(max_new, 1), max_len};
 }
@@ -1574,7 +1574,7 @@ damp_status kv_latent_append(const void* c, const void* k_rope, const int64_t* s
 size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t d_latent, int32_t max_new, int32_t max_len) {
   if (B <= 0 || num_heads <= 0 || (d_latent != 256 && d_latent != 512) || max_new < 0 || max_new > (1 << 30) || max_len < 0 || max_len > (1 << 30)) return 0;
   const damp::TreeSizes z = tree_sizes(B, num_heads, 1, max_new, max_len);
-  return tree_fits(z) && damp::latent_grid(z, d_latent) <= kMaxGroups ? damp::latent_ws_bytes(z, d_latent) : 0;
+  return tree_fits(z) && damp::latent_grid(z) <= kMaxGroups ? damp::latent_ws_bytes(z, d_latent) : 0;
 }
 
 damp_status kv_latent_attention(const void* q, const void* pages, const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_new,
@@ -1594,7 +1594,7 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
   if (!aligned(q, 16) || !aligned(pages, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_new, 4) || !aligned(mask, 8))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "q, the pages and out must be 16-byte, mask 8-byte, block_table, seq_lens and cu_new 4-byte aligned");
   const damp::TreeSizes z = tree_sizes(B, num_heads, 1, max_new, max_len);
-  if (!tree_fits(z) || damp::latent_grid(z, d_latent) > kMaxGroups)
+  if (!tree_fits(z) || damp::latent_grid(z) > kMaxGroups)
     return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d with max_new = %d and max_len = %d exceeds the grid limit", B, max_new, max_len);
   st = check_workspace(workspace, workspace_bytes, damp::latent_ws_bytes(z, d_latent));
   if (st != DAMP_OK) return st;

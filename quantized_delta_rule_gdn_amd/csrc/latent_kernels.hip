@@ -679,9 +679,9 @@ hipError_t launch_latent_append(const LatentAppendArgs& a, hipStream_t s) {
 }
 
 // (in workgroups of 256 threads: those of more than 16 rows have twice as many)
-int64_t latent_grid(const TreeSizes& z, int32_t dc) {
+int64_t latent_grid(const TreeSizes& z) {
   const TokenPlan p = latent_plan(z);
-  return std::max<int64_t>(token_groups(p, z, dc), p.rows_log2 > 4 ? int64_t(2) * p.groups : 0);
+  return p.rows_log2 > 4 ? int64_t(2) * p.groups : p.groups;
 }
 
 size_t latent_ws_bytes(const TreeSizes& z, int32_t dc) { return parts_bytes(latent_plan(z), z, dc); }

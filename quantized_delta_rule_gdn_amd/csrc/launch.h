@@ -192,7 +192,7 @@ struct TreeSizes {
   int32_t B, Hq, Hkv, max_new, max_len;
 };
 
-int64_t kv_tree_grid(const TreeSizes& z, int32_t d);   // workgroups of its largest launch
+int64_t kv_tree_grid(const TreeSizes& z, int32_t d);   // workgroups
 size_t kv_tree_ws_bytes(const TreeSizes& z, int32_t d);
 hipError_t launch_kv_tree(int d, const TreeArgs& a, hipStream_t s);
 
@@ -208,7 +208,7 @@ struct LatentAppendArgs {
 
 hipError_t launch_latent_append(const LatentAppendArgs& a, hipStream_t s);
 // Absorbed form: TreeArgs with Hkv = 1, k_pages the latents, q [T][Hq][dc + dr], out [T][Hq][dc].
-int64_t latent_grid(const TreeSizes& z, int32_t dc);
+int64_t latent_grid(const TreeSizes& z);
 size_t latent_ws_bytes(const TreeSizes& z, int32_t dc);
 hipError_t launch_latent(int dc, const TreeArgs& a, hipStream_t s);
 

@@ -559,7 +559,7 @@ hipError_t tree_d(const TreeArgs& a, const TreeSizes& z, hipStream_t s) {
 
 }  // namespace
 
-int64_t kv_tree_grid(const TreeSizes& z, int32_t d) { return token_groups(tree_plan(z, d), z, d); }
+int64_t kv_tree_grid(const TreeSizes& z, int32_t d) { return tree_plan(z, d).groups; }
 
 size_t kv_tree_ws_bytes(const TreeSizes& z, int32_t d) { return parts_bytes(tree_plan(z, d), z, d); }
 

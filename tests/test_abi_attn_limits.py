@@ -16,3 +16,36 @@ def test_the_workspace_is_what_one_round_of_workgroups_leaves(name, head, rows, 
             got = size(B, *head, most, 4096) - 8 * B
             assert 0 < got <= min(768 * rows * width * 4, 2 ** 26), (B, most, got)
             assert got == size(48, *head, 32, 4096) - 8 * 48
+
+
+X = 0x100000   # never dereferenced: every case is settled on the host
+MOST = {"kv_tree_attention": 2 ** 24 - 2 ** 10, "kv_latent_attention": 2 ** 23 - 2 ** 10}
+
+
+def _takes(name, B, Hkv, group, most, max_len):
+    """Whether the call with these sizes gets as far as its workspace, or to rows that are none."""
+    if name == "kv_tree_attention":
+        ws = lib.load().kv_tree_attention_workspace_bytes(B, Hkv * group, Hkv, 128, most, max_len)
+        status = lib.load().kv_tree_attention(X, X, X, X, X, X, None, 0, 1, B, most, Hkv * group, Hkv, 128, 9, 16, 4, max_len, 1.0, X, None, 0, None)
+    else:
+        ws = lib.load().kv_latent_attention_workspace_bytes(B, group, 512, most, max_len)
+        status = lib.load().kv_latent_attention(X, X, X, X, X, None, 0, 1, B, most, group, 512, 64, 9, 16, 4, max_len, 1.0, X, None, 0, None)
+    assert status == lib.DAMP_ERR_INVALID_ARGUMENT
+    assert ("workspace" in lib.last_error()) == (ws > 0) and ("grid limit" in lib.last_error()) == (ws == 0), lib.last_error()
+    return ws > 0
+
+
+@pytest.mark.parametrize("B", [1, 48, 256, 512])
+@pytest.mark.parametrize("name,Hkv,group", [("kv_tree_attention", 1, 64), ("kv_tree_attention", 8, 128), ("kv_latent_attention", 1, 64), ("kv_latent_attention", 1, 128)])
+def test_every_call_up_to_the_documented_size(name, Hkv, group, B):
+    """Tiles of 64 query rows over all requests and key-value heads, requests that may be cut and so are joined."""
+    most = MOST[name] // (B * Hkv * group // 64)
+    if most * Hkv * group < 2 ** 30:
+        assert _takes(name, B, Hkv, group, most, 4096)
+    assert not _takes(name, B, Hkv, group, 4 * most, 4096)
+
+
+def test_one_tile_a_request_up_to_the_documented_size():
+    """Where tiles have 64 rows the limit is met on both sides."""
+    assert _takes("kv_tree_attention", 512, 32766, 64, 1, 4096) and not _takes("kv_tree_attention", 512, 32768, 64, 1, 4096)
+    assert _takes("kv_latent_attention", 512, 1, 64, 16382, 4096) and not _takes("kv_latent_attention", 512, 1, 64, 16384, 4096)

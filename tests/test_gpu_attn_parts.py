@@ -122,3 +122,31 @@ def test_the_workspace_of_cut_latents(what, most, H, dc):
     got = _guarded(lib.kv_latent_attention_workspace_bytes(len(lens), H, dc, most, max(lens)),
                    lambda ws: lib.kv_latent_attention(q, pages, table, ln, out, 0.05, cu_new=cu, max_new=most, max_len=max(lens), workspace=ws), out)
     assert bool((got == 1.0).all())
+
+
+@pytest.mark.parametrize("most,there,Hq,Hkv,d", [(96, 96, 8, 2, 128), (400, 2, 32, 8, 64)])
+def test_more_pieces_to_join_than_workgroups(most, there, Hq, Hkv, d):
+    """The launch that joins takes several pieces a workgroup."""
+    lens = [40 if b % 5 else 1700 for b in range(512)]
+    new = [min(n, there) for n in lens]
+    table, live, cu = _ones(lens, new, 16)
+    kp = torch.randn((live.shape[0], Hkv, 16, d), device="cuda").bfloat16()
+    vp = torch.where(live[:, None, :, None], 1.0, float("nan")).bfloat16().expand(-1, Hkv, -1, d).contiguous()
+    q = torch.randn((sum(new), Hq, d), device="cuda").bfloat16()
+    out, ln = torch.empty_like(q), _i32(lens)
+    got = _guarded(lib.kv_tree_attention_workspace_bytes(512, Hq, Hkv, d, most, 1700),
+                   lambda ws: lib.kv_tree_attention(q, kp, vp, table, ln, cu, out, max_new=most, max_len=1700, workspace=ws), out)
+    assert bool((got == 1.0).all())
+
+
+def test_as_many_latent_tiles_as_a_call_takes():
+    """512 requests that may have 131,072 rows each: an eighth of the limit, and 2^24 pieces to join."""
+    lens, H = [30 if b % 7 else 2000 for b in range(512)], 128
+    new = [1 + b % 2 for b in range(512)]
+    table, live, cu = _ones(lens, new, 16)
+    pages = torch.randn((live.shape[0], 16, 576), device="cuda").bfloat16()
+    pages[..., :512] = torch.where(live[..., None], 1.0, float("nan")).bfloat16()
+    q = torch.randn((1024, H, 576), device="cuda").bfloat16()
+    out, ln = torch.zeros((1024, H, 512), dtype=torch.bfloat16, device="cuda"), _i32(lens)
+    lib.kv_latent_attention(q, pages, table, ln, out, 0.05, cu_new=cu, max_new=1024, max_len=4096)
+    assert bool((out[:sum(new)] == 1.0).all()) and not bool(out[sum(new):].any())
