@@ -739,7 +739,7 @@ size_t kv_latent_attention_workspace_bytes(int32_t B, int32_t num_heads, int32_t
  * part), out dev bf16 [T][num_heads][d_latent] (the value up-projection follows). scale is that of the
  * expanded form's channels. cu_new NULL: one token per request (T == B, max_new 1, no mask). Other arguments
  * and limits as kv_tree_attention (tiles of 64 rows of all heads, at most 2^23 - 2^10). The softmax weights enter the product
- * rounded to bf16 (2^-9 of each), over the sum of the rounded ones, whatever the number of rows. */
+ * as there: in two pieces where max_new * num_heads is at most 16, and else rounded once. */
 damp_status kv_latent_attention(const void* q, const void* pages, const int32_t* block_table,
                                 const int32_t* seq_lens, const int32_t* cu_new, const int64_t* mask,
                                 int32_t mask_words, int32_t T, int32_t B, int32_t max_new,
@@ -758,7 +758,7 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
  *   cu_q, cu_k  dev int32 [B + 1], ascending, kept inside [0, Tq] and [0, Tk]. Rows of out behind the last
  *               request are not written.
  * All 16-byte aligned but cu_q and cu_k. d is 64 or 128, Tq and Tk at most 2^30. Scores, statistics and sums are binary32, the
- * weights rounded as in kv_latent_attention. A NaN or infinity of a token reaches only queries that see
+ * weights rounded once, as in kv_tree_attention of many rows. A NaN or infinity of a token reaches only queries that see
  * it. (Tq / 64 + B) * num_heads stays below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d), HIP. */
 damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride,
                                        int64_t k_head_stride, const void* k_rope, const void* v,

@@ -124,15 +124,16 @@ __device__ __forceinline__ uint32_t round_pair(float x0, float x1, float& sum) {
   return w;
 }
 
+__device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& upper, uint32_t& rest, float& sum) {
+  const uint32_t w0 = __float_as_uint(x0 * 0x1.ffep-1f), w1 = __float_as_uint(x1 * 0x1.ffep-1f);
+  upper = __builtin_amdgcn_perm(w1, w0, 0x07060302u);
+  rest = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
+  sum += x0 + x1;
+}
+
 __device__ __forceinline__ void pack_weights(const float (&p)[8], Frag (&pf)[2], float& sum) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x0 = p[2 * i], x1 = p[2 * i + 1];
-    const uint32_t w0 = __float_as_uint(x0 * 0x1.ffep-1f), w1 = __float_as_uint(x1 * 0x1.ffep-1f);
-    pf[0].w[i] = __builtin_amdgcn_perm(w1, w0, 0x07060302u);
-    pf[1].w[i] = pack_bf16(x0 - __uint_as_float(w0 & 0xffff0000u), x1 - __uint_as_float(w1 & 0xffff0000u));
-    sum += x0 + x1;
-  }
+  for (int i = 0; i < 4; ++i) split_pair(p[2 * i], p[2 * i + 1], pf[0].w[i], pf[1].w[i], sum);
 }
 
 // 0x8000 / 0x80000000 bits of the halves that hold an infinity or a NaN.

@@ -30,12 +30,14 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppendAr
 // workgroup holds in LDS serves both products of all its rows.
 constexpr int kLatTile = 64;
 
-// Up to 16 rows: the stream of the cache is what takes longest (64 requests, 266,000 tokens, 16 heads: 67 us and 6
-// for the join; 5.3 TB/s behind the first 8 us, in which lengths, pages and the first tiles are on their way;
+// Up to 16 rows: the stream of the cache is what takes longest (64 requests, 266,000 tokens, 16 heads: 68 us and 6
+// for the join; 5.2 TB/s behind the first 8 us, in which lengths, pages and the first tiles are on their way;
 // the eight waves below take the same, and 17 instead of 16 us for one request of 700 tokens). The 4 waves
 // share out the scores by tokens, meet for the maximum of each row, hand the weights over through LDS, and
 // share out the readout by channels, so that a tile is read from LDS once (scores: as rows; readout:
-// transposed on the way). The next tile is on its way in registers meanwhile.
+// transposed on the way). The next tile is on its way in registers meanwhile. The weights go in two pieces, as for
+// few rows of the other caches: that takes 1 to 4% of the call (these requests 68.4 -> 69.9 us, 250 of 200 tokens
+// 20.6 -> 21.4), and without it values that cancel are off by 2^-8 of their size, not 2^-15.
 template <int DC>
 struct LatGeo {
   static constexpr int DR = DC / 8, W = DC + DR;     // channels of a row
@@ -51,7 +53,7 @@ __global__ __launch_bounds__(256, 2) void latent_kernel(const TreeArgs a, const 
   constexpr int W = Geo::W, KS = W / 32, CB = DC / 64;          // k steps; 16-channel blocks of a wave's share
   constexpr int LDP = kLatTile * 2 + 16;
   __shared__ __align__(16) uint8_t tile_k[kLatTile * Geo::LD];
-  __shared__ __align__(16) uint8_t tile_p[16][LDP];
+  __shared__ __align__(16) uint8_t tile_p[2][16][LDP];              // the weights' two pieces
   __shared__ float part[4][16];
   __shared__ uint32_t tile_live[4], tile_odd[4];
 
@@ -210,19 +212,23 @@ __global__ __launch_bounds__(256, 2) void latent_kernel(const TreeArgs a, const 
       const float base = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = pow2(p[i] - base);
-      const uint32_t w0 = round_pair(p[0], p[1], sum), w1 = round_pair(p[2], p[3], sum);
-      *reinterpret_cast<uint2*>(&tile_p[r][(16 * wv + 4 * g) * 2]) = make_uint2(w0, w1);
+      uint2 upper, rest;
+      split_pair(p[0], p[1], upper.x, rest.x, sum);
+      split_pair(p[2], p[3], upper.y, rest.y, sum);
+      *reinterpret_cast<uint2*>(&tile_p[0][r][(16 * wv + 4 * g) * 2]) = upper;
+      *reinterpret_cast<uint2*>(&tile_p[1][r][(16 * wv + 4 * g) * 2]) = rest;
     }
     __syncthreads();
     // readout^T [channel][row] += V^T P^T, this wave's channels
 #pragma unroll
     for (int step = 0; step < kLatTile / 32; ++step) {
-      const Frag pf = load_frag(&tile_p[r][(32 * step + 8 * g) * 2]);
+      const Frag pf[2] = {load_frag(&tile_p[0][r][(32 * step + 8 * g) * 2]), load_frag(&tile_p[1][r][(32 * step + 8 * g) * 2])};
       const uint8_t* v = tile_k + (32 * step + 8 * g + (r >> 2)) * Geo::LD + (wv * (DC / 4) + 4 * (r & 3)) * 2;
 #pragma unroll
       for (int m = 0; m < CB; ++m) {
         const Frag vf = load_frag_t(reinterpret_cast<const uint16_t*>(v + 32 * m), reinterpret_cast<const uint16_t*>(v + 32 * m + 4 * Geo::LD));
-        o[m] = mfma(vf, pf, o[m]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) o[m] = mfma(vf, pf[x], o[m]);
       }
     }
   }

@@ -150,3 +150,23 @@ def test_as_many_latent_tiles_as_a_call_takes():
     out, ln = torch.zeros((1024, H, 512), dtype=torch.bfloat16, device="cuda"), _i32(lens)
     lib.kv_latent_attention(q, pages, table, ln, out, 0.05, cu_new=cu, max_new=1024, max_len=4096)
     assert bool((out[:sum(new)] == 1.0).all()) and not bool(out[sum(new):].any())
+
+
+@pytest.mark.parametrize("dc", [256, 512])
+@pytest.mark.parametrize("H,most", [(1, 1), (5, 3), (16, 1), (4, 4)])
+@pytest.mark.parametrize("n", [4, 17, 70, 900])
+def test_latent_weights_of_few_rows(dc, H, most, n):
+    """Up to 16 rows: values of either sign that cancel, so that a weight rounded once to bf16 would show."""
+    W = dc + dc // 8
+    gen, pages, _, table, keys = build([n], [most], 1, dc, 16, latent=W)
+    k = keys[0]
+    k[:, :dc] = 64.0 * (1 - 2 * torch.randint(0, 2, (n, dc), generator=gen))
+    pos = torch.arange(n)
+    pages[table[0, pos // 16].long(), pos % 16] = k
+    q = torch.randn((most, H, W), generator=gen).bfloat16()
+    q[..., :dc] = 0.0
+    out = torch.zeros((most, H, dc), dtype=torch.bfloat16, device="cuda")
+    lib.kv_latent_attention(q.cuda(), pages.cuda(), table.cuda(), _i32([n]), out, 0.02, cu_new=_i32([0, most]))
+    kd = k.double()[:, None]
+    o, mag, e = ref.attend(q.double(), kd, kd[..., :dc], ref.seen(most, n), 0.02)
+    ref.is_close(out, o, ref.tolerance(o, mag, e, n, weight(H * most)), f"{n} tokens")
