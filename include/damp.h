@@ -704,7 +704,7 @@ size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t
  *               further ones get no readout
  * Other arguments as kv_decode_attention; pages may be shared, nothing is stored. Scores, softmax
  * statistics and sums are binary32. The softmax weights enter the product with V as in kv_decode_attention
- * where max_new * num_q_heads / num_kv_heads is at most 16, and else rounded to bf16 (2^-9 of each),
+ * where max_new * num_q_heads / num_kv_heads is at most 16, and else rounded to bf16 (2^-8 of each),
  * over the sum of the rounded ones; they are relative to a score that the row's highest may pass by up to
  * 2^8, so values of 2^120 and more may end infinite. Readouts do not depend on the other requests of a call;
  * they may differ in their last bit with max_new, max_len and how the requests' lengths share out the work.

@@ -110,8 +110,8 @@ __device__ __forceinline__ T rarely(T x) {
 __device__ __forceinline__ Frag ones() { return Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}; }
 
 // Softmax weights of one row as an operand of the product with V, in one of two ways. Rounded to bf16 (to
-// 2^-9 of each), with a sum over the rounded ones, so that equal values come back as they are: what a row
-// gets is then off by 2^-9 of the weighted mean of |v - o|, the size of its own rounding. Or in two pieces,
+// 2^-8 of each), with a sum over the rounded ones, so that equal values come back as they are: what a row
+// gets is then off by up to 2^-8 of the weighted mean of |v - o|, the size of its own rounding. Or in two pieces,
 // the upper 16 bits of the weight (less 2^-12) and the rest rounded, good to 2^-15 + 2^-20 of it, the rest
 // never 0 (an infinite value times 0 would be NaN): twice the products, which few rows have to spare.
 __device__ __forceinline__ Frag round_weights(const float (&p)[8]) {
