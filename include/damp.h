@@ -705,8 +705,9 @@ size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t
  * Other arguments as kv_decode_attention; pages may be shared, nothing is stored. Scores, softmax
  * statistics and sums are binary32. The softmax weights enter the product with V as in kv_decode_attention
  * where max_new * num_q_heads / num_kv_heads is at most 16, and else rounded to bf16 (2^-8 of each),
- * over the sum of the rounded ones; they are relative to a score that the row's highest may pass by up to
- * 2^8, so values of 2^120 and more may end infinite. Readouts do not depend on the other requests of a call;
+ * over the sum of the rounded ones; they are relative to a score that the row's highest may pass by a factor
+ * of up to 2^8 and are divided by their sum in the end, so over n tokens values of 2^120 / n and more may end
+ * infinite. Readouts do not depend on the other requests of a call;
  * they may differ in their last bit with max_new, max_len and how the requests' lengths share out the work.
  * A NaN or infinity of a new token's value reaches only the tokens that see it. max_new * num_q_heads
  * stays at most 2^30 - 1, and B * num_kv_heads times the tiles of 64 query rows of a request's max_new tokens
@@ -758,7 +759,7 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
  *   cu_q, cu_k  dev int32 [B + 1], ascending, kept inside [0, Tq] and [0, Tk]. Rows of out behind the last
  *               request are not written.
  * All 16-byte aligned but cu_q and cu_k. d is 64 or 128, Tq and Tk at most 2^30. Scores, statistics and sums are binary32, the
- * weights rounded once, as in kv_tree_attention of many rows. A NaN or infinity of a token reaches only queries that see
+ * weights rounded once, as in kv_tree_attention of many rows, with the same bound of the values. A NaN or infinity of a token reaches only queries that see
  * it. (Tq / 64 + B) * num_heads stays below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d), HIP. */
 damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride,
                                        int64_t k_head_stride, const void* k_rope, const void* v,

@@ -1,5 +1,5 @@
-"""Attention of several new tokens where its parts meet: the waves of a workgroup, and the runs of a request that
-was cut. References: cache_ref in 64 bits, bounds cache_ref.tolerance."""
+"""Attention of several new tokens and of latents where its parts meet (the waves of a workgroup, the runs of a request that
+was cut), its workspace, its weights and its largest values. References: cache_ref in 64 bits, bounds cache_ref.tolerance."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -170,3 +170,67 @@ def test_latent_weights_of_few_rows(dc, H, most, n):
     kd = k.double()[:, None]
     o, mag, e = ref.attend(q.double(), kd, kd[..., :dc], ref.seen(most, n), 0.02)
     ref.is_close(out, o, ref.tolerance(o, mag, e, n, weight(H * most)), f"{n} tokens")
+
+
+# Large values over long contexts: scores that pass the first tiles' by a little less than 2^8 (references stay where they
+# are), values of half the bound 2^120 / n. All equal, so the mean is the value itself, and it comes back exactly.
+LONG, RISE = 65536, 7.9
+
+
+def _steps(n, low):
+    """A score of RISE binary orders for all tokens but the first `low`, as a key's channel beside a query's of 8."""
+    k = torch.full((n,), RISE * 0.6931 / 8).bfloat16()
+    k[:low] = 0.0
+    assert float(k.max()) * 8 / 0.6931 < 8.0
+    return k
+
+
+def _layout(B, n):
+    """Request 0 of n tokens, the others of one; pages of 16 in order."""
+    lens = [n] + [1] * (B - 1)
+    table, live, cu = _ones(lens, [1] * B, 16)
+    pos = torch.arange(n, device="cuda")
+    return lens, table, live, cu, pos
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv", [(1, 2, 1), (1, 20, 1), (1, 280, 2), (520, 4, 4), (520, 160, 8), (520, 640, 8)])
+def test_large_values(B, Hq, Hkv, d):
+    """Of one request that is cut, and of one among so many that none is."""
+    value = 2.0 ** 119 / LONG
+    lens, table, live, cu, pos = _layout(B, LONG)
+    kp = torch.zeros((live.shape[0], Hkv, 16, d), dtype=torch.bfloat16, device="cuda")
+    kp[pos // 16, :, pos % 16, 5] = _steps(LONG, 256).cuda()[:, None]
+    vp = torch.where(live[:, None, :, None], value, float("nan")).bfloat16().expand(-1, Hkv, -1, d).contiguous()
+    q = torch.zeros((B, Hq, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = 8.0
+    out = torch.zeros_like(q)
+    lib.kv_tree_attention(q, kp, vp, table, _i32(lens), cu, out, max_new=1, scale=1.0)
+    assert bool((out == value).all())
+
+
+@pytest.mark.parametrize("dc", [256, 512])
+@pytest.mark.parametrize("B,H", [(1, 3), (1, 20), (1, 100), (1100, 1), (1100, 20), (1100, 40)])
+def test_large_latents(B, H, dc):
+    value = 2.0 ** 119 / LONG
+    lens, table, live, cu, pos = _layout(B, LONG)
+    pages = torch.zeros((live.shape[0], 16, dc + dc // 8), dtype=torch.bfloat16, device="cuda")
+    pages[..., :dc] = torch.where(live[..., None], value, float("nan")).bfloat16()
+    pages[pos // 16, pos % 16, dc + 5] = _steps(LONG, 256).cuda()
+    q = torch.zeros((B, H, dc + dc // 8), dtype=torch.bfloat16, device="cuda")
+    q[..., dc + 5] = 8.0
+    out = torch.zeros((B, H, dc), dtype=torch.bfloat16, device="cuda")
+    lib.kv_latent_attention(q, pages, table, _i32(lens), out, 1.0, cu_new=cu, max_new=1)
+    assert bool((out == value).all())
+
+
+@pytest.mark.parametrize("d,H,nq", [(64, 2, 3), (128, 2, 70), (64, 256, 70)])
+def test_large_prompt_values(d, H, nq):
+    n = 4096
+    value = 2.0 ** 119 / n
+    q, k, kr = (torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((nq, H, d + d // 2), (n, H, d), (n, d // 2)))
+    q[..., 5], k[..., 5] = 8.0, _steps(n, 64).cuda()[:, None]
+    v = torch.full((n, H, d), value, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((nq, H, d), dtype=torch.bfloat16, device="cuda")
+    lib.kv_latent_prompt_attention(q, k, kr, v, _i32([0, nq]), out, cu_k=_i32([0, n]), scale=1.0)
+    assert bool((out == value).all())
