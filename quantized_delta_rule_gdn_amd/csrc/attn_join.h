@@ -160,6 +160,11 @@ __device__ __forceinline__ Spot spot_of(const TreeArgs& a, const TokenPlan& plan
   return Spot{-1};
 }
 
+// What is left of readouts that weigh nothing (see add_part).
+__device__ __forceinline__ float4 infinite_only(float4 x) {
+  return make_float4(add_part(0.0f, x.x, 0.0f), add_part(0.0f, x.y, 0.0f), add_part(0.0f, x.z, 0.0f), add_part(0.0f, x.w, 0.0f));
+}
+
 // The runs of a (request, row) joined: sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, four channels of K rows a
 // thread, U runs at a time; S threads share out the runs of a row, and meet in LDS. K 1,024 / (D S) rows a
 // workgroup. Bound by the launch and by dependent loads.
@@ -208,19 +213,31 @@ __device__ __forceinline__ void join_piece(const TreeArgs& a, const TokenPlan& p
         if (s0 + i * S >= info.y) x[k][i] = make_float2(-INFINITY, 0.0f);
         top = fmaxf(top, x[k][i].x);
       }
-      const float base = top == -INFINITY ? 0.0f : top, shrink = part_factor(m[k] - base);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float shrink = m[k] == -INFINITY ? 1.0f : pow2(m[k] - base), f[U], least = shrink;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        f[i] = s0 + i * S < info.y ? pow2(x[k][i].x - base) : 1.0f;
+        least = fminf(least, f[i]);
+      }
       m[k] = top;
       l[k] *= shrink;
+#pragma unroll
+      for (int i = 0; i < U; ++i) l[k] = fmaf(f[i], x[k][i].y, l[k]);
+      if (__any(least == 0.0f)) {
+        if (shrink == 0.0f) acc[k] = infinite_only(acc[k]), shrink = 1.0f;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (f[i] == 0.0f) v[k][i] = infinite_only(v[k][i]), f[i] = 1.0f;
+      }
       acc[k].x *= shrink; acc[k].y *= shrink; acc[k].z *= shrink; acc[k].w *= shrink;
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         if (s0 + i * S >= info.y) break;               // (its values stand in for none)
-        const float f = part_factor(x[k][i].x - base);
-        l[k] = fmaf(f, x[k][i].y, l[k]);
-        acc[k].x = fmaf(f, v[k][i].x, acc[k].x);
-        acc[k].y = fmaf(f, v[k][i].y, acc[k].y);
-        acc[k].z = fmaf(f, v[k][i].z, acc[k].z);
-        acc[k].w = fmaf(f, v[k][i].w, acc[k].w);
+        acc[k].x = fmaf(f[i], v[k][i].x, acc[k].x);
+        acc[k].y = fmaf(f[i], v[k][i].y, acc[k].y);
+        acc[k].z = fmaf(f[i], v[k][i].z, acc[k].z);
+        acc[k].w = fmaf(f[i], v[k][i].w, acc[k].w);
       }
     }
   }
@@ -239,13 +256,10 @@ __device__ __forceinline__ void join_piece(const TreeArgs& a, const TokenPlan& p
     l[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const float f = part_factor(part_ml[i][lane].x - base);
+      const float f = pow2(part_ml[i][lane].x - base);
       const float4 v = part_o[i][lane];
       l[0] = fmaf(f, part_ml[i][lane].y, l[0]);
-      acc[0].x = fmaf(f, v.x, acc[0].x);
-      acc[0].y = fmaf(f, v.y, acc[0].y);
-      acc[0].z = fmaf(f, v.z, acc[0].z);
-      acc[0].w = fmaf(f, v.w, acc[0].w);
+      acc[0] = make_float4(add_part(f, v.x, acc[0].x), add_part(f, v.y, acc[0].y), add_part(f, v.z, acc[0].z), add_part(f, v.w, acc[0].w));
     }
   }
 #pragma unroll

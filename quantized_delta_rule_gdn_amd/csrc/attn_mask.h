@@ -88,10 +88,10 @@ __device__ __forceinline__ float max_row_slots(float x) {
   return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-// What a part of a row's tokens (a wave's, a run's) counts where the parts are joined, x the base-2 logarithm
-// of that. Never 0: a part's readout may hold an infinity that another part's scores pass by far, or one added back
-// to a wave that saw no token (0 * infinity is NaN). What is finite counts at most 2^-126 too much.
-__device__ __forceinline__ float part_factor(float x) { return fmaxf(pow2(x), 0x1p-126f); }
+// sum + f x, where f is what a part of a row's tokens (a wave's, a run's) counts beside the others and x a channel
+// of its readout. f may be 0, where the other parts' scores are higher by far or the part saw no token; the weights
+// behind it are not, so an infinity counts all the same (0 * infinity is NaN).
+__device__ __forceinline__ float add_part(float f, float x, float sum) { return fmaf(__builtin_isfinite(x) ? f : 1.0f, x, sum); }
 
 // A row's running maximum stays as it is until a score passes it by more than this factor 2^kSlack: weights of
 // up to 2^8 lose nothing in binary32 or bf16 (sums over n tokens overflow from values of 2^120 / n on), and most tiles then need neither the other lanes' maxima nor

@@ -234,8 +234,8 @@ __global__ __launch_bounds__(256, 3) void kv_tree_kernel(const TreeArgs a, const
     float acc = 0.0f, l = 0.0f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float f = part_factor(part_m[w][h] - base);
-      acc = fmaf(f, part_o[w][h][c], acc);
+      const float f = pow2(part_m[w][h] - base);
+      acc = add_part(f, part_o[w][h][c], acc);
       l = fmaf(f, part_l[w][h], l);
     }
     if (splits == 1) {

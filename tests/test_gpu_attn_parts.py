@@ -234,3 +234,21 @@ def test_large_prompt_values(d, H, nq):
     out = torch.zeros((nq, H, d), dtype=torch.bfloat16, device="cuda")
     lib.kv_latent_prompt_attention(q, k, kr, v, _i32([0, nq]), out, cu_k=_i32([0, n]), scale=1.0)
     assert bool((out == value).all())
+
+
+@pytest.mark.parametrize("d,most,Hq,Hkv", [(64, 1, 4, 1), (128, 3, 4, 1), (64, 20, 2, 1), (128, 70, 4, 2)])
+def test_large_values_that_weigh_nothing(d, most, Hq, Hkv):
+    """Values of 2^100 that score 2^-300 below the others: not even a small part of them is seen beside values of 2^-30."""
+    n = 4000
+    table, live, cu = _ones([n], [most], 16)
+    pos = torch.arange(n, device="cuda")
+    for low in (range(64), range(2000, n - 100), [t for t in range(n - 100) if t // 32 % 4 == 0]):
+        kp = torch.zeros((live.shape[0], Hkv, 16, d), dtype=torch.bfloat16, device="cuda")
+        vp = torch.full_like(kp, 2.0 ** -30)
+        t = pos[list(low)]
+        kp[t // 16, :, t % 16, 5], vp[t // 16, :, t % 16] = -26.0, 2.0 ** 100
+        q = torch.zeros((most, Hq, d), dtype=torch.bfloat16, device="cuda")
+        q[..., 5] = 8.0
+        out = torch.zeros_like(q)
+        lib.kv_tree_attention(q, kp, vp, table, _i32([n]), cu, out, scale=1.0)
+        assert bool((out == 2.0 ** -30).all())
