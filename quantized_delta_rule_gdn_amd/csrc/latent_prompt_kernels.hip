@@ -308,15 +308,18 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void latent_prompt_kernel(con
   }
 }
 
-// Row tiles there may be, whatever the lists hold. 128 rows where that gives a workgroup to every CU, else 64 (203
-// tokens of 4 prompts, 8 heads of d = 64, take 7.4 us with 128 and 5.5 with 64; 12,288 of 8, 16 heads of d = 128, 210
-// and 270).
+// Row tiles there may be, whatever the lists hold. 128 rows where that takes every place for a workgroup on the chip
+// (2 a CU with d = 128, 3 with d = 64), else 64. With 128 and 64 rows (us): d = 128, one prompt of 4,096 tokens
+// and 8 heads (264 workgroups of 128 rows) 95 and 74, 12 heads (396) 103 and 85, 16 (528) 110 and 115, 24 (792) 136 and 159; 4 of
+// 1,024 with 14 heads (504) 39.4 and 39.6, with 32 (1,152) 66 and 73; d = 64, 2 of 2,048 with 16 heads (544) 40 and 35, with 20 (680)
+// 43.0 and 42.6, with 32 (1,088) 59 and 62. Lengths that fill 128 rows better than 64, or worse, move the border: 16 of
+// 300 tokens and 8 heads (424) 17.7 and 19.6, 40 of 150 with 16 (1,376) 21.4 and 19.4.
 int64_t prompt_items(int64_t B, int64_t Tq, int rows) { return std::min(Tq, Tq / rows + B); }
 
 template <int D>
 hipError_t prompt_d(const LatentPromptArgs& a, hipStream_t s) {
   const int64_t wide = prompt_items(a.B, a.Tq, 128);
-  if (wide * a.H >= 256) {
+  if (wide * a.H >= (D == 64 ? 768 : 512)) {
     hipLaunchKernelGGL((latent_prompt_kernel<D, 2>), dim3(static_cast<unsigned>(wide * a.H)), dim3(256), 0, s, a);
   } else {
     const int64_t n = prompt_items(a.B, a.Tq, 64);
