@@ -99,9 +99,12 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(const CopyArgs a, unsigned
 // as its threads hold in registers. A token never moves up (its place in the list is at most its
 // number), so a batch's stores cannot reach a later batch's tokens: the next batch is loaded before
 // this one is stored, its pages looked up a batch ahead, and the list read one more ahead. Within a
-// batch every load has returned before the first store. Bound by the stream for long lists (32 requests
-// of up to 8,192 tokens halved, 553 MB moved in 133 us, 4.2 TB/s: rows of 256 bytes from here and there; splitting
-// rows over workgroups did not help, stores past the caches took 144 instead of 150 us), by latency for short ones (6 us).
+// batch every load has returned before the first store. Long lists are bound by
+// the stream of rows of 256 bytes from here and there, and by the longest of them: a workgroup's batches follow each other,
+// and all 512 workgroups of 32 requests of up to 8,192 tokens halved (the longest has 32 batches, the mean is 16.5)
+// start at once, so that in the end few are at work. That takes 134 us for 553 MB, as many bytes in 32 even lists 118, 4.7
+// TB/s. Splitting rows over workgroups did not help; stores past the caches take 135 and 119, and where the same arrays are
+// moved again and again 125 instead of 118. Short lists are bound by latency (6 us).
 constexpr int kKeepUnroll = 8;
 
 __global__ __launch_bounds__(256) void kv_compact_kernel(const CompactArgs a, int arrays) {
@@ -169,7 +172,7 @@ __global__ __launch_bounds__(256) void kv_compact_kernel(const CompactArgs a, in
     for (int u = 0; u < U; ++u) {
       if (moves(j0, now, u)) {
         const uint32_t to = ((static_cast<uint32_t>(now.pt[u]) * a.Hkv + h) << a.page_log2) + ((base + j0 + u * rows + row) & in_page);
-        __builtin_nontemporal_store(w[u], pages + int64_t(to) * per_row + piece);
+        pages[int64_t(to) * per_row + piece] = w[u];
       }
       w[u] = ahead[u];
     }
