@@ -30,7 +30,7 @@ __global__ __launch_bounds__(256) void latent_append_kernel(const LatentAppendAr
 // workgroup holds in LDS serves both products of all its rows.
 constexpr int kLatTile = 64;
 
-// Up to 16 rows: the stream of the cache is what takes longest (64 requests, 266,000 tokens, 16 heads: 68 us and 6
+// Up to 16 rows: the stream of the cache is what takes longest (64 requests, 266,000 tokens, 16 heads: 63 to 68 us and 6
 // for the join; 5.2 TB/s behind the first 8 us, in which lengths, pages and the first tiles are on their way;
 // the eight waves below take the same, and 17 instead of 16 us for one request of 700 tokens). The 4 waves
 // share out the scores by tokens, meet for the maximum of each row, hand the weights over through LDS, and
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(256, 2) void latent_kernel(const TreeArgs a, const 
 // one barrier a tile. The rows' references (what their weights are relative to) stay as they are until a
 // score passes one by 2^kSlack, as it does in a run's first tile: then, two more barriers are met, in which
 // the scoring waves agree on new ones.
-// 24 requests of up to 4,096 tokens with up to 4 drafted and 128 heads: 66 us and 8 for the join (85 with tiles
+// 24 requests of up to 4,096 tokens with up to 4 drafted and 128 heads: 66 to 69 us and 9 for the join (85 with tiles
 // carried through registers, stored to LDS between two barriers), 520 TFLOP/s. A tile of 32 tokens takes some 2,400
 // cycles: 1,088 of products on each SIMD, 850 for its loads to go out (36 KB through a path of 64 bytes a cycle),
 // the rest exponentials, looking what is rare and the barrier; the loads among the products slowed both (72 us),

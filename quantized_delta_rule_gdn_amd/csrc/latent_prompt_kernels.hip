@@ -14,8 +14,8 @@ namespace {
 // maximum takes two exchanges, and the scores' C tiles are the B operand of out^T = V^T P^T as they
 // stand (lane group g holds keys 4 g .. + 3 of both halves of 32; V^T is read transposed from LDS in the
 // same order). Bound by the products and by the exponentials between them: 8 prompts, 12,288 tokens, 16 heads of
-// d = 128, 210 us or 900 TFLOP/s (1,358 for a large product alone; the clock falls under this load, and medians of
-// 215 to 240 us are seen too).
+// d = 128, 200 to 210 us or 900 TFLOP/s (1,358 for a large product alone; matrix cores are busy 48% of the SIMDs' cycles; the
+// clock falls under this load, and medians of 215 to 240 us are seen too).
 constexpr int kKeyTile = 64;
 
 struct Request {

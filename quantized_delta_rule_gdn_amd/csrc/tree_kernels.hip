@@ -13,9 +13,9 @@ namespace {
 // token, a request's tokens are cut into items, each of the 4 waves of a workgroup takes every fourth
 // tile of 32 tokens straight from the pages into registers as operands, and the waves meet in LDS
 // at the end. The rows of a product are the (drafted token, query head) pairs of one key-value head,
-// 16 a workgroup. Bound by the stream of the cache: 64 requests of 8,000 tokens, 8 heads of d = 128, 353 us
-// or 5.9 TB/s (reading alone reaches 7.1); short ones by latency (one request of 500 tokens 10 us, call
-// included). The weights' second piece costs nothing there.
+// 16 a workgroup. Bound by the stream of the cache: 64 requests of 8,000 tokens, 8 heads of d = 128, 354 us with 4
+// rows a head and with 16, or 5.9 TB/s (reading alone reaches 7.1; waves wait 64% of their time, matrix cores are busy 6%); short
+// ones by latency (one request of 500 tokens 10 us, call included). The weights' second piece costs nothing there.
 template <int D, bool P16>
 __global__ __launch_bounds__(256, 3) void kv_tree_kernel(const TreeArgs a, const TokenPlan plan) {
   constexpr int KS = D / 32;       // k steps of the score product
@@ -254,9 +254,9 @@ __global__ __launch_bounds__(256, 3) void kv_tree_kernel(const TreeArgs a, const
 // the next one among this one's products, with one barrier a tile (read by every wave for itself, 64 rows
 // would draw 64 KB a tile from the L1, as long as their products take). The weights are rounded once: a
 // second piece took 15 to 20% more time (48 requests 127 -> 142 us, 4 long ones 166 -> 203, before the tiles were
-// loaded ahead). 48 requests of up to 4,096 tokens, 128 rows, 8 heads of d = 128: 97 us and 8 for the join,
-// which is 4.4 TB/s; the matrix cores are busy for a fifth of the time, the waves wait for the stream (a third
-// tile on its way did not help: 119 us with it, 114 without). 4 requests of up to 65,536 tokens, 512 rows
+// loaded ahead). 48 requests of up to 4,096 tokens, 128 rows, 8 heads of d = 128: 97 to 104 us and 9 for the
+// join, which is 4.1 to 4.4 TB/s; the matrix cores are busy for a fifth of the time, the waves wait for the stream, of which
+// the longest run has 43 tiles and the mean 25 (a third tile on its way did not help: 119 us with it, 114 without). 4 requests of up to 65,536 tokens, 512 rows
 // of d = 64: 85 us and 8, 660 TFLOP/s; matrix cores busy 37%, vector unit 55%: for 16 x 16 scores the products take
 // 72 cycles, the exponentials alone 64 and the rest of the softmax 40.
 constexpr int kWideTile = 64;
