@@ -30,11 +30,9 @@ struct TokenPlan {
   int whole;      // no request is cut
 };
 
-// Runs that units are cut into, at most. Few are up to as many as the workgroups that the chip holds. Of requests of 90 to
-// 4,000 tokens, 352 units on 512 take 101 us as few and 121 as many, 448 128 and 139, 480 138 and 147; of latents 176
-// units on 256 take 87 and 115, 224 119 and 129, 240 126 and 135; 512 units of 4 rows on 512 111.5 and 109.7. Where
-// lengths are even the two are alike.
-__host__ __device__ inline bool few_units(int64_t units, int slots) { return units <= slots; }
+// Runs that units are cut into, at most. Few are up to three quarters of the workgroups that the chip holds (with half
+// instead, 384 units of 200 to 4,096 tokens on 512 took 122 us instead of 115, 138 of latents on 256 92 instead of 75).
+__host__ __device__ inline bool few_units(int64_t units, int slots) { return 4 * units <= 3 * int64_t(slots); }
 __host__ __device__ inline int64_t runs_of(int64_t units, int slots) { return few_units(units, slots) ? slots : units + slots / 2; }
 
 // Neighbouring parts that a die takes at a time.
