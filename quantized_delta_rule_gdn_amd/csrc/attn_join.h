@@ -30,8 +30,12 @@ struct TokenPlan {
   int whole;      // no request is cut
 };
 
-// Runs that units are cut into, at most. Few are up to three quarters of the workgroups that the chip holds (with half
-// instead, 384 units of 200 to 4,096 tokens on 512 took 122 us instead of 115, 138 of latents on 256 92 instead of 75).
+// Runs that units are cut into, at most. Few are up to three quarters of the workgroups that the chip holds: so much room
+// is left to cut the longest. 32 drafted tokens, 8 heads of d = 128, 512 workgroups at once, as few and as many (us): requests of 1/B
+// to all of 4,000 tokens, 272 units 75 and 98, 320 96 and 117, 384 117 and 131, 448 128 and 139, 480 138 and 147; one of 60,000 tokens
+// among others of 1,200, 272 units 84 and 102, 320 92 and 101, 352 97 and 99, 384 170 and 100, 448 239 and 110, 512 1,260 and 121.
+// Latents of 128 heads, 256 at once: 224 units of even steps 119 and 129; one long one among 160 99 and 112, 176 108 and 110, 192 211
+// and 114.
 __host__ __device__ inline bool few_units(int64_t units, int slots) { return 4 * units <= 3 * int64_t(slots); }
 __host__ __device__ inline int64_t runs_of(int64_t units, int slots) { return few_units(units, slots) ? slots : units + slots / 2; }
 
