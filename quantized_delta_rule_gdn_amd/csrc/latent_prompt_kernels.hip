@@ -308,18 +308,19 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void latent_prompt_kernel(con
   }
 }
 
-// Row tiles there may be, whatever the lists hold. 128 rows where that takes every place for a workgroup on the chip
-// (2 a CU with d = 128, 3 with d = 64), else 64. With 128 and 64 rows (us): d = 128, one prompt of 4,096 tokens
-// and 8 heads (264 workgroups of 128 rows) 95 and 74, 12 heads (396) 103 and 85, 16 (528) 110 and 115, 24 (792) 136 and 159; 4 of
-// 1,024 with 14 heads (504) 39.4 and 39.6, with 32 (1,152) 66 and 73; d = 64, 2 of 2,048 with 16 heads (544) 40 and 35, with 20 (680)
-// 43.0 and 42.6, with 32 (1,088) 59 and 62. Lengths that fill 128 rows better than 64, or worse, move the border: 16 of
-// 300 tokens and 8 heads (424) 17.7 and 19.6, 40 of 150 with 16 (1,376) 21.4 and 19.4.
+// Row tiles there may be, whatever the lists hold. 64 rows while full tiles of 64 are no more than the workgroups that the chip
+// holds at once (2 a CU with d = 128, 3 with d = 64), else 128. With 64 and 128 rows (us; in parentheses the tiles of 64): d =
+// 128, one prompt of 4,096 tokens and 8 heads (512) 74 and 95, 8 of 300 and 10 (375) 12.0 and 14.8, 16 of 100 behind 4,000 and 16
+// (400) 126 and 137; 8 of 300 and 14 (525) 16.6 and 16.7, 16 of 300 and 8 (600) 19.6 and 17.7, 2 of 1,000 behind 4,000 and
+// 24 (750) 174 and 157, 4 of 512 behind 8,000 and 24 (768) 404 and 287, 8 of 1,536 and 16 270 and 210; d = 64, 2 of 2,048 and 8
+// (512) 27 and 36, 16 of 100 behind 4,000 and 24 (600) 120 and 111, one of 8,192 and 16 (2,048) 212 and 190. Where a prompt's tiles
+// differ much in how many keys they see, more rounds of the shorter ones do as well: one of 4,096 and 12 (768) 85 and 103.
 int64_t prompt_items(int64_t B, int64_t Tq, int rows) { return std::min(Tq, Tq / rows + B); }
 
 template <int D>
 hipError_t prompt_d(const LatentPromptArgs& a, hipStream_t s) {
-  const int64_t wide = prompt_items(a.B, a.Tq, 128);
-  if (wide * a.H >= (D == 64 ? 768 : 512)) {
+  if (int64_t(a.Tq) * a.H > 64 * (D == 64 ? 768 : 512)) {
+    const int64_t wide = prompt_items(a.B, a.Tq, 128);
     hipLaunchKernelGGL((latent_prompt_kernel<D, 2>), dim3(static_cast<unsigned>(wide * a.H)), dim3(256), 0, s, a);
   } else {
     const int64_t n = prompt_items(a.B, a.Tq, 64);

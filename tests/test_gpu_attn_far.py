@@ -138,17 +138,28 @@ def test_every_latent_of_many_requests_counts_once(what, most, H):
     _latent(lens, [most - b % 3 * (most // 3) for b in range(len(lens))], H, 256, 16, 1 if what == "one of many" else 64)
 
 
+def _prompts(nq, lens, H, d, by):
+    v = torch.cat([_hot(torch.arange(n, device="cuda"), by, d) for n in lens])[:, None].expand(-1, H, -1).contiguous()
+    q = torch.randn((sum(nq) + 2, H, d + d // 2), device="cuda").bfloat16()
+    out = torch.full((sum(nq) + 2, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    cu_q, cu_k = ([sum(x[:b]) for b in range(len(x) + 1)] for x in (nq, lens))
+    lib.kv_latent_prompt_attention(q, torch.zeros_like(v), torch.zeros((sum(lens), d // 2), dtype=torch.bfloat16, device="cuda"), v, _i32(cu_q), out, cu_k=_i32(cu_k))
+    _holds(out, lens, nq, by, d)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("H", [1, 40])
 @pytest.mark.parametrize("by", [1, 64])
 def test_every_key_of_a_prompt_counts_once(d, H, by):
     """In row tiles of 64 queries, and of 128 where there are many; behind cached tokens and not."""
+    nq = [1, 63, 64, 65, 127, 128, 129, 200, 700]
     for before in (0, 1, 100, 1000):
-        nq = [1, 63, 64, 65, 127, 128, 129, 200, 700]
-        lens = [n + before * (b % 2) for b, n in enumerate(nq)]
-        v = torch.cat([_hot(torch.arange(n, device="cuda"), by, d) for n in lens])[:, None].expand(-1, H, -1).contiguous()
-        q = torch.randn((sum(nq) + 2, H, d + d // 2), device="cuda").bfloat16()
-        out = torch.full((sum(nq) + 2, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
-        cu_q, cu_k = ([sum(x[:b]) for b in range(len(x) + 1)] for x in (nq, lens))
-        lib.kv_latent_prompt_attention(q, torch.zeros_like(v), torch.zeros((sum(lens), d // 2), dtype=torch.bfloat16, device="cuda"), v, _i32(cu_q), out, cu_k=_i32(cu_k))
-        _holds(out, lens, nq, by, d)
+        _prompts(nq, [n + before * (b % 2) for b, n in enumerate(nq)], H, d, by)
+
+
+@pytest.mark.parametrize("d,most", [(64, 768), (128, 512)])
+def test_prompts_on_both_sides_of_the_wider_tiles(d, most):
+    """As many full tiles of 64 rows as are taken so, and a few queries more."""
+    for extra in (-2, -1, 0, 1):                      # (two rows are behind the last request)
+        n = 64 * most // 16 + extra
+        _prompts([n - 200, 200], [n - 200, 300], 16, d, 1)
