@@ -252,3 +252,25 @@ def test_large_values_that_weigh_nothing(d, most, Hq, Hkv):
         out = torch.zeros_like(q)
         lib.kv_tree_attention(q, kp, vp, table, _i32([n]), cu, out, scale=1.0)
         assert bool((out == 2.0 ** -30).all())
+
+
+def test_the_default_bound_of_new_tokens():
+    """Without max_new a call takes any batch that it takes with one: 512 requests, 16 drafted each, of which any may have all."""
+    lens, new = [60] * 511 + [5000], [16] * 512
+    table, live, cu = _ones(lens, new, 16)
+    T, ln = sum(new), _i32(lens)
+    kp = torch.randn((live.shape[0], 2, 16, 64), device="cuda").bfloat16()
+    vp = torch.where(live[:, None, :, None], 1.0, float("nan")).bfloat16().expand(-1, 2, -1, 64).contiguous()
+    q = torch.randn((T, 8, 64), device="cuda").bfloat16()
+    out = torch.empty_like(q)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    lib.kv_tree_attention(q, kp, vp, table, ln, cu, out)
+    assert bool((out == 1.0).all())
+    pages = torch.randn((live.shape[0], 16, 288), device="cuda").bfloat16()
+    pages[..., :256] = torch.where(live[..., None], 1.0, float("nan")).bfloat16()
+    q, out = torch.randn((T, 8, 288), device="cuda").bfloat16(), torch.zeros((T, 8, 256), dtype=torch.bfloat16, device="cuda")
+    lib.kv_latent_attention(q, pages, table, ln, out, 0.05, cu_new=cu)
+    assert bool((out == 1.0).all())
+    assert torch.cuda.max_memory_allocated() - before < 2 ** 30
