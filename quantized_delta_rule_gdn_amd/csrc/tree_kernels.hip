@@ -288,7 +288,7 @@ __global__ __launch_bounds__(256, D == 64 ? 3 : 2) void kv_tree_wide_kernel(cons
   const int live_rows = static_cast<int>(min(rows - row0, int64_t(64 * R)));
   const bool idle = wv * 16 * R >= live_rows;           // none of the rows is this wave's
   // (a negative scale goes into the queries' signs; one of 0 becomes the least one, as 0 times -infinity is NaN)
-  const float scale = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
+  const float scale = fabsf(a.scale_log2) < 0x1p-126f ? 0x1p-126f : fabsf(a.scale_log2);     // (NaN stays NaN)
   const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0;
   const float slack = fminf(kSlack / scale, 0x1p100f);
 

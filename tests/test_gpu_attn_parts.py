@@ -274,3 +274,20 @@ def test_the_default_bound_of_new_tokens():
     lib.kv_latent_attention(q, pages, table, ln, out, 0.05, cu_new=cu)
     assert bool((out == 1.0).all())
     assert torch.cuda.max_memory_allocated() - before < 2 ** 30
+
+
+def test_a_scale_of_nan_is_seen():
+    nan = float("nan")
+    for most, Hq in ((1, 4), (20, 4), (70, 8)):
+        table, live, cu = _ones([100], [most], 16)
+        kp, vp = (torch.randn((live.shape[0], 1, 16, 64), device="cuda").bfloat16() for _ in range(2))
+        q = torch.randn((most, Hq, 64), device="cuda").bfloat16()
+        out = torch.zeros_like(q)
+        lib.kv_tree_attention(q, kp, vp, table, _i32([100]), cu, out, scale=nan)
+        assert bool(torch.isnan(out).all()), f"{most} tokens"
+        pages, q, out = (torch.randn(s, device="cuda").bfloat16() for s in ((live.shape[0], 16, 288), (most, Hq, 288), (most, Hq, 256)))
+        lib.kv_latent_attention(q, pages, table, _i32([100]), out, nan, cu_new=cu)
+        assert bool(torch.isnan(out).all()), f"latents, {most} tokens"
+    q, k, kr, out = (torch.randn(s, device="cuda").bfloat16() for s in ((90, 2, 96), (90, 2, 64), (90, 32), (90, 2, 64)))
+    lib.kv_latent_prompt_attention(q, k, kr, k, _i32([0, 90]), out, scale=nan)
+    assert bool(torch.isnan(out).all())
