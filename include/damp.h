@@ -633,7 +633,7 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages,
  *   copy_src, copy_dst, copy_rows dev int32 [n] (output): the partly filled page, its replacement, its
  *               filled rows, for kv_copy_pages (once per layer); -1, -1, 0 where nothing is to be copied
  *   used        dev int32 [1] (output): pages needed; beyond num_free of them the entries are -1
- * At most 8,000 forks (else UNSUPPORTED). Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP. */
+ * An array that is written overlaps none of the others. At most 8,000 forks (else UNSUPPORTED). Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP. */
 damp_status kv_fork_tables(const int32_t* src, const int32_t* dst, int32_t n, int32_t* seq_lens, int32_t B,
                            const int32_t* free_pages, int32_t num_free, int32_t* block_table,
                            int32_t max_blocks, int32_t* shares, int32_t num_pages, int32_t page_size,

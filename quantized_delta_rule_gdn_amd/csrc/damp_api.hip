@@ -513,7 +513,7 @@ constexpr double kLog2E = 1.4426950408889634;
 // Two int32 arrays share memory.
 bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + static_cast<uintptr_t>(nq) * 4 && b < a + static_cast<uintptr_t>(np) * 4;
+  return p && q && np > 0 && nq > 0 && a < b + static_cast<uintptr_t>(nq) * 4 && b < a + static_cast<uintptr_t>(np) * 4;
 }
 
 // Pages of any row that is whole 16-byte pieces, for the calls that only move rows.
@@ -1384,6 +1384,13 @@ damp_status kv_fork_tables(const int32_t* src, const int32_t* dst, int32_t n, in
   if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(seq_lens, 4) || !aligned(free_pages, 4) || !aligned(block_table, 4) || !aligned(shares, 4) ||
       !aligned(copy_src, 4) || !aligned(copy_dst, 4) || !aligned(copy_rows, 4) || !aligned(used, 4))
     return fail(DAMP_ERR_INVALID_ARGUMENT, "misaligned pointer (need natural alignment)");
+  // (each fork counts the pages that the ones before it need: what they read must stay as it is meanwhile)
+  const struct { const int32_t* p; int64_t n; } arrays[] = {{copy_src, n}, {copy_dst, n}, {copy_rows, n}, {used, 1}, {seq_lens, B},
+                                                            {block_table, int64_t(B) * max_blocks}, {shares, num_pages}, {src, n}, {dst, n}, {free_pages, num_free}};
+  for (int i = 0; n > 0 && i < 7; ++i)
+    for (int j = i + 1; j < 10; ++j)
+      if (overlap(arrays[i].p, arrays[i].n, arrays[j].p, arrays[j].n))
+        return fail(DAMP_ERR_INVALID_ARGUMENT, "an array that is written (seq_lens, block_table, shares, copy_src, copy_dst, copy_rows, used) overlaps another one");
   damp::ForkArgs a{};
   a.src = src;
   a.dst = dst;

@@ -49,3 +49,24 @@ def test_one_tile_a_request_up_to_the_documented_size():
     """Where tiles have 64 rows the limit is met on both sides."""
     assert _takes("kv_tree_attention", 512, 32766, 64, 1, 4096) and not _takes("kv_tree_attention", 512, 32768, 64, 1, 4096)
     assert _takes("kv_latent_attention", 512, 1, 64, 16382, 4096) and not _takes("kv_latent_attention", 512, 1, 64, 16384, 4096)
+
+
+FORK = ("src", "dst", "lens", "free", "table", "shares", "cs", "cd", "cr", "used")
+
+
+def _forked(**where):
+    at = {name: X + 4096 * i for i, name in enumerate(FORK)}
+    at.update(where)
+    return lib.load().kv_fork_tables(at["src"], at["dst"], 3, at["lens"], 2, at["free"], 5, at["table"], 4, at["shares"], 9, 16, at["cs"], at["cd"], at["cr"], at["used"], None)
+
+
+@pytest.mark.parametrize("written", ["lens", "table", "shares", "cs", "cd", "cr", "used"])
+def test_a_fork_s_outputs_overlap_nothing(written):
+    """Workgroups read the lists while others write: an array over another one is refused, also where it only reaches into it."""
+    count = dict(src=3, dst=3, lens=2, free=5, table=8, shares=9, cs=3, cd=3, cr=3, used=1)
+    for i, other in enumerate(FORK):
+        if other == written:
+            continue
+        base = X + 4096 * i
+        for at in (base, base + 4 * (count[other] - 1), base - 4 * (count[written] - 1)):
+            assert _forked(**{written: at}) == lib.DAMP_ERR_INVALID_ARGUMENT and "overlaps" in lib.last_error(), (other, at - base)

@@ -291,3 +291,14 @@ def test_a_scale_of_nan_is_seen():
     q, k, kr, out = (torch.randn(s, device="cuda").bfloat16() for s in ((90, 2, 96), (90, 2, 64), (90, 32), (90, 2, 64)))
     lib.kv_latent_prompt_attention(q, k, kr, k, _i32([0, 90]), out, scale=nan)
     assert bool(torch.isnan(out).all())
+
+
+def test_forks_beside_empty_arrays():
+    """A free list of no pages and a table of no blocks share no memory with anything, wherever they point."""
+    lens, shares = _i32([5, 0]), _i32([0] * 9)
+    copies = [_i32([7]) for _ in range(3)]
+    used = _i32([7])
+    lib.kv_fork_tables(_i32([0]), _i32([1]), lens, shares[4:4], torch.zeros((2, 0), dtype=torch.int32, device="cuda"), shares, 16, *copies, used)
+    assert lens.tolist() == [5, 5] and shares.tolist() == [0] * 9 and [c.item() for c in copies] == [-1, -1, 0] and used.item() == 0
+    with pytest.raises(lib.DampError, match="overlaps"):
+        lib.kv_fork_tables(_i32([0]), _i32([1]), lens, shares[4:5], torch.zeros((2, 1), dtype=torch.int32, device="cuda"), shares, 16, *copies, used)
