@@ -668,7 +668,7 @@ size_t kv_free_pages_workspace_bytes(int32_t num_pages);
 
 /* Gives back pages: of each request those behind its first keep_lens[b] tokens (dev int32 [B], NULL: all),
  * up to the last that seq_lens[b] tokens fill. A page with shares left loses one; the others are listed.
- *   shares    dev int32 [num_pages]: updated (calls on it that overlap race)
+ *   shares    dev int32 [num_pages]: updated (calls on it that overlap race); none of the other arrays
  *   freed     dev int32 [num_pages] (output): ids of the pages that no request holds any more, ascending;
  *             entries behind the last are left as they were
  *   num_freed dev int32 [1] (output)

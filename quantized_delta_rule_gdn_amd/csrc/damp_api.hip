@@ -1489,6 +1489,8 @@ damp_status kv_free_pages(const int32_t* keep_lens, const int32_t* seq_lens, int
   if (B > kMaxGroups) return fail(DAMP_ERR_INVALID_ARGUMENT, "B = %d exceeds the grid limit", B);
   st = check_workspace(workspace, workspace_bytes, damp::kv_free_ws_bytes(num_pages));
   if (st != DAMP_OK) return st;
+  if (overlap(shares, num_pages, seq_lens, B) || overlap(shares, num_pages, keep_lens, B) || overlap(shares, num_pages, block_table, int64_t(B) * max_blocks))
+    return fail(DAMP_ERR_INVALID_ARGUMENT, "shares overlaps seq_lens, keep_lens or block_table, which are read while it is updated");
   damp::FreeArgs a{};
   a.keep_lens = keep_lens;
   a.seq_lens = seq_lens;

@@ -70,3 +70,11 @@ def test_a_fork_s_outputs_overlap_nothing(written):
         base = X + 4096 * i
         for at in (base, base + 4 * (count[other] - 1), base - 4 * (count[written] - 1)):
             assert _forked(**{written: at}) == lib.DAMP_ERR_INVALID_ARGUMENT and "overlaps" in lib.last_error(), (other, at - base)
+
+
+@pytest.mark.parametrize("other,count", [("lens", 2), ("keep", 2), ("table", 8)])
+def test_shares_overlap_nothing_that_is_read_beside_them(other, count):
+    for offset in (0, 4 * (count - 1), -4 * 8):
+        at = dict(keep=X, lens=X + 4096, table=X + 8192)
+        status = lib.load().kv_free_pages(at["keep"], at["lens"], 2, at["table"], 4, at[other] + offset, 9, 16, X + 2 ** 20, X + 2 ** 21, None, 0, None)
+        assert status == lib.DAMP_ERR_INVALID_ARGUMENT and "shares overlaps" in lib.last_error()
