@@ -633,7 +633,8 @@ damp_status kv_decode_attention(const void* q, void* k_pages, void* v_pages,
  *   copy_src, copy_dst, copy_rows dev int32 [n] (output): the partly filled page, its replacement, its
  *               filled rows, for kv_copy_pages (once per layer); -1, -1, 0 where nothing is to be copied
  *   used        dev int32 [1] (output): pages needed; beyond num_free of them the entries are -1
- * An array that is written overlaps none of the others. At most 8,000 forks (else UNSUPPORTED). Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP. */
+ * An array that is written overlaps none of the others. At most 8,000 forks (else UNSUPPORTED).
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, HIP. */
 damp_status kv_fork_tables(const int32_t* src, const int32_t* dst, int32_t n, int32_t* seq_lens, int32_t B,
                            const int32_t* free_pages, int32_t num_free, int32_t* block_table,
                            int32_t max_blocks, int32_t* shares, int32_t num_pages, int32_t page_size,
@@ -707,8 +708,9 @@ size_t kv_tree_attention_workspace_bytes(int32_t B, int32_t num_q_heads, int32_t
  * where max_new * num_q_heads / num_kv_heads is at most 16, and else rounded to bf16 (2^-8 of each),
  * over the sum of the rounded ones; they are relative to a score that the row's highest may pass by a factor
  * of up to 2^8 and are divided by their sum in the end, so over n tokens values of 2^120 / n and more may end
- * infinite. Readouts do not depend on the other requests of a call;
- * they may differ in their last bit with max_new, max_len and how the requests' lengths share out the work.
+ * infinite. Readouts do not depend on the other requests' data;
+ * they may differ in their last bit with max_len and how the requests' lengths share out the work, and where
+ * values cancel in several last bits as max_new decides between the two forms of the weights.
  * A NaN or infinity of a new token's value reaches only the tokens that see it. max_new * num_q_heads
  * stays at most 2^30 - 1, and B * num_kv_heads times the tiles of 64 query rows of a request's max_new tokens
  * at most 2^24 - 2^10. Errors: INVALID_ARGUMENT, UNSUPPORTED (d, page_size), HIP. */
@@ -758,9 +760,9 @@ damp_status kv_latent_attention(const void* q, const void* pages, const int32_t*
  *   out         dev bf16 [Tq][num_heads][d]; a query that sees no key gives 0
  *   cu_q, cu_k  dev int32 [B + 1], ascending, kept inside [0, Tq] and [0, Tk]. Rows of out behind the last
  *               request are not written.
- * All 16-byte aligned but cu_q and cu_k. d is 64 or 128, Tq and Tk at most 2^30. Scores, statistics and sums are binary32, the
- * weights rounded once, as in kv_tree_attention of many rows, with the same bound of the values. A NaN or infinity of a token reaches only queries that see
- * it. (Tq / 64 + B) * num_heads stays below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d), HIP. */
+ * All 16-byte aligned but cu_q and cu_k. d is 64 or 128, Tq and Tk at most 2^30. Scores, statistics and sums
+ * are binary32, the weights rounded once, as in kv_tree_attention of many rows, with the same bound of the
+ * values. A NaN or infinity of a token reaches only queries that see it. (Tq / 64 + B) * num_heads stays below 2^24. Errors: INVALID_ARGUMENT, UNSUPPORTED (d), HIP. */
 damp_status kv_latent_prompt_attention(const void* q, const void* k, int64_t k_token_stride,
                                        int64_t k_head_stride, const void* k_rope, const void* v,
                                        int64_t v_token_stride, int64_t v_head_stride, const int32_t* cu_q,

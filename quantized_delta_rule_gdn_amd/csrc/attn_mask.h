@@ -94,7 +94,8 @@ __device__ __forceinline__ float max_row_slots(float x) {
 __device__ __forceinline__ float add_part(float f, float x, float sum) { return fmaf(__builtin_isfinite(x) ? f : 1.0f, x, sum); }
 
 // A row's running maximum stays as it is until a score passes it by more than this factor 2^kSlack: weights of
-// up to 2^8 lose nothing in binary32 or bf16 (sums over n tokens overflow from values of 2^120 / n on), and most tiles then need neither the other lanes' maxima nor
+// up to 2^8 lose nothing in binary32 or bf16 (sums over n tokens overflow from values of 2^120 / n on), and most
+// tiles then need neither the other lanes' maxima nor
 // sums scaled down.
 constexpr float kSlack = 8.0f;
 

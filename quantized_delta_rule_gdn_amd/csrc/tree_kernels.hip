@@ -255,8 +255,9 @@ __global__ __launch_bounds__(256, 3) void kv_tree_kernel(const TreeArgs a, const
 // would draw 64 KB a tile from the L1, as long as their products take). The weights are rounded once: a
 // second piece took 15 to 20% more time (48 requests 127 -> 142 us, 4 long ones 166 -> 203, before the tiles were
 // loaded ahead). 48 requests of up to 4,096 tokens, 128 rows, 8 heads of d = 128: 97 to 104 us and 9 for the
-// join, which is 4.1 to 4.4 TB/s; the matrix cores are busy for a fifth of the time, the waves wait for the stream, of which
-// the longest run has 43 tiles and the mean 25 (a third tile on its way did not help: 119 us with it, 114 without). 4 requests of up to 65,536 tokens, 512 rows
+// join, which is 4.1 to 4.4 TB/s; the matrix cores are busy for a fifth of the time, the waves wait for the stream, of
+// which the longest run has 43 tiles and the mean 25 (a third tile on its way did not help: 119 us with it, 114
+// without). 4 requests of up to 65,536 tokens, 512 rows
 // of d = 64: 85 us and 8, 660 TFLOP/s; matrix cores busy 37%, vector unit 55%: for 16 x 16 scores the products take
 // 72 cycles, the exponentials alone 64 and the rest of the softmax 40.
 constexpr int kWideTile = 64;
