@@ -95,8 +95,7 @@ __device__ __forceinline__ float add_part(float f, float x, float sum) { return 
 
 // A row's running maximum stays as it is until a score passes it by more than this factor 2^kSlack: weights of
 // up to 2^8 lose nothing in binary32 or bf16 (sums over n tokens overflow from values of 2^120 / n on), and most
-// tiles then need neither the other lanes' maxima nor
-// sums scaled down.
+// tiles then need neither the other lanes' maxima nor sums scaled down.
 constexpr float kSlack = 8.0f;
 
 // x, in a branch that few tiles take: what goes by it is not worked out before the branch (for all tiles, to be
